@@ -22,6 +22,8 @@ import os
 
 import torch
 
+from . import layer
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsvgemm.so")
 
@@ -67,6 +69,7 @@ def _load():
     lib.svg_weight_sizes.restype = ctypes.c_int
     lib.svg_last_error.argtypes = []
     lib.svg_last_error.restype = ctypes.c_char_p
+    layer._bind(lib)
     return lib
 
 
@@ -530,3 +533,7 @@ class LinearPass:
         """Whether a run of this pass ever gave up a bounded wait (word 0 of
         its workspace; its outputs are then undefined)."""
         return bool(int(self.workspace[:4].view(torch.int32).cpu()[0]))
+
+
+# --------------------------------------- the steps around the linears (layer.py)
+from .layer import add_rmsnorm_quant_i8  # noqa: E402,F401

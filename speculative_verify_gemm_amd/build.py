@@ -21,7 +21,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsvgemm.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["rht_quant.hip", "linear_w4.hip", "linear_w8.hip", "tree_accept.hip", "tree_deltanet.hip",
-           "pass.hip", "layout.hip", "svgemm.hip"]
+           "pass.hip", "layout.hip", "svgemm.hip", "norm_quant.hip", "layer.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [
@@ -37,7 +37,7 @@ CFLAGS = [
 
 def source_digest() -> str:
     """Digest of everything that decides the built kernels: the sources, the
-    public header and the compile flags.  Profile summaries record it, so a
+    public headers and the compile flags.  Profile summaries record it, so a
     counter reading can be matched to the code it was taken on."""
     import hashlib
     h = hashlib.sha256()
@@ -46,8 +46,9 @@ def source_digest() -> str:
         h.update(name.encode())
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(f.read())
-    with open(os.path.join(ROOT, "include", "svgemm.h"), "rb") as f:
-        h.update(f.read())
+    for name in ("svgemm.h", "svgemm_layer.h"):
+        with open(os.path.join(ROOT, "include", name), "rb") as f:
+            h.update(f.read())
     h.update(" ".join(CFLAGS[:-4]).encode())  # flags, without the include paths
     return h.hexdigest()[:16]
 

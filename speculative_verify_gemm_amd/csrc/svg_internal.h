@@ -5,6 +5,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+// The per-thread error text behind svg_last_error() (svgemm.hip): each sets or
+// clears it and returns the status.
+int svg_fail(int code, const char* fn, const char* what);
+int svg_ok();
+int svg_hip_status(const char* fn, hipError_t e);
+
 // `block`: the transform block, 32 or 64 (checked by the caller).
 hipError_t svg_launch_act_rht_quant(const float* X, int M, int K, const int8_t* signs, int block, int8_t* xq,
                                     float* x_scale, hipStream_t stream);
@@ -53,6 +59,12 @@ const char* svg_pass_check(const svg_pass_step* steps, int nsteps, int M, int fm
                            uint64_t* plan_bytes, uint64_t* ws_bytes, int* code);
 void svg_pass_write(const svg_pass_step* steps, int nsteps, int M, int fmt, int group, int block, void* plan_host);
 hipError_t svg_launch_pass(const void* plan, int M, int fmt, int group, void* ws, hipStream_t stream);
+
+// Residual addition, norm, rotation and quantization (norm_quant.hip); types
+// as in svgemm_layer.h.
+hipError_t svg_launch_norm_quant(const void* x, int x_type, float* residual, const void* weight, int w_type,
+                                 double eps, int M, int K, const int8_t* signs, int block, float* y, int8_t* xq,
+                                 float* x_scale, hipStream_t stream);
 
 // Layout conversions (layout.hip): canonical row-major arrays <-> storage.
 hipError_t svg_launch_import_weights(int fmt_w8, int z4, int group, int N, int K, const void* codes,

@@ -61,6 +61,10 @@ bool fits_w8(int N, int K) {
 
 }  // namespace
 
+int svg_fail(int code, const char* fn, const char* what) { return fail(code, fn, what); }
+int svg_ok() { return ok(); }
+int svg_hip_status(const char* fn, hipError_t e) { return hip_status(fn, e); }
+
 int svg_cu_count() {
   static std::atomic<int> counts[64];  // per device; every calling thread finds the same value
   int dev = 0;
