@@ -54,6 +54,122 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
                                 double eps, int M, int K, const int8_t* signs, int block, float* y, int8_t* xq,
                                 float* x_scale, void* stream);
 
+/*
+ * svg_kv_cache -- a paged cache of keys and values and the slots that use it:
+ * a host struct that every call below reads during the call only.
+ *
+ *  k, v      the pages of all layers, 16-byte aligned: page p of layer l of
+ *            each starts at element (l * n_pages + p) * heads * page * dim.
+ *  type      SVG_F16 or SVG_BF16.
+ *  heads     key/value heads, 1 .. 1024.   dim   64, 128 or 256 values a head.
+ *  page      tokens of a page: 32, 64 or 128.
+ *  n_pages   1 .. 2^20.    n_layers  1 .. 65535.    n_slots  0 .. 1024 sequences.
+ *  width     entries of a table row; width * page < 2^31 - 2^20.
+ *  table     int32 [n_slots][width]: the pages of a slot in token order; token t
+ *            of slot s lies in page table[s][t / page], place t % page.
+ *  pages     int32 [n_slots]: entries of each row that are in use.
+ *  len       int32 [n_slots]: committed tokens of each slot.
+ *  refs      int32 [n_pages]: the number of slots that hold each page; a page is
+ *            free where it is 0.  A page that several slots hold is never written.
+ *  (table, pages, len, refs: 4-byte aligned.  Each call names the ones it needs.)
+ *
+ * A page holds head after head, page * dim values each, in the lane order of
+ * the matrix instructions that read them (v_mfma_f32_16x16x32), so that a wave
+ * reads 32 tokens of a head as contiguous KiB and needs no exchange:
+ *   keys    value (t, d) is element ((t / 16) * (dim / 32) + d / 32) * 512
+ *           + (16 * ((d % 32) / 8) + t % 16) * 8 + d % 8.
+ *   values  value (t, d) is element ((t / 32) * (dim / 16) + d / 16) * 512
+ *           + (16 * ((t % 16) / 4) + d % 16) * 8 + 4 * ((t % 32) / 16) + t % 4.
+ */
+typedef struct svg_kv_cache {
+    void* k;
+    void* v;
+    int type, heads, dim, page, n_pages, n_layers, n_slots, width;
+    int32_t* table;
+    int32_t* pages;
+    int32_t* len;
+    int32_t* refs;
+} svg_kv_cache;
+
+/*
+ * kv_append -- write the keys and values of new tokens behind the committed
+ * ones of each slot, in one layer.  len does not change (kv_commit does that).
+ *
+ *  k, v      fp32 [n_slots * T] rows of heads * dim values, rows ld_k / ld_v
+ *            values apart (a multiple of 4, >= heads * dim), 16-byte aligned: row
+ *            s * T + i is token i of slot s, written to position len[s] + i, rounded to nearest (even) once.
+ *  T         rows of each slot, >= 1.
+ *  n_rows    int32 [n_slots] or NULL: rows of each slot that are written (the
+ *            nearest of 0 .. T); NULL: all T.
+ *  A row whose position is not inside the slot's pages, or whose page number is not one of
+ *  the cache's, is not written.  The pages written have to be the slot's own (kv_reserve).
+ *  Reads table, pages, len.  Errors: SVG_EINVAL for a null required pointer, T < 1 or a layer
+ *  outside 0 .. n_layers - 1; SVG_EUNSUPPORTED for a cache outside the limits above, n_slots * T >= 2^31
+ *  or ld_k / ld_v; SVG_EALIGN.
+ */
+svg_status kv_append(const svg_kv_cache* cache, int layer, const float* k, int64_t ld_k, const float* v, int64_t ld_v, int T,
+                     const int32_t* n_rows, void* stream);
+
+/*
+ * kv_commit -- keep the accepted path of each slot's draft tree: its tokens move
+ * together behind the root, in every layer, and the slot's length grows.
+ *
+ *  T         nodes of each slot's tree, 1 .. SVG_TREE_MAX_NODES: node i of slot s was
+ *            appended at position len[s] + i.
+ *  path      int32 [n_slots][T], n_emit int32 [n_slots]: as tree_accept_greedy writes
+ *            them for each slot's tree (path rising node numbers below the root).
+ *  len_out   int32 [n_slots]: len[s] + n_emit[s] (the root and the accepted nodes are
+ *            committed); may be len itself.
+ *  The token of node path[s][j] moves to position len[s] + 1 + j, j < n_emit[s] - 1.  A slot with
+ *  n_emit outside 1 .. T, a path that is not rising inside 1 .. T - 1, or positions outside its pages keeps
+ *  its tokens, and len_out[s] = len[s].
+ *  Reads table, pages, len.  Errors as for kv_append.
+ */
+svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, const int32_t* n_emit, int32_t* len_out,
+                     void* stream);
+
+/*
+ * kv_fork -- give every slot the state of a slot: forking, keeping and freeing
+ * in one call, as if all at once.
+ *
+ *  src       int32 [n_slots]: slot s becomes a fork of slot src[s]: it holds the pages of src[s]'s
+ *            committed tokens (the last one may be partly filled) and has its length; its own
+ *            pages are given up.  src[s] == s keeps the slot as it is; -1 frees it (no pages, length
+ *            0); any other number outside 0 .. n_slots - 1 keeps it.
+ *  cache     read: table, pages, len.   refs is updated (one count for each slot that holds a page).
+ *  table_out, pages_out, len_out   the new tables, of the sizes of table, pages and len, and not
+ *            these themselves.  Entries of table_out behind a row's pages_out are left as they were.
+ *  No page is copied: kv_reserve does that for those that a fork writes to.
+ *  Errors as for kv_append, and SVG_EINVAL where an output is its input.
+ */
+svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table_out, int32_t* pages_out,
+                   int32_t* len_out, void* stream);
+
+/*
+ * kv_reserve -- make room: after it, the tokens len[s] .. len[s] + need[s] - 1 of each slot
+ * lie in pages that no other slot holds.
+ *
+ *  need      int32 [n_slots]; a slot with need < 1 is left as it is.
+ *  status    OUTPUT int32 [n_slots]: 0 done; 1 not enough free pages; 2 more than a table row holds, or
+ *            a slot whose pages, length or last page number is not valid.  A slot with 1 or 2 is left as it was.
+ *  workspace SVG_KV_WORKSPACE_BYTES(n_slots) bytes, 8-byte aligned; its contents need not be kept.  Calls that
+ *            may overlap need different ones (and may not share refs).
+ *  The slots are served in order.  Where the page of token len - 1 is partly filled and other slots hold it too
+ *  (refs > 1 when the slot's turn comes), a free page takes its place and its contents in every layer; then
+ *  pages are added behind.  Each page taken is the free one with the lowest number.
+ *  Updates table, pages, refs.  Errors as for kv_append.
+ */
+#define SVG_KV_WORKSPACE_BYTES(n_slots) (8 * (uint64_t)(n_slots) + 16)
+svg_status kv_reserve(const svg_kv_cache* cache, const int32_t* need, int32_t* status, void* workspace, void* stream);
+
+/*
+ * kv_copy_pages -- copy page src[i] to page dst[i], i < n, in every layer (to compact a
+ * pool, or to keep a copy).  The pages of dst are different ones, and none of them is in src.  A
+ * pair with a number outside 0 .. n_pages - 1 is passed over.  Reads no table.
+ *  Errors as for kv_append, and SVG_EINVAL for n < 0 (n == 0: nothing enqueued).
+ */
+svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -536,4 +536,5 @@ class LinearPass:
 
 
 # --------------------------------------- the steps around the linears (layer.py)
-from .layer import add_rmsnorm_quant_i8  # noqa: E402,F401
+from .layer import (KVCache, add_rmsnorm_quant_i8, kv_append, kv_commit, kv_copy_pages,  # noqa: E402,F401
+                    kv_fork, kv_reserve, kv_workspace)

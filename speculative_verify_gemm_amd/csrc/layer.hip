@@ -9,6 +9,38 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool type_ok(int t) { return t == SVG_F32 || t == SVG_F16 || t == SVG_BF16; }
+hipStream_t to_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
+
+enum { kTable = 1, kPages = 2, kLen = 4, kRefs = 8 };  // what a call needs of a cache
+
+svg_status check_cache(const char* fn, const svg_kv_cache* c, int needs) {
+  if (!c) return svg_fail(SVG_EINVAL, fn, "null cache");
+  if (!c->k || !c->v) return svg_fail(SVG_EINVAL, fn, "null cache pages");
+  if (c->type != SVG_F16 && c->type != SVG_BF16) return svg_fail(SVG_EUNSUPPORTED, fn, "cache type must be fp16 or bf16");
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return svg_fail(SVG_EUNSUPPORTED, fn, "dim must be 64, 128 or 256");
+  if (c->page != 32 && c->page != 64 && c->page != 128)
+    return svg_fail(SVG_EUNSUPPORTED, fn, "page must be 32, 64 or 128");
+  if (c->heads < 1 || c->heads > 1024) return svg_fail(SVG_EUNSUPPORTED, fn, "heads must be 1 .. 1024");
+  if (c->n_pages < 1 || c->n_pages > (1 << 20)) return svg_fail(SVG_EUNSUPPORTED, fn, "n_pages must be 1 .. 2^20");
+  if (c->n_layers < 1 || c->n_layers > 65535) return svg_fail(SVG_EUNSUPPORTED, fn, "n_layers must be 1 .. 65535");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return svg_fail(SVG_EALIGN, fn, "cache pages need 16-byte alignment");
+  if (!needs) return SVG_OK;
+  if (c->n_slots < 0 || c->width < 0) return svg_fail(SVG_EINVAL, fn, "n_slots < 0 or width < 0");
+  if (c->n_slots > 1024) return svg_fail(SVG_EUNSUPPORTED, fn, "n_slots > 1024");
+  if ((int64_t)c->width * c->page >= (1ll << 31) - (1ll << 20))
+    return svg_fail(SVG_EUNSUPPORTED, fn, "width * page must be below 2^31 - 2^20");
+  if (c->n_slots == 0) return SVG_OK;
+  const struct { int bit; const void* p; const char* null; } fields[] = {{kTable, c->table, "null table"},
+                                                                          {kPages, c->pages, "null pages"},
+                                                                          {kLen, c->len, "null len"},
+                                                                          {kRefs, c->refs, "null refs"}};
+  for (const auto& f : fields) {
+    if (!(needs & f.bit)) continue;
+    if (!f.p) return svg_fail(SVG_EINVAL, fn, f.null);
+    if (!aligned(f.p, 4)) return svg_fail(SVG_EALIGN, fn, "table, pages, len and refs need 4-byte alignment");
+  }
+  return SVG_OK;
+}
 
 }  // namespace
 
@@ -34,6 +66,69 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
     return svg_fail(SVG_EALIGN, fn, "signs / x_scale need 4-byte alignment");
   return svg_hip_status(fn, svg_launch_norm_quant(x, x_type, residual, weight, w_type, eps, M, K, signs, block, y, xq,
                                                   x_scale, reinterpret_cast<hipStream_t>(stream)));
+}
+
+svg_status kv_append(const svg_kv_cache* cache, int layer, const float* k, int64_t ld_k, const float* v, int64_t ld_v, int T,
+                     const int32_t* n_rows, void* stream) {
+  static const char* fn = "kv_append";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (T < 1) return svg_fail(SVG_EINVAL, fn, "T < 1");
+  if (layer < 0 || layer >= cache->n_layers) return svg_fail(SVG_EINVAL, fn, "layer outside the cache");
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  if ((int64_t)cache->n_slots * T >= (1ll << 31)) return svg_fail(SVG_EUNSUPPORTED, fn, "n_slots * T >= 2^31");
+  if (ld_k < row || ld_v < row || ld_k % 4 || ld_v % 4 || ld_k >= (1ll << 31) || ld_v >= (1ll << 31))
+    return svg_fail(SVG_EUNSUPPORTED, fn, "ld_k, ld_v must be multiples of 4, at least heads * dim and below 2^31");
+  if (cache->n_slots == 0) return svg_ok();
+  if (!k || !v) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (!aligned(k, 16) || !aligned(v, 16)) return svg_fail(SVG_EALIGN, fn, "k and v need 16-byte alignment");
+  if (!aligned(n_rows, 4)) return svg_fail(SVG_EALIGN, fn, "n_rows needs 4-byte alignment");
+  return svg_hip_status(fn, svg_launch_kv_append(*cache, layer, k, ld_k, v, ld_v, T, n_rows, to_stream(stream)));
+}
+
+svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, const int32_t* n_emit, int32_t* len_out,
+                     void* stream) {
+  static const char* fn = "kv_commit";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (T < 1) return svg_fail(SVG_EINVAL, fn, "T < 1");
+  if (T > SVG_TREE_MAX_NODES) return svg_fail(SVG_EUNSUPPORTED, fn, "T > SVG_TREE_MAX_NODES");
+  if (cache->n_slots == 0) return svg_ok();
+  if (!path || !n_emit || !len_out) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (!aligned(path, 4) || !aligned(n_emit, 4) || !aligned(len_out, 4))
+    return svg_fail(SVG_EALIGN, fn, "path, n_emit and len_out need 4-byte alignment");
+  return svg_hip_status(fn, svg_launch_kv_commit(*cache, T, path, n_emit, len_out, to_stream(stream)));
+}
+
+svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table_out, int32_t* pages_out,
+                   int32_t* len_out, void* stream) {
+  static const char* fn = "kv_fork";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
+  if (cache->n_slots == 0) return svg_ok();
+  if (!src || !table_out || !pages_out || !len_out) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (table_out == cache->table || pages_out == cache->pages || len_out == cache->len)
+    return svg_fail(SVG_EINVAL, fn, "an output is its input");
+  if (!aligned(src, 4) || !aligned(table_out, 4) || !aligned(pages_out, 4) || !aligned(len_out, 4))
+    return svg_fail(SVG_EALIGN, fn, "src and the outputs need 4-byte alignment");
+  return svg_hip_status(fn, svg_launch_kv_fork(*cache, src, table_out, pages_out, len_out, to_stream(stream)));
+}
+
+svg_status kv_reserve(const svg_kv_cache* cache, const int32_t* need, int32_t* status, void* workspace, void* stream) {
+  static const char* fn = "kv_reserve";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
+  if (cache->n_slots == 0) return svg_ok();
+  if (!need || !status || !workspace) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (!aligned(need, 4) || !aligned(status, 4)) return svg_fail(SVG_EALIGN, fn, "need and status need 4-byte alignment");
+  if (!aligned(workspace, 8)) return svg_fail(SVG_EALIGN, fn, "workspace needs 8-byte alignment");
+  return svg_hip_status(fn, svg_launch_kv_reserve(*cache, need, status, workspace, to_stream(stream)));
+}
+
+svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream) {
+  static const char* fn = "kv_copy_pages";
+  if (const svg_status st = check_cache(fn, cache, 0)) return st;
+  if (n < 0) return svg_fail(SVG_EINVAL, fn, "n < 0");
+  if (n == 0) return svg_ok();
+  if (!src || !dst) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (!aligned(src, 4) || !aligned(dst, 4)) return svg_fail(SVG_EALIGN, fn, "src and dst need 4-byte alignment");
+  return svg_hip_status(fn, svg_launch_kv_copy(*cache, src, dst, n, to_stream(stream)));
 }
 
 }  // extern "C"

@@ -66,6 +66,19 @@ hipError_t svg_launch_norm_quant(const void* x, int x_type, float* residual, con
                                  double eps, int M, int K, const int8_t* signs, int block, float* y, int8_t* xq,
                                  float* x_scale, hipStream_t stream);
 
+// The paged cache (kv_pages.hip); every argument checked by the caller.
+struct svg_kv_cache;
+hipError_t svg_launch_kv_append(const svg_kv_cache& c, int layer, const float* k, int64_t ld_k, const float* v,
+                                int64_t ld_v, int T, const int32_t* n_rows, hipStream_t stream);
+hipError_t svg_launch_kv_commit(const svg_kv_cache& c, int T, const int32_t* path, const int32_t* n_emit,
+                                int32_t* len_out, hipStream_t stream);
+hipError_t svg_launch_kv_fork(const svg_kv_cache& c, const int32_t* src, int32_t* table_out, int32_t* pages_out,
+                              int32_t* len_out, hipStream_t stream);
+hipError_t svg_launch_kv_reserve(const svg_kv_cache& c, const int32_t* need, int32_t* status, void* workspace,
+                                 hipStream_t stream);
+hipError_t svg_launch_kv_copy(const svg_kv_cache& c, const int32_t* src, const int32_t* dst, int n,
+                              hipStream_t stream);
+
 // Layout conversions (layout.hip): canonical row-major arrays <-> storage.
 hipError_t svg_launch_import_weights(int fmt_w8, int z4, int group, int N, int K, const void* codes,
                                      const uint16_t* scale, const void* zero, void* wq, uint16_t* w_scale,

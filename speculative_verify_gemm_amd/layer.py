@@ -16,6 +16,21 @@ def _bind(lib):
     vp, i, d = ctypes.c_void_p, ctypes.c_int, ctypes.c_double
     lib.add_rmsnorm_quant_i8.argtypes = [vp, i, vp, vp, i, d, i, i, vp, i, vp, vp, vp, vp]
     lib.add_rmsnorm_quant_i8.restype = ctypes.c_int
+    kv, i64 = ctypes.POINTER(KVCacheC), ctypes.c_int64
+    lib.kv_append.argtypes = [kv, i, vp, i64, vp, i64, i, vp, vp]
+    lib.kv_commit.argtypes = [kv, i, vp, vp, vp, vp]
+    lib.kv_fork.argtypes = [kv, vp, vp, vp, vp, vp]
+    lib.kv_reserve.argtypes = [kv, vp, vp, vp, vp]
+    lib.kv_copy_pages.argtypes = [kv, vp, vp, i, vp]
+    for fn in (lib.kv_append, lib.kv_commit, lib.kv_fork, lib.kv_reserve, lib.kv_copy_pages):
+        fn.restype = ctypes.c_int
+
+
+class KVCacheC(ctypes.Structure):
+    """svg_kv_cache (include/svgemm_layer.h)."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v")]
+                + [(n, ctypes.c_int) for n in ("type", "heads", "dim", "page", "n_pages", "n_layers", "n_slots", "width")]
+                + [(n, ctypes.c_void_p) for n in ("table", "pages", "len", "refs")])
 
 
 def _tensor(t, name, dtype, dev):
@@ -81,6 +96,136 @@ def add_rmsnorm_quant_i8(x, residual, weight, eps, signs, xq, x_scale, y=None, b
             or weight.numel() != K or signs.numel() != K or xq.numel() != M * K or x_scale.numel() != M):
         raise ValueError("need residual and y [M, K], weight and signs [K], xq of M * K codes and x_scale [M]")
     _call(_lib().add_rmsnorm_quant_i8, dev, stream, px, kx, pr, pw, kw, eps, M, K, ps, block, py, pq, pc)
+
+
+# ------------------------------------------------------------------ the cache
+class KVCache:
+    """A paged key/value cache and the slots that use it (svg_kv_cache of
+    include/svgemm_layer.h): k, v fp16 or bf16 [n_layers, n_pages, heads, page *
+    dim]; table int32 [n_slots, width], pages and len [n_slots], refs [n_pages]
+    (without them only kv_copy_pages takes the cache).  The object keeps the
+    tensors; their contents are read by the calls on the device only."""
+
+    def __init__(self, k, v, table=None, pages=None, len=None, refs=None, *, dim, page):
+        dev = _device(k, "k")
+        if k.dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"k must be float16 or bfloat16, got {k.dtype}")
+        if k.dim() != 4 or k.shape != v.shape or k.shape[3] != page * dim:
+            raise ValueError("k and v must be [n_layers, n_pages, heads, page * dim]")
+        L, P, H, _ = k.shape
+        c = KVCacheC(_tensor(k, "k", k.dtype, dev), _tensor(v, "v", k.dtype, dev), _FLOATS[k.dtype], H, dim, page, P, L)
+        if table is not None:
+            if table.dim() != 2:
+                raise ValueError("table must be [n_slots, width]")
+            S, c.width = table.shape
+            c.n_slots = S
+            c.table = _tensor(table, "table", torch.int32, dev)
+            for name, t, n in (("pages", pages, S), ("len", len, S), ("refs", refs, P)):
+                if t is None or t.shape != (n,):
+                    raise ValueError(f"{name} must have shape [{n}]")
+                setattr(c, name, _tensor(t, name, torch.int32, dev))
+        self.k, self.v, self.table, self.pages, self.len, self.refs = k, v, table, pages, len, refs
+        self.dim, self.page, self.heads, self.device = dim, page, H, dev
+        self.n_layers, self.n_pages = L, P
+        self.n_slots, self.width = c.n_slots, c.width
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, n_layers, n_pages, heads, dim, page, n_slots, width, dtype=torch.float16, device="cuda"):
+        """A cache of free pages and empty slots (the pages' contents are not set)."""
+        shape = (n_layers, n_pages, heads, page * dim)
+        zeros = lambda n: torch.zeros(n, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device),
+                   torch.full((n_slots, width), -1, dtype=torch.int32, device=device), zeros(n_slots), zeros(n_slots),
+                   zeros(n_pages), dim=dim, page=page)
+
+    def other_tables(self):
+        """The same pages and counts with tables of their own (empty slots): what kv_fork writes to."""
+        return KVCache(self.k, self.v, torch.full_like(self.table, -1), torch.zeros_like(self.pages),
+                       torch.zeros_like(self.len), self.refs, dim=self.dim, page=self.page)
+
+
+def _rows(t, name, cache, width):
+    """fp32 rows [n, ...] of `width` values each, a row contiguous: (address, row stride, n)."""
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
+    n = t.shape[0]
+    if t.dim() == 3:
+        ok = t.shape[1] * t.shape[2] == width and t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+    else:
+        ok = t.dim() == 2 and t.shape[1] == width and t.stride(1) == 1
+    if not ok:
+        raise ValueError(f"{name} must be [n, {width}] or [n, heads, dim] with contiguous rows")
+    return t.data_ptr(), (t.stride(0) if n > 1 else width), n
+
+
+def _slots(t, name, cache, *more):
+    """An int32 tensor of one entry (or a row of `more`) for each slot."""
+    if t.shape != (cache.n_slots, *more):
+        raise ValueError(f"{name} must have shape {[cache.n_slots, *more]}")
+    return _tensor(t, name, torch.int32, cache.device)
+
+
+def kv_append(cache, layer, k, v, T, n_rows=None, stream=None):
+    """Write T new tokens of each slot behind its committed ones, in one layer:
+    k, v fp32 [n_slots * T, heads * dim] (or [.., heads, dim]; rows may lie apart,
+    as in the output of a fused projection); n_rows int32 [n_slots]: fewer of them."""
+    pk, lk, nk = _rows(k, "k", cache, cache.heads * cache.dim)
+    pv, lv, nv = _rows(v, "v", cache, cache.heads * cache.dim)
+    if nk != cache.n_slots * T or nv != nk:
+        raise ValueError("k and v must have n_slots * T rows")
+    pn = None if n_rows is None else _slots(n_rows, "n_rows", cache)
+    _call(_lib().kv_append, cache.device, stream, cache._ref, layer, pk, lk, pv, lv, T, pn)
+
+
+def kv_commit(cache, path, n_emit, len_out=None, stream=None):
+    """Move the accepted path of each slot's tree behind its root, in every
+    layer: path int32 [n_slots, T] and n_emit [n_slots] as tree_accept_greedy
+    writes them; the new lengths go to len_out (None: into the cache's own)."""
+    if path.dim() != 2:
+        raise ValueError("path must be [n_slots, T]")
+    T = path.shape[1]
+    out = cache.len if len_out is None else len_out
+    _call(_lib().kv_commit, cache.device, stream, cache._ref, T, _slots(path, "path", cache, T),
+          _slots(n_emit, "n_emit", cache), _slots(out, "len_out", cache))
+
+
+def kv_fork(cache, src, out, stream=None):
+    """Every slot s of `out` (a KVCache over the same pages and counts, with
+    tables of its own: cache.other_tables()) becomes a fork of slot src[s] of
+    `cache`, keeps it (src[s] == s) or is freed (-1).  Afterwards `cache`'s tables are spent."""
+    if out.k.data_ptr() != cache.k.data_ptr() or out.refs.data_ptr() != cache.refs.data_ptr():
+        raise ValueError("out must be a cache over the same pages and counts")
+    if out.table.shape != cache.table.shape:
+        raise ValueError("out needs tables of the same shape")
+    _call(_lib().kv_fork, cache.device, stream, cache._ref, _slots(src, "src", cache), out._c.table, out._c.pages,
+          out._c.len)
+
+
+def kv_workspace(cache):
+    """A workspace for kv_reserve."""
+    return torch.empty(2 * cache.n_slots + 4, dtype=torch.int32, device=cache.device)
+
+
+def kv_reserve(cache, need, status, workspace, stream=None):
+    """Room for need[s] more tokens of each slot, in pages of its own; status
+    int32 [n_slots]: 0 done, 1 not enough free pages, 2 does not fit the table."""
+    pw = _tensor(workspace, "workspace", torch.int32, cache.device)
+    if workspace.numel() < 2 * cache.n_slots + 4:
+        raise ValueError("workspace is smaller than kv_workspace(cache)")
+    _call(_lib().kv_reserve, cache.device, stream, cache._ref, _slots(need, "need", cache),
+          _slots(status, "status", cache), pw)
+
+
+def kv_copy_pages(cache, src, dst, stream=None):
+    """Copy pages src (int32 [n]) to pages dst in every layer."""
+    if src.dim() != 1 or src.shape != dst.shape:
+        raise ValueError("src and dst must be [n]")
+    _call(_lib().kv_copy_pages, cache.device, stream, cache._ref, _tensor(src, "src", torch.int32, cache.device),
+          _tensor(dst, "dst", torch.int32, cache.device), src.shape[0])
 
 
 def _lib():

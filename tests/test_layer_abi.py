@@ -56,3 +56,63 @@ def test_norm_refusals(svg, kw, code):
 def test_empty_norm(svg):
     assert norm(svg, M=0) == 0 and svg.last_error() == ""
     assert norm(svg, M=0, res=None, y=None) == 0
+
+
+# ---------------------------------------------------------------- the cache
+def cache(svg, **kw):
+    f = dict(k=A, v=A, type=1, heads=2, dim=64, page=32, n_pages=8, n_layers=2, n_slots=2, width=4, table=A, pages=A,
+             len=A, refs=A)
+    f.update(kw)
+    return svg.layer.KVCacheC(*f.values())
+
+
+CACHE_CALLS = {
+    "kv_append": lambda L, c: L.kv_append(c, 0, A, 128, A, 128, 1, None, None),
+    "kv_commit": lambda L, c: L.kv_commit(c, 4, A, A, A + 64, None),
+    "kv_fork": lambda L, c: L.kv_fork(c, A, A + 64, A + 64, A + 64, None),
+    "kv_reserve": lambda L, c: L.kv_reserve(c, A, A, A, None),
+    "kv_copy_pages": lambda L, c: L.kv_copy_pages(c, A, A, 1, None),
+}
+
+
+@pytest.mark.parametrize("call", CACHE_CALLS)
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(type=0), 2), (dict(type=3), 2), (dict(dim=96), 2), (dict(page=16), 2),
+    (dict(heads=0), 2), (dict(heads=1025), 2), (dict(n_pages=0), 2), (dict(n_pages=(1 << 20) + 1), 2), (dict(n_layers=0), 2),
+    (dict(n_layers=65536), 2), (dict(k=MIS), 3), (dict(v=MIS), 3),
+    (dict(n_slots=-1), 1), (dict(width=-1), 1), (dict(n_slots=1025), 2), (dict(width=1 << 26), 2), (dict(table=None), 1),
+    (dict(pages=MIS + 1), 3), (dict(len=None), 1),
+])
+def test_cache_refusals(svg, call, kw, code):
+    if call == "kv_copy_pages" and set(kw) & {"n_slots", "width", "table", "pages", "len"}:
+        pytest.skip("needs no tables")
+    assert CACHE_CALLS[call](svg.lib, ctypes.byref(cache(svg, **kw))) == code
+    assert svg.last_error().startswith(call + ":")
+    assert CACHE_CALLS[call](svg.lib, None) == 1
+
+
+@pytest.mark.parametrize("call", [c for c in CACHE_CALLS if c != "kv_copy_pages"])
+def test_no_slots_is_an_empty_call(svg, call):
+    c = cache(svg, n_slots=0, width=0, table=None, pages=None, len=None, refs=None)
+    assert CACHE_CALLS[call](svg.lib, ctypes.byref(c)) == 0
+
+
+def test_cache_call_refusals(svg):
+    L, c = svg.lib, ctypes.byref(cache(svg))
+    for args, code in (((2, A, 128, A, 128, 1, None), 1), ((-1, A, 128, A, 128, 1, None), 1), ((0, None, 128, A, 128, 1, None), 1),
+                       ((0, A, 128, None, 128, 1, None), 1), ((0, A, 128, A, 128, 0, None), 1), ((0, A, 124, A, 128, 1, None), 2),
+                       ((0, A, 130, A, 128, 1, None), 2), ((0, A, 128, A, 1 << 31, 1, None), 2), ((0, A, 128, A, 128, 1 << 30, None), 2),
+                       ((0, MIS, 128, A, 128, 1, None), 3), ((0, A, 128, MIS, 128, 1, None), 3), ((0, A, 128, A, 128, 1, MIS), 3)):
+        assert L.kv_append(c, *args, None) == code, args
+    for args, code in (((0, A, A, A), 1), ((33, A, A, A), 2), ((4, None, A, A), 1), ((4, A, None, A), 1), ((4, A, A, None), 1),
+                       ((4, MIS, A, A), 3), ((4, A, MIS, A), 3), ((4, A, A, MIS), 3)):
+        assert L.kv_commit(c, *args, None) == code, args
+    B = A + 64
+    for args, code in (((None, B, B, B), 1), ((A, None, B, B), 1), ((A, A, B, B), 1), ((A, B, A, B), 1), ((A, B, B, A), 1),
+                       ((MIS, B, B, B), 3), ((A, B, B, MIS), 3)):
+        assert L.kv_fork(c, *args, None) == code, args
+    assert L.kv_fork(ctypes.byref(cache(svg, refs=None)), A, B, B, B, None) == 1
+    for args, code in (((None, A, A), 1), ((A, None, A), 1), ((A, A, None), 1), ((A, A, A + 4), 3), ((MIS, A, A), 3)):
+        assert L.kv_reserve(c, *args, None) == code, args
+    for args, code in (((A, A, -1), 1), ((None, A, 1), 1), ((A, None, 1), 1), ((MIS, A, 1), 3), ((None, None, 0), 0)):
+        assert L.kv_copy_pages(c, *args, None) == code, args
