@@ -170,6 +170,47 @@ svg_status kv_reserve(const svg_kv_cache* cache, const int32_t* need, int32_t* s
  */
 svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream);
 
+/*
+ * tree_attention -- attention of the draft trees of all slots over the cache, in
+ * one layer: the keys and values of a tree's nodes have been appended
+ * (kv_append) and are not committed yet.  Plain decoding is a tree of one node.
+ *
+ *  q         fp32 [n_slots * T] rows of q_heads * dim values, rows ld_q values apart (a multiple
+ *            of 4, >= q_heads * dim), 16-byte aligned: row s * T + i is node i of slot s, whose key and
+ *            value lie at position len[s] + i.
+ *  q_heads   a multiple of heads: query head a reads key/value head a / (q_heads / heads); at most 4096.
+ *  parent    int32 [n_slots][T]: parent[s][0] = -1, 0 <= parent[s][i] < i (as tree_accept_greedy);
+ *            NULL: parent[i] = i - 1, a chain.
+ *  T         nodes of a slot, 1 .. SVG_TREE_MAX_NODES.
+ *  n_nodes   int32 [n_slots] or NULL: nodes of each slot (the nearest of 0 .. T; 0: the slot is
+ *            idle); NULL: all T.  Behind a slot's nodes rows of q do not matter and rows of out are left as they were.
+ *  shared    int32 [1] or NULL: a number of leading tokens that are the same pages in the
+ *            table rows of all slots that are not idle (as after kv_fork).  They are read once for
+ *            all rows.  What is used is the largest multiple of 32 that neither this number nor any
+ *            of those slots' len is below; it does not change what is computed.
+ *  scale     finite; the scores are scale * q . k.
+ *  out       fp32 [n_slots * T][q_heads * dim], 16-byte aligned.
+ *  workspace tree_attention_workspace() bytes, 256-byte aligned; its contents need not be set or kept.
+ *            Calls that may overlap need different ones.
+ *
+ *  Row (s, i, a): o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale * q . k_t), over the positions t < len[s] and
+ *  len[s] + j for the nodes j of i's root path, i included.  Sums and accumulators are fp32; q and p
+ *  enter the 16-bit matrix products in parts that carry at least 16 bits of each, so an output is within about 1e-5 of
+ *  its row's largest of an exact one.  Keys and values of tokens that a row does not see never reach it, whatever they are.
+ *  NaN rows: a node whose root path breaks the rule above; a row that reads a page number outside the cache; all of a
+ *  slot whose pages do not cover len + n_nodes.
+ *  Reads table, pages, len.  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the
+ *  cache or a scale that is not finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads
+ *  or ld_q; SVG_EALIGN.
+ *
+ * tree_attention_workspace -- the bytes of that workspace (host only).
+ */
+#define SVG_ATTN_MAX_GROUPS 512
+svg_status tree_attention_workspace(const svg_kv_cache* cache, int q_heads, int T, uint64_t* bytes);
+svg_status tree_attention(const svg_kv_cache* cache, int layer, const float* q, int64_t ld_q, int q_heads, const int32_t* parent,
+                          int T, const int32_t* n_nodes, const int32_t* shared, float scale, float* out, void* workspace,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif

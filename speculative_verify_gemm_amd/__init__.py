@@ -537,4 +537,4 @@ class LinearPass:
 
 # --------------------------------------- the steps around the linears (layer.py)
 from .layer import (KVCache, add_rmsnorm_quant_i8, kv_append, kv_commit, kv_copy_pages,  # noqa: E402,F401
-                    kv_fork, kv_reserve, kv_workspace)
+                    kv_fork, kv_reserve, kv_workspace, tree_attention, tree_attention_workspace)

@@ -21,7 +21,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libsvgemm.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["rht_quant.hip", "linear_w4.hip", "linear_w8.hip", "tree_accept.hip", "tree_deltanet.hip",
-           "pass.hip", "layout.hip", "svgemm.hip", "norm_quant.hip", "kv_pages.hip", "layer.hip"]
+           "pass.hip", "layout.hip", "svgemm.hip", "norm_quant.hip", "kv_pages.hip",
+           "tree_attention.hip", "layer.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [
@@ -33,6 +34,11 @@ CFLAGS = [
     "-Wall", "-Wno-unused-function",
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
+
+
+# Sources compiled without one of the flags: the attention's accumulators take
+# turns with its operands, and the compiler is left to place them.
+LESS_FLAGS = {"tree_attention.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
 
 
 def source_digest() -> str:
@@ -62,7 +68,12 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-    cmd = [hipcc(), *CFLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    flags = list(CFLAGS)
+    less = LESS_FLAGS.get(src)
+    if less:
+        at = next(i for i in range(len(flags)) if tuple(flags[i:i + len(less)]) == less)
+        del flags[at:at + len(less)]
+    cmd = [hipcc(), *flags, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

@@ -131,4 +131,41 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
   return svg_hip_status(fn, svg_launch_kv_copy(*cache, src, dst, n, to_stream(stream)));
 }
 
+static svg_status check_heads(const char* fn, const svg_kv_cache* c, int q_heads, int T) {
+  if (T < 1 || q_heads < 1) return svg_fail(SVG_EINVAL, fn, "T < 1 or q_heads < 1");
+  if (T > SVG_TREE_MAX_NODES) return svg_fail(SVG_EUNSUPPORTED, fn, "T > SVG_TREE_MAX_NODES");
+  if (q_heads % c->heads || q_heads > 4096)
+    return svg_fail(SVG_EUNSUPPORTED, fn, "q_heads must be a multiple of the cache's heads, at most 4096");
+  return SVG_OK;
+}
+
+svg_status tree_attention_workspace(const svg_kv_cache* cache, int q_heads, int T, uint64_t* bytes) {
+  static const char* fn = "tree_attention_workspace";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = check_heads(fn, cache, q_heads, T)) return st;
+  if (!bytes) return svg_fail(SVG_EINVAL, fn, "null bytes");
+  *bytes = cache->n_slots ? svg_tree_attention_bytes(*cache, T, q_heads / cache->heads) : 0;
+  return svg_ok();
+}
+
+svg_status tree_attention(const svg_kv_cache* cache, int layer, const float* q, int64_t ld_q, int q_heads, const int32_t* parent,
+                          int T, const int32_t* n_nodes, const int32_t* shared, float scale, float* out, void* workspace,
+                          void* stream) {
+  static const char* fn = "tree_attention";
+  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = check_heads(fn, cache, q_heads, T)) return st;
+  if (layer < 0 || layer >= cache->n_layers) return svg_fail(SVG_EINVAL, fn, "layer outside the cache");
+  if (!std::isfinite(scale)) return svg_fail(SVG_EINVAL, fn, "scale must be finite");
+  if (ld_q < (int64_t)q_heads * cache->dim || ld_q % 4 || ld_q >= (1ll << 31))
+    return svg_fail(SVG_EUNSUPPORTED, fn, "ld_q must be a multiple of 4, at least q_heads * dim and below 2^31");
+  if (cache->n_slots == 0) return svg_ok();
+  if (!q || !out || !workspace) return svg_fail(SVG_EINVAL, fn, "null required pointer");
+  if (!aligned(q, 16) || !aligned(out, 16)) return svg_fail(SVG_EALIGN, fn, "q and out need 16-byte alignment");
+  if (!aligned(workspace, 256)) return svg_fail(SVG_EALIGN, fn, "workspace needs 256-byte alignment");
+  if (!aligned(parent, 4) || !aligned(n_nodes, 4) || !aligned(shared, 4))
+    return svg_fail(SVG_EALIGN, fn, "parent, n_nodes and shared need 4-byte alignment");
+  return svg_hip_status(fn, svg_launch_tree_attention(*cache, layer, q, ld_q, q_heads / cache->heads, parent, T, n_nodes,
+                                                      shared, scale, out, workspace, to_stream(stream)));
+}
+
 }  // extern "C"

@@ -79,6 +79,13 @@ hipError_t svg_launch_kv_reserve(const svg_kv_cache& c, const int32_t* need, int
 hipError_t svg_launch_kv_copy(const svg_kv_cache& c, const int32_t* src, const int32_t* dst, int n,
                               hipStream_t stream);
 
+// Attention over the paged cache (tree_attention.hip); G query heads share a
+// key/value head.  bytes: the workspace.
+uint64_t svg_tree_attention_bytes(const svg_kv_cache& c, int T, int G);
+hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const float* q, int64_t ld_q, int G,
+                                     const int32_t* parent, int T, const int32_t* n_nodes, const int32_t* shared,
+                                     float scale, float* out, void* workspace, hipStream_t stream);
+
 // Layout conversions (layout.hip): canonical row-major arrays <-> storage.
 hipError_t svg_launch_import_weights(int fmt_w8, int z4, int group, int N, int K, const void* codes,
                                      const uint16_t* scale, const void* zero, void* wq, uint16_t* w_scale,

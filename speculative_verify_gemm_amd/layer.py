@@ -22,7 +22,9 @@ def _bind(lib):
     lib.kv_fork.argtypes = [kv, vp, vp, vp, vp, vp]
     lib.kv_reserve.argtypes = [kv, vp, vp, vp, vp]
     lib.kv_copy_pages.argtypes = [kv, vp, vp, i, vp]
-    for fn in (lib.kv_append, lib.kv_commit, lib.kv_fork, lib.kv_reserve, lib.kv_copy_pages):
+    lib.tree_attention_workspace.argtypes = [kv, i, i, ctypes.POINTER(ctypes.c_uint64)]
+    lib.tree_attention.argtypes = [kv, i, vp, i64, i, vp, i, vp, vp, ctypes.c_float, vp, vp, vp]
+    for fn in (lib.tree_attention_workspace, lib.tree_attention, lib.kv_append, lib.kv_commit, lib.kv_fork, lib.kv_reserve, lib.kv_copy_pages):
         fn.restype = ctypes.c_int
 
 
@@ -130,6 +132,7 @@ class KVCache:
         self.n_slots, self.width = c.n_slots, c.width
         self._c = c
         self._ref = ctypes.byref(c)
+        self._attn_bytes = {}  # workspace sizes by (q_heads, T)
 
     @classmethod
     def empty(cls, n_layers, n_pages, heads, dim, page, n_slots, width, dtype=torch.float16, device="cuda"):
@@ -226,6 +229,47 @@ def kv_copy_pages(cache, src, dst, stream=None):
         raise ValueError("src and dst must be [n]")
     _call(_lib().kv_copy_pages, cache.device, stream, cache._ref, _tensor(src, "src", torch.int32, cache.device),
           _tensor(dst, "dst", torch.int32, cache.device), src.shape[0])
+
+
+# -------------------------------------------------------------- attention
+def tree_attention_workspace(cache, q_heads, T):
+    """A workspace for tree_attention calls of these sizes (one for each stream that makes them)."""
+    n = ctypes.c_uint64()
+    status = _lib().tree_attention_workspace(cache._ref, q_heads, T, ctypes.byref(n))
+    if status:
+        from . import SvgError, last_error
+        raise SvgError(status, last_error())
+    return torch.empty(max(n.value, 1), dtype=torch.uint8, device=cache.device)
+
+
+def tree_attention(cache, layer, q, parent, out, workspace, scale=None, n_nodes=None, shared=None, stream=None):
+    """Attention of every slot's draft tree over the cache, in one layer: q fp32
+    [n_slots * T, q_heads, dim] (rows may lie apart, as in the output of a fused
+    projection), parent int32 [n_slots, T] (None: chains; T is then q's rows per
+    slot), out fp32 of q's shape, workspace from tree_attention_workspace();
+    scale defaults to 1 / sqrt(dim); n_nodes int32 [n_slots]: nodes of each tree;
+    shared int32 [1]: leading tokens that are the same pages in every slot."""
+    S, D = cache.n_slots, cache.dim
+    heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // D
+    pq, ld, n = _rows(q, "q", cache, heads * D)
+    T = n // S if S else 1
+    if n != S * T:
+        raise ValueError("q must have n_slots * T rows")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    need = cache._attn_bytes.get((heads, T))
+    if need is None:
+        b = ctypes.c_uint64()
+        if _lib().tree_attention_workspace(cache._ref, heads, T, ctypes.byref(b)) == 0:
+            need = cache._attn_bytes[(heads, T)] = b.value
+    if need is not None and workspace.numel() * workspace.element_size() < need:
+        raise ValueError("workspace is smaller than tree_attention_workspace(cache, q_heads, T)")
+    pp = None if parent is None else _slots(parent, "parent", cache, T)
+    pn = None if n_nodes is None else _slots(n_nodes, "n_nodes", cache)
+    ps = None if shared is None else _tensor(shared, "shared", torch.int32, cache.device)
+    _call(_lib().tree_attention, cache.device, stream, cache._ref, layer, pq, ld, heads, pp, T, pn, ps,
+          D ** -0.5 if scale is None else scale, _tensor(out, "out", torch.float32, cache.device),
+          _tensor(workspace, "workspace", torch.uint8, cache.device))
 
 
 def _lib():

@@ -72,26 +72,29 @@ CACHE_CALLS = {
     "kv_fork": lambda L, c: L.kv_fork(c, A, A + 64, A + 64, A + 64, None),
     "kv_reserve": lambda L, c: L.kv_reserve(c, A, A, A, None),
     "kv_copy_pages": lambda L, c: L.kv_copy_pages(c, A, A, 1, None),
+    "tree_attention": lambda L, c: L.tree_attention(c, 0, A, 512, 8, A, 4, None, None, 0.1, A, A, None),
+    "tree_attention_workspace": lambda L, c: L.tree_attention_workspace(c, 8, 4, ctypes.byref(ctypes.c_uint64())),
 }
+NO_TABLES = {"kv_copy_pages"}
 
 
-@pytest.mark.parametrize("call", CACHE_CALLS)
-@pytest.mark.parametrize("kw,code", [
-    (dict(k=None), 1), (dict(v=None), 1), (dict(type=0), 2), (dict(type=3), 2), (dict(dim=96), 2), (dict(page=16), 2),
-    (dict(heads=0), 2), (dict(heads=1025), 2), (dict(n_pages=0), 2), (dict(n_pages=(1 << 20) + 1), 2), (dict(n_layers=0), 2),
-    (dict(n_layers=65536), 2), (dict(k=MIS), 3), (dict(v=MIS), 3),
-    (dict(n_slots=-1), 1), (dict(width=-1), 1), (dict(n_slots=1025), 2), (dict(width=1 << 26), 2), (dict(table=None), 1),
-    (dict(pages=MIS + 1), 3), (dict(len=None), 1),
-])
+def cache_refusals():
+    bad = [(dict(k=None), 1), (dict(v=None), 1), (dict(type=0), 2), (dict(type=3), 2), (dict(dim=96), 2), (dict(page=16), 2),
+           (dict(heads=0), 2), (dict(heads=1025), 2), (dict(n_pages=0), 2), (dict(n_pages=(1 << 20) + 1), 2),
+           (dict(n_layers=0), 2), (dict(n_layers=65536), 2), (dict(k=MIS), 3), (dict(v=MIS), 3)]
+    tables = [(dict(n_slots=-1), 1), (dict(width=-1), 1), (dict(n_slots=1025), 2), (dict(width=1 << 26), 2),
+              (dict(table=None), 1), (dict(pages=MIS + 1), 3), (dict(len=None), 1)]
+    return [(call, kw, code) for call in CACHE_CALLS for kw, code in bad + ([] if call in NO_TABLES else tables)]
+
+
+@pytest.mark.parametrize("call,kw,code", cache_refusals())
 def test_cache_refusals(svg, call, kw, code):
-    if call == "kv_copy_pages" and set(kw) & {"n_slots", "width", "table", "pages", "len"}:
-        pytest.skip("needs no tables")
     assert CACHE_CALLS[call](svg.lib, ctypes.byref(cache(svg, **kw))) == code
     assert svg.last_error().startswith(call + ":")
     assert CACHE_CALLS[call](svg.lib, None) == 1
 
 
-@pytest.mark.parametrize("call", [c for c in CACHE_CALLS if c != "kv_copy_pages"])
+@pytest.mark.parametrize("call", [c for c in CACHE_CALLS if c not in NO_TABLES])
 def test_no_slots_is_an_empty_call(svg, call):
     c = cache(svg, n_slots=0, width=0, table=None, pages=None, len=None, refs=None)
     assert CACHE_CALLS[call](svg.lib, ctypes.byref(c)) == 0
@@ -116,3 +119,34 @@ def test_cache_call_refusals(svg):
         assert L.kv_reserve(c, *args, None) == code, args
     for args, code in (((A, A, -1), 1), ((None, A, 1), 1), ((A, None, 1), 1), ((MIS, A, 1), 3), ((None, None, 0), 0)):
         assert L.kv_copy_pages(c, *args, None) == code, args
+
+
+def attention(svg, c=None, **kw):
+    a = dict(layer=0, q=A, ld=512, heads=8, parent=A, T=4, n=None, shared=None, scale=0.1, out=A, ws=A)
+    a.update(kw)
+    return svg.lib.tree_attention(ctypes.byref(c or cache(svg)), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(layer=2), 1), (dict(layer=-1), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(ws=None), 1), (dict(T=0), 1),
+    (dict(heads=0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(T=33), 2), (dict(heads=7), 2),
+    (dict(heads=4098, ld=1 << 20), 2), (dict(ld=508), 2), (dict(ld=514), 2), (dict(ld=1 << 31), 2), (dict(q=MIS), 3),
+    (dict(out=MIS), 3), (dict(ws=A + 128), 3), (dict(parent=MIS), 3), (dict(n=MIS), 3), (dict(shared=MIS), 3),
+])
+def test_attention_refusals(svg, kw, code):
+    assert attention(svg, **kw) == code
+    assert svg.last_error().startswith("tree_attention:")
+
+
+def test_attention_workspace_sizes(svg):
+    n = ctypes.c_uint64()
+
+    def size(heads, T, **kw):
+        assert svg.lib.tree_attention_workspace(ctypes.byref(cache(svg, **kw)), heads, T, ctypes.byref(n)) == 0
+        return n.value
+
+    # a partial for each of 512 workgroups at least: one row tile of 16 rows, dim + 2 values
+    assert size(2, 1, n_slots=1) >= 512 * 16 * 66 * 4
+    assert size(8, 32, n_slots=8) > size(8, 1, n_slots=8) > size(8, 1, n_slots=1)
+    assert size(8, 4, n_slots=0) == 0
+    assert svg.lib.tree_attention_workspace(ctypes.byref(cache(svg)), 8, 4, None) == 1
