@@ -64,7 +64,7 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
  *  heads     key/value heads, 1 .. 1024.   dim   64, 128 or 256 values a head.
  *  page      tokens of a page: 32, 64 or 128.
  *  n_pages   1 .. 2^20.    n_layers  1 .. 65535.    n_slots  0 .. 1024 sequences.
- *  width     entries of a table row; width * page < 2^31 - 2^20.
+ *  width     entries of a table row; width * page <= 2^25 tokens.
  *  table     int32 [n_slots][width]: the pages of a slot in token order; token t
  *            of slot s lies in page table[s][t / page], place t % page.
  *  pages     int32 [n_slots]: entries of each row that are in use.

@@ -27,8 +27,8 @@ svg_status check_cache(const char* fn, const svg_kv_cache* c, int needs) {
   if (!needs) return SVG_OK;
   if (c->n_slots < 0 || c->width < 0) return svg_fail(SVG_EINVAL, fn, "n_slots < 0 or width < 0");
   if (c->n_slots > 1024) return svg_fail(SVG_EUNSUPPORTED, fn, "n_slots > 1024");
-  if ((int64_t)c->width * c->page >= (1ll << 31) - (1ll << 20))
-    return svg_fail(SVG_EUNSUPPORTED, fn, "width * page must be below 2^31 - 2^20");
+  if ((int64_t)c->width * c->page > (1ll << 25))
+    return svg_fail(SVG_EUNSUPPORTED, fn, "width * page > 2^25");
   if (c->n_slots == 0) return SVG_OK;
   const struct { int bit; const void* p; const char* null; } fields[] = {{kTable, c->table, "null table"},
                                                                           {kPages, c->pages, "null pages"},

@@ -14,12 +14,20 @@
 // writes one partial (O, M, sum) for each item it meets.  The lengths are read
 // on the device: the same launch serves any lengths, also from a captured graph.
 //
-// A workgroup's four waves split an item's rows (16 RT each) as far as it has them,
-// and its tiles otherwise.  A page is laid out in the lane order of
-// v_mfma_f32_16x16x32: S^T = K Q^T leaves a row's scores in one lane column, four
-// consecutive tokens in each lane, which is the order the values are stored in, so
-// the probabilities go from the first product's result registers into the second's
-// operand registers with no exchange and no LDS: O^T += V^T P^T.
+// Layout.  A page is laid out in the lane order of v_mfma_f32_16x16x32: S^T = K Q^T
+// leaves a row's scores in one lane column, four consecutive tokens in each lane,
+// which is the order the values are stored in, so the probabilities go from the
+// first product's result registers into the second's operand registers with no
+// exchange: O^T += V^T P^T.  A wave reads a tile as contiguous KiB.
+//
+// Two ways over an item's tiles, by the rows that the launch's largest item may have:
+//  * thin (up to 16 RT rows: plain decoding, small trees): bound by the cache's
+//    bytes.  Each of the eight waves takes every eighth tile for all the rows,
+//    keys and values straight into registers, the next tile's requested as
+//    soon as the registers are free; the waves' results are joined in LDS.
+//  * thick (more rows: large trees, shared prefixes): every tile is used by up to eight
+//    waves of 16 rows each.  It is brought into LDS once, by loads that go there
+//    directly and run STAGES - 1 tiles ahead, one barrier a tile.
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
 // two and split into 16-bit parts (two of fp16: 22 bits; three of bf16: 24 bits), one
@@ -40,7 +48,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256, kWaves = 4;
+constexpr int kThreads = 512, kWaves = 8;
 constexpr int kMaxGroups = SVG_ATTN_MAX_GROUPS;
 constexpr int kMaxSlots = 1024;
 constexpr float kLift = 9.f, kSlack = 6.f;
@@ -48,7 +56,15 @@ constexpr float kLow = -1e30f;  // below every score: no token seen yet
 // A probability is 2^(f s + bias), bias = kLift - f m: one operation, off by half a step of f m.  Beyond
 // kFar that step would be felt as a factor, and far beyond it would overflow: 2^(f (s - m) + kLift) then.
 constexpr float kFar = 65536.f;
-constexpr int kMinTiles = 4;    // tiles of a workgroup at least
+// A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
+// takes.  A workgroup gets kMinThin / kMinThick units at least.
+constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 16, kMinThick = 6;
+
+// Row tiles of an item that is walked the thin way.
+template <int D>
+constexpr int kThinTiles = D < 256 ? 2 : 1;  // (dim 256: the accumulators of two do not fit)
+
+enum { kPrefix = 1, kSlots = 2 };
 
 struct AttnArgs {
   svg_kv_cache c;
@@ -57,19 +73,27 @@ struct AttnArgs {
   const int32_t* n_nodes;
   const int32_t* shared;
   float* out;
-  float* part;        // partials: see Shape
+  char* ws;           // see Shape
   long ld_q;
   int layer, T, G, groups;
+  int min_units, item_cost;
+  int kinds;          // items of this launch: kPrefix, kSlots
   float scale;
 };
 
-// Rows of an item block and the places of partials, the same on host and device.
+// What the second launch has to know of an item: the workgroups that wrote partials of it.
+struct Span {
+  int first, count;
+};
+
+// Rows of an item block and the workspace's parts, the same on host and device:
+// a header (the prefix that was used), a Span for each item, (M, sum) and O of every row of partials.
 struct Shape {
   int block_p, block_s;   // rows of a prefix item, of a slot item
   int rb_p, rb_s;         // row blocks
   long items_p, items_s;
-  __host__ __device__ Shape(int S, int T, int G, int heads, int rt) {
-    const int most = 16 * rt * kWaves;
+  __host__ __device__ Shape(int S, int T, int G, int heads) {
+    const int most = 16 * kWaves;
     const long rows_p = (long)S * T * G, rows_s = (long)T * G;
     block_p = (int)(rows_p < most ? (rows_p + 15) / 16 * 16 : most);
     block_s = (int)(rows_s < most ? (rows_s + 15) / 16 * 16 : most);
@@ -78,7 +102,8 @@ struct Shape {
     items_p = (long)heads * rb_p;
     items_s = (long)heads * rb_s * S;
   }
-  // first row of partials of workgroup w in item j (prefix items, then slot items)
+  // first row of partials of workgroup w in item j (prefix items, then slot items): either number rising by one
+  // is another place, and the pairs that occur rise in both
   __host__ __device__ long slot_p(long w, long j) const { return (w + j) * block_p; }
   __host__ __device__ long slot_s(long w, long j) const {
     return (long)(kMaxGroups + items_p) * block_p + (w + j) * block_s;
@@ -86,18 +111,27 @@ struct Shape {
   __host__ __device__ long rows() const {
     return (long)(kMaxGroups + items_p) * block_p + (long)(kMaxGroups + items_s) * block_s;
   }
+  __host__ __device__ size_t spans_at() const { return 256; }
+  __host__ __device__ size_t stats_at() const { return (spans_at() + (size_t)(items_p + items_s) * sizeof(Span) + 255) / 256 * 256; }
+  __host__ __device__ size_t parts_at() const { return (stats_at() + (size_t)rows() * 8 + 255) / 256 * 256; }
+  __host__ __device__ size_t bytes(int dim) const { return parts_at() + (size_t)rows() * dim * 4; }
 };
 
 // How the launch's work is dealt out; the same in every workgroup.
 struct Plan {
-  long cum[kMaxSlots + 1];  // tiles of the slots before s (own tokens)
+  int cum[kMaxSlots + 1];   // units of an item of each slot before s (own tokens), added up
   int len[kMaxSlots];       // committed tokens; -1: not a valid slot
   int nodes[kMaxSlots];
+  int red[4][kWaves];
+};
+// The part of it that every wave keeps in scalar registers.
+struct Deal {
   int prefix, first;        // shared tokens (a multiple of 32), a slot whose row names their pages
   long total, units_p;      // units of the launch, of the prefix items
-  int groups;               // workgroups that take part
-  long wred[kWaves];
-  int ired[3][kWaves];
+  int groups;               // workgroups that take part: w has the units from start(w) on
+  long quot;                // total / groups, and the rest
+  int rest;
+  SVG_DEV long start(int w) const { return w * quot + (u32)(w * rest) / (u32)groups; }
 };
 
 SVG_DEV int node_count(const AttnArgs& a, int s) {
@@ -105,84 +139,136 @@ SVG_DEV int node_count(const AttnArgs& a, int s) {
   const int n = a.n_nodes[s];
   return n < 0 ? 0 : (n > a.T ? a.T : n);
 }
+// Committed tokens of a slot, -1 where its pages do not cover them and its nodes.
+SVG_DEV int valid_len(const AttnArgs& a, int s, int nodes) {
+  const int held = a.c.pages[s], len = a.c.len[s];
+  return len < 0 || held < 0 || held > a.c.width || (long)len + nodes > (long)held * a.c.page ? -1 : len;
+}
 
-SVG_DEV void make_plan(const AttnArgs& a, const Shape& sh, Plan& p) {
+// u / d and the rest, 0 <= u < 2^48: the estimate is off by one at most.
+SVG_DEV long divide(long u, int d, int& rest) {
+  const double y = (double)d;
+  double x = __builtin_amdgcn_rcp(y);
+  x = __builtin_fma(__builtin_fma(-y, x, 1.0), x, x);
+  x = __builtin_fma(__builtin_fma(-y, x, 1.0), x, x);
+  long q = (long)((double)u * x);
+  long r = u - q * d;
+  if (r < 0) { --q; r += d; }
+  if (r >= d) { ++q; r -= d; }
+  rest = (int)r;
+  return q;
+}
+SVG_DEV long uniform(long v) {
+  return (long)(((unsigned long)(u32)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                (u32)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+// Minimum and sum over the wave, the same in every lane; the sum of the lanes up to this one.
+template <int CTRL>
+SVG_DEV int dpp(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false); }
+SVG_DEV int min_i(int a, int b) { return a < b ? a : b; }
+SVG_DEV int wave_min(int v) {
+  v = min_i(v, dpp<0xB1>(v));
+  v = min_i(v, dpp<0x4E>(v));
+  v = min_i(v, dpp<0x124>(v));
+  v = min_i(v, dpp<0x128>(v));
+  return min_i(min_i(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+               min_i(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+SVG_DEV int wave_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 16; off <<= 1) {
+    const int y = off == 1 ? dpp<0x111>(v) : (off == 2 ? dpp<0x112>(v) : (off == 4 ? dpp<0x114>(v) : dpp<0x118>(v)));
+    if ((lane & 15) >= off) v += y;
+  }
+  const int a = __builtin_amdgcn_readlane(v, 15), b = a + __builtin_amdgcn_readlane(v, 31),
+            c = b + __builtin_amdgcn_readlane(v, 47);
+  return v + (lane < 16 ? 0 : (lane < 32 ? a : (lane < 48 ? b : c)));
+}
+
+SVG_DEV Deal make_plan(const AttnArgs& a, const Shape& sh, Plan& p) {
   const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // a slot with nodes whose tokens lie inside its pages is active; the others take no part
-  int low = 0x7FFFFFFF, active = 0, first = S;
-  for (int s = tid; s < S; s += kThreads) {
-    const int n = node_count(a, s), held = a.c.pages[s];
-    int len = a.c.len[s];
-    if (len < 0 || held < 0 || held > a.c.width || (long)len + n > (long)held * a.c.page) len = -1;
-    p.len[s] = len;
-    p.nodes[s] = n;
-    if (n > 0 && len >= 0) {
-      low = len < low ? len : low;
-      ++active;
-      first = s < first ? s : first;
+  const int said = a.shared != nullptr ? a.shared[0] : 0;
+  // a slot with nodes whose tokens lie inside its pages is active; the others take no part.  Two slots a thread
+  int n[2], len[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = 2 * tid + i;
+    n[i] = len[i] = 0;
+    if (s < S) {
+      n[i] = node_count(a, s);
+      len[i] = valid_len(a, s, n[i]);
+      p.nodes[s] = n[i];
+      p.len[s] = len[i];
+      if (len[i] < 0) n[i] = 0;
     }
   }
+  Deal d;
+  d.prefix = 0;
+  d.first = 0;
+  if (a.shared != nullptr) {
+    int low = 0x7FFFFFFF, first = S;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int l2 = __shfl_xor(low, off), f2 = __shfl_xor(first, off);
-    low = l2 < low ? l2 : low;
-    first = f2 < first ? f2 : first;
-    active += __shfl_xor(active, off);
+    for (int i = 1; i >= 0; --i)
+      if (n[i] > 0) {
+        low = min_i(low, len[i]);
+        first = 2 * tid + i;
+      }
+    const int two = __builtin_popcountll(__ballot(n[0] > 0)) + __builtin_popcountll(__ballot(n[1] > 0));
+    low = wave_min(low);
+    first = wave_min(first);
+    if (lane == 0) {
+      p.red[0][wave] = low;
+      p.red[1][wave] = first;
+      p.red[2][wave] = two;
+    }
+    __syncthreads();
+    int active = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      low = min_i(low, p.red[0][w]);
+      first = min_i(first, p.red[1][w]);
+      active += p.red[2][w];
+    }
+    if (active > 1) d.prefix = __builtin_amdgcn_readfirstlane((said < 0 ? 0 : min_i(said, low)) & ~31);
+    d.first = __builtin_amdgcn_readfirstlane(first < S ? first : 0);
   }
-  if (lane == 0) {
-    p.ired[0][wave] = low;
-    p.ired[1][wave] = active;
-    p.ired[2][wave] = first;
-  }
+  // units before each slot
+  const int t0 = n[0] > 0 ? ((len[0] + n[0] - d.prefix + 31) >> 5) + a.item_cost : 0;
+  const int t1 = n[1] > 0 ? ((len[1] + n[1] - d.prefix + 31) >> 5) + a.item_cost : 0;
+  const int upto = wave_scan(t0 + t1);
+  if (lane == 63) p.red[3][wave] = upto;
   __syncthreads();
-  active = 0;
+  int before = upto - t0 - t1, all = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    low = p.ired[0][w] < low ? p.ired[0][w] : low;
-    first = p.ired[2][w] < first ? p.ired[2][w] : first;
-    active += p.ired[1][w];
+    const int t = p.red[3][w];
+    if (w < wave) before += t;
+    all += t;
   }
-  int prefix = 0;
-  if (a.shared != nullptr && active > 1) {
-    prefix = a.shared[0];
-    prefix = prefix < 0 ? 0 : (prefix < low ? prefix : low);
-    prefix &= ~31;
-  }
-  // tiles before each slot: four consecutive slots a thread
-  long t[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = 4 * tid + i;
-    t[i] = sum;
-    if (s < S && p.nodes[s] > 0 && p.len[s] >= 0) sum += ((long)p.len[s] + p.nodes[s] - prefix + 31) >> 5;
-  }
-  long x = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const long y = __shfl_up(x, off);
-    if (lane >= off) x += y;
-  }
-  if (lane == 63) p.wred[wave] = x;
+  if (2 * tid < S) p.cum[2 * tid] = before;
+  if (2 * tid + 1 < S) p.cum[2 * tid + 1] = before + t0;
+  if (tid == 0) p.cum[S] = all;
+  d.units_p = (a.kinds & kPrefix) && d.prefix > 0 ? sh.items_p * ((d.prefix >> 5) + a.item_cost) : 0;
+  d.total = uniform(d.units_p + (a.kinds & kSlots ? all * (long)a.c.heads * sh.rb_s : 0));
+  int left;
+  const long want = divide(d.total + a.min_units - 1, a.min_units, left);
+  d.groups = __builtin_amdgcn_readfirstlane(want < 1 ? 1 : (want < a.groups ? (int)want : a.groups));
+  d.quot = uniform(divide(d.total, d.groups, left));
+  d.rest = __builtin_amdgcn_readfirstlane(left);
   __syncthreads();
-  long before = x - sum, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += p.wred[w];
-    all += p.wred[w];
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (4 * tid + i < S) p.cum[4 * tid + i] = before + t[i];
-  if (tid == 0) {
-    p.cum[S] = all;
-    p.prefix = prefix;
-    p.first = first;
-    p.units_p = sh.items_p * (prefix >> 5);
-    p.total = p.units_p + all * (long)a.c.heads * sh.rb_s;
-    const long want = (p.total + kMinTiles - 1) / kMinTiles;
-    p.groups = want < 1 ? 1 : (want < a.groups ? (int)want : a.groups);
-  }
-  __syncthreads();
+  return d;
+}
+static_assert(2 * kThreads >= kMaxSlots, "two slots a thread");
+
+// The workgroup that holds unit u (an estimate, put right: it is off by one at most).
+SVG_DEV int group_of(long u, const Deal& p) {
+  int w = (int)((double)u * __builtin_amdgcn_rcp((double)p.total) * p.groups);
+  w = w < p.groups ? w : p.groups - 1;
+  while (p.start(w) > u) --w;
+  while (w + 1 < p.groups && p.start(w + 1) <= u) ++w;
+  return w;
 }
 
 // ------------------------------------------------------------ 16-bit operands
@@ -224,42 +310,94 @@ SVG_DEV void split2(float x, float y, u32 (&w)[N]) {
 }
 
 // ----------------------------------------------------------------- the kernel
+// vmcnt(N), the other counters left alone.
+template <int N>
+SVG_DEV void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+SVG_DEV void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// 1 KiB from global memory (16 bytes a lane) straight into LDS at byte `to` (the same for the wave).  In asm: the compiler
+// would wait for all of them before it reads any LDS; here wait_loads() and the barrier say what has arrived.
+SVG_DEV void load_to_lds(const char* from, u32 to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(from) : "memory");
+}
+// Bytes of LDS before p.
+SVG_DEV u32 lds_at(const char* p) { return (u32)(uintptr_t)(const __attribute__((address_space(3))) char*)p; }
+
+// This item: one head of one layer, the pages of one table row.
+struct Item {
+  const char *k, *v;         // page 0 of the head, this lane's 16 bytes
+  const int32_t* table;
+  size_t stride;             // bytes of a page of all heads
+  int log_tp;                // log2(tiles of a page)
+  int n_pages;
+  int len, total;            // tree tokens begin at len; tokens in all (a prefix item: beyond every tile)
+  SVG_DEV bool bad(int page) const { return (u32)page >= (u32)n_pages; }
+};
+
+// The page numbers of a run of tiles: 64 of them at a time in the lanes of a register, so that a tile's costs no
+// memory access (which the loads behind it would have to wait for).
+struct Pages {
+  int base, last, v;  // table entry of lane 0; the last entry of the run
+  SVG_DEV void look(const Item& it, int entry) {
+    base = entry;
+    const int e = entry + (int)(threadIdx.x & 63u);
+    v = it.table[e < last ? e : last];
+  }
+  SVG_DEV void start(const Item& it, int tile, int last_tile) {
+    last = last_tile >> it.log_tp;
+    look(it, tile >> it.log_tp);
+  }
+  // tiles in rising order
+  SVG_DEV int at(const Item& it, int tile) {
+    const int entry = tile >> it.log_tp;
+    if (entry - base >= 64) look(it, entry);
+    return __builtin_amdgcn_readlane(v, entry - base);
+  }
+};
+
 template <int D, bool BF, int RT>
 struct Attn {
   using O = Ops<BF>;
   static constexpr int NQ = O::kQ, NC = D / 32, ND = D / 16;
+  static constexpr int TILE = 128 * D;               // bytes of a tile: 32 keys, 32 values
+  static constexpr int QBYTES = RT * NC * NQ * 1024;  // thin: q's parts in LDS
+  static constexpr int JOIN = RT * ND * 1024;         // O of a wave in LDS
+  // thick: TW waves for each share of the rows, tiles of a step; RW shares of RT row tiles; STEPS steps in LDS
+  static constexpr int TW = 1, RW = kWaves / TW, STEPS = D < 256 ? 4 : 3;
+  static constexpr int RING = STEPS * TW * TILE;
+  static_assert(RT * NC <= kWaves, "a wave splits one chunk of q");
+  static_assert(RW * JOIN <= RING || TW == 1, "the join of the token waves takes the ring's place");
 
   struct Row {                 // per lane: row n = lane % 16 of a row tile
     f32x4 o[ND];
     float m, thr, bias, l, f;  // maximum (in units of q . k), when to raise it, exponent's offset, sum, factor
+    float slack;               // kSlack in units of q . k
     int far;                   // (the same for the wave) maxima beyond kFar: the offset is not used
+    SVG_DEV void start(float factor) {
+      f = factor;
+      slack = kSlack * __builtin_amdgcn_rcpf(f);
+      m = thr = kLow;
+      bias = kLift - kLow * f;
+      l = 0.f;
+      far = 0;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     // the maximum in powers of two that o and l are relative to
     SVG_DEV float top() const { return m == kLow ? kLow : (far ? m * f : kLift - bias); }
   };
 
-  // This item: one head of one layer, the pages of one table row.
-  struct Item {
-    const char *k, *v;         // page 0 of the head, this lane's 16 bytes
-    const int32_t* table;
-    size_t stride;             // bytes of a page of all heads
-    int log_tp;                // log2(tiles of a page)
-    int n_pages;
-    int len, total;            // tree tokens begin at len; tokens in all (a prefix item: beyond every tile)
-  };
-
-  SVG_DEV static int page_at(const Item& it, int tile) { return it.table[tile >> it.log_tp]; }
   // Bytes before a tile's keys (and values); a page number outside the cache gives page 0 (and NaN rows).
   SVG_DEV static size_t tile_at(const Item& it, int tile, int page) {
     const u32 in = (u32)tile & ((1u << it.log_tp) - 1u);
-    return (size_t)((u32)page < (u32)it.n_pages ? page : 0) * it.stride + (size_t)in * (32 * D * 2);
-  }
-  SVG_DEV static void load_k(const Item& it, size_t off, u32x4 (&k)[2][NC]) {
-#pragma unroll
-    for (int i = 0; i < 2 * NC; ++i) k[i / NC][i % NC] = *reinterpret_cast<const u32x4*>(it.k + off + 1024 * i);
-  }
-  SVG_DEV static void load_v(const Item& it, size_t off, u32x4 (&v)[ND]) {
-#pragma unroll
-    for (int i = 0; i < ND; ++i) v[i] = *reinterpret_cast<const u32x4*>(it.v + off + 1024 * i);
+    return (size_t)(it.bad(page) ? 0u : (u32)page) * it.stride + (size_t)in * (32 * D * 2);
   }
 
   // Raise the running maximum of a row tile to the largest score seen.
@@ -271,22 +409,23 @@ struct Attn {
     r.far = __any(fabsf(bias) > kFar);
     const float w = __builtin_amdgcn_exp2f(r.far ? (r.m - m) * r.f : bias - r.bias);
     r.m = m;
-    r.thr = m + kSlack / r.f;
+    r.thr = m + r.slack;
     r.bias = bias;
     r.l *= w;
 #pragma unroll
     for (int d = 0; d < ND; ++d) r.o[d] *= w;
   }
 
-  // Scores to probabilities, split in two parts in the order of the second product's operand.  tree: the
+  // Scores to probabilities, split in two parts in the order of the second product's operand.  TREE: the
   // tile holds tree tokens, of which the row sees those of `seen`; its root path being broken makes it NaN.
-  SVG_DEV static void soften(const Item& it, int tile, bool tree, const f32x4 (&s)[2], Row& r, u32 seen, bool broken,
+  template <bool TREE>
+  SVG_DEV static void soften(const Item& it, int tile, const f32x4 (&s)[2], Row& r, u32 seen, bool broken,
                              u32x4 (&p)[2]) {
     float x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][j & 3];
     u32 ok = 0xFFu;
-    if (tree) {
+    if constexpr (TREE) {
       const int first = tile * 32 + 4 * (int)((threadIdx.x & 63) >> 4) - it.len;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -299,16 +438,12 @@ struct Attn {
     }
     const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
     if (__any(top > r.thr)) raise(r, top);
-    if (r.far) {
+    const float less = r.far ? r.m : 0.f, more = r.far ? kLift : r.bias;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j] - r.m, r.f, kLift);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j], r.f, r.bias);
-    }
+    for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j] - less, r.f, more);
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j]);
-    if (tree) {
+    if constexpr (TREE) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (!((ok >> j) & 1u)) x[j] = 0.f;
@@ -325,203 +460,360 @@ struct Attn {
     }
   }
 
-  // Values of a tile with tree tokens: those behind the last token are whatever the page held, and become 0.  True
-  // (for the wave) if any other is not finite.
-  SVG_DEV static bool clean(const Item& it, int tile, u32x4 (&v)[ND]) {
+  // Which halves of a lane's words are tokens of the item: those behind the last token are whatever the page held.
+  SVG_DEV static u32x4 token_mask(const Item& it, int tile) {
     const int first = tile * 32 + 4 * (int)((threadIdx.x & 63) >> 4);
-    u32 odd = 0, keep[4];
+    u32x4 keep;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const int tok = first + 2 * (w & 1) + 16 * (w >> 1);
       keep[w] = (tok < it.total ? 0xFFFFu : 0u) | (tok + 1 < it.total ? 0xFFFF0000u : 0u);
     }
+    return keep;
+  }
+  // O += V^T P^T, val(d) the values of columns 16 d ..
+  template <class F>
+  SVG_DEV static void gather(F val, const u32x4 (&p)[2], Row& r) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
+      const u32x4 v = val(d);
+      r.o[d] = O::mfma(v, p[0], r.o[d]);
+      r.o[d] = O::mfma(v, p[1], r.o[d]);
+    }
+  }
+  // The same for a tile with tree tokens.  Values that are not finite are left out of the product (0 times them
+  // would be NaN in every row) and make NaN where a row has a share of them.
+  template <class F>
+  SVG_DEV static void gather_tree(F val, const u32x4 keep, const u32x4 (&p)[2], Row& r) {
+    u32 odd = 0;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      u32x4 v = val(d) & keep;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        v[d][w] &= keep[w];
-        odd |= O::odd(v[d][w]);
+        const u32 b = O::odd(v[w]) >> 15;  // 1 in each half
+        odd |= b;
+        v[w] &= ~(b * 0xFFFFu);
       }
-      __builtin_amdgcn_sched_barrier(0);
+      r.o[d] = O::mfma(v, p[0], r.o[d]);
+      r.o[d] = O::mfma(v, p[1], r.o[d]);
+      __builtin_amdgcn_sched_barrier(0);  // one block at a time: this path must not set the kernel's registers
     }
-    return __any(odd != 0);
-  }
-
-  // O += V^T P^T.
-  SVG_DEV static void gather(const u32x4 (&v)[ND], const u32x4 (&p)[2], Row& r) {
+    if (__any(odd != 0)) {
+      u32x4 some;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      r.o[d] = O::mfma(v[d], p[0], r.o[d]);
-      r.o[d] = O::mfma(v[d], p[1], r.o[d]);
-    }
-  }
-  // The same with values that are not finite: they are left out of the product (0 times them would be NaN in
-  // every row) and make NaN where a row has a share of them.
-  SVG_DEV static void gather_odd(const u32x4 (&v)[ND], const u32x4 (&p)[2], Row& r) {
-    u32x4 some;
+      for (int w = 0; w < 4; ++w)
+        some[w] = ((p[0][w] & 0xFFFFu) ? O::kOne : 0u) | ((p[0][w] >> 16) ? O::kOne << 16 : 0u);
 #pragma unroll
-    for (int w = 0; w < 4; ++w)
-      some[w] = ((p[0][w] & 0xFFFFu) ? O::kOne : 0u) | ((p[0][w] >> 16) ? O::kOne << 16 : 0u);
+      for (int d = 0; d < ND; ++d) {
+        u32x4 y = val(d) & keep;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      u32x4 x = v[d], y;
+        for (int w = 0; w < 4; ++w) y[w] = (O::odd(y[w]) >> 15) * O::kOne;
+        const f32x4 hit = O::mfma(y, some, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const u32 b = O::odd(x[w]) >> 15;  // 1 in each half
-        y[w] = b * O::kOne;
-        x[w] &= ~(b * 0xFFFFu);
+        for (int i = 0; i < 4; ++i) r.o[d][i] = hit[i] == 0.f ? r.o[d][i] : __builtin_nanf("");
+        __builtin_amdgcn_sched_barrier(0);
       }
-      r.o[d] = O::mfma(x, p[0], r.o[d]);
-      r.o[d] = O::mfma(x, p[1], r.o[d]);
-      const f32x4 hit = O::mfma(y, some, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!(hit[i] == 0.f)) r.o[d][i] = __builtin_nanf("");
-      __builtin_amdgcn_sched_barrier(0);  // one block at a time: a rare path must not set the kernel's registers
     }
   }
 
-  // Tiles t, t + tw, ... up to `last` of an item for a wave's row tiles.  Keys of the next tile are
-  // requested as soon as this one's are used, values likewise: one set of registers
-  // of each, always a request in flight.
-  SVG_DEV static void walk(const Item& it, int t, int tw, int last, const u32x4 (&q)[RT][NC][NQ], Row (&row)[RT], int nrt,
-                           const u32 (&seen)[RT], u32 broken) {
+  // ------------------------------------------------------------------- thin
+  struct Regs {
     u32x4 k[2][NC], v[ND];
-    int page = page_at(it, t);
-    int t2 = t + tw <= last ? t + tw : last, page2 = page_at(it, t2);
-    size_t at = tile_at(it, t, page);
-    load_k(it, at, k);
-    load_v(it, at, v);
-    for (;;) {
-      const int t3 = t2 + tw <= last ? t2 + tw : last, page3 = page_at(it, t3);
-      const bool tree = t * 32 + 32 > it.len;
-      f32x4 s[RT][2];
+  };
+  SVG_DEV static void load_k(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (rt < nrt) {
+    for (int i = 0; i < 2 * NC; ++i) g.k[i / NC][i % NC] = *reinterpret_cast<const u32x4*>(it.k + off + 1024 * i);
+  }
+  SVG_DEV static void load_v(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+    for (int i = 0; i < ND; ++i) g.v[i] = *reinterpret_cast<const u32x4*>(it.v + off + 1024 * i);
+  }
+  // Tile t for all row tiles (nrt of them): it is in g or on its way, and the next one (t2, on `page2`) follows: its keys
+  // are requested as soon as this one's are used, its values likewise: one set of registers of each, always a
+  // request in flight.
+  template <bool TREE>
+  SVG_DEV static void thin_tile(const Item& it, int t, int t2, Regs& g, int page, int page2, const char* ql, Row (&row)[RT], int nrt,
+                                const u32 (&seen)[RT], u32 broken) {
+    asm volatile("" : "+v"(ql));  // q is read again for every tile, not kept
+    f32x4 s[RT][2];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              s[rt][0] = O::mfma(k[0][c], q[rt][c][n], s[rt][0]);
-              s[rt][1] = O::mfma(k[1][c], q[rt][c][n], s[rt][1]);
-            }
-        }
-      }
-      const size_t at2 = tile_at(it, t2, page2);
-      __builtin_amdgcn_sched_barrier(0);  // the next keys take these keys' registers, not others
-      load_k(it, at2, k);
-      if ((u32)page >= (u32)it.n_pages) {
+    for (int rt = 0; rt < RT; ++rt) {
+      s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (rt < nrt) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) row[rt].l = __builtin_nanf("");
-      }
-      bool odd = false;
-      if (tree) odd = clean(it, t, v);
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if (rt < nrt) {
-          u32x4 p[2];
-          soften(it, t, tree, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p);
-          if (odd) gather_odd(v, p, row[rt]);
-          else gather(v, p, row[rt]);
-        }
+          for (int n = 0; n < NQ; ++n) {
+            const u32x4 q = *reinterpret_cast<const u32x4*>(ql + ((rt * NC + c) * NQ + n) * 1024);
+            s[rt][0] = O::mfma(g.k[0][c], q, s[rt][0]);
+            s[rt][1] = O::mfma(g.k[1][c], q, s[rt][1]);
+            if (D == 256) __builtin_amdgcn_sched_barrier(0);
+          }
       }
       __builtin_amdgcn_sched_barrier(0);
-      load_v(it, at2, v);
-      t += tw;
-      if (t > last) break;
+    }
+    const size_t at2 = tile_at(it, t2, page2);
+    __builtin_amdgcn_sched_barrier(0);  // the next keys take these keys' registers, not others
+    load_k(it, at2, g);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (rt < nrt) {
+        if (it.bad(page)) row[rt].l = __builtin_nanf("");
+        u32x4 p[2];
+        soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p);
+        if constexpr (TREE) gather_tree([&](int d) { return g.v[d]; }, token_mask(it, t), p, row[rt]);
+        else gather([&](int d) { return g.v[d]; }, p, row[rt]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    load_v(it, at2, g);
+  }
+  // Tiles t, t + kWaves, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
+  SVG_DEV static void walk_thin(const Item& it, int t, int last, Regs& g, Pages& pages, int page, const char* qs, Row (&row)[RT],
+                                int nrt, const u32 (&seen)[RT], u32 broken) {
+    const char* ql = qs + (threadIdx.x & 63u) * 16u;
+    for (; t <= last && t * 32 + 32 <= it.len; t += kWaves) {
+      const int t2 = t + kWaves <= last ? t + kWaves : last, page2 = pages.at(it, t2);
+      thin_tile<false>(it, t, t2, g, page, page2, ql, row, nrt, seen, broken);
       page = page2;
-      page2 = page3;
-      t2 = t3;
+    }
+    for (; t <= last; t += kWaves) {
+      const int t2 = t + kWaves <= last ? t + kWaves : last, page2 = pages.at(it, t2);
+      thin_tile<true>(it, t, t2, g, page, page2, ql, row, nrt, seen, broken);
+      page = page2;
     }
   }
 
-  // LDS: one buffer of O for each row wave while the token waves are joined.
-  static constexpr int kJoin = 2 * RT * ND * 64;  // float4s
+  // ------------------------------------------------------------------ thick
+  // This wave's share of step i (tiles TW i ..) of a run on its way into the step's place at byte `to` of LDS.  Tiles behind the
+  // last one are the last one again.  Returns bit j for a page number outside the cache at tile j.
+  static constexpr int SHARE = TW * TILE / 1024 / kWaves;
+  SVG_DEV static u32 fetch(const Item& it, Pages& pages, int tile, int last, u32 to, int wave) {
+    u32 bad = 0;
+    size_t off[TW];
+#pragma unroll
+    for (int j = 0; j < TW; ++j) {
+      const int t = tile + j <= last ? tile + j : last, page = pages.at(it, t);
+      if (it.bad(page)) bad |= 1u << j;
+      off[j] = tile_at(it, t, page);
+    }
+#pragma unroll
+    for (int i = 0; i < SHARE; ++i) {
+      constexpr int per = TILE / 1024;
+      const int x = wave * SHARE + i;                 // KiB of the step
+      const int j = TW == 1 ? 0 : x / per, y = x - j * per;  // of tile j: keys, then values
+      const size_t o = off[0] + (TW > 1 && j ? off[TW - 1] - off[0] : 0);
+      load_to_lds(y < 2 * NC ? it.k + o + 1024 * y : it.v + o + 1024 * (y - 2 * NC), to + 1024 * x);
+    }
+    return bad;
+  }
+  // Tile t, whose keys and values begin at kt (this lane's 16 bytes) in LDS, for this wave's row tiles (nrt of them).
+  template <bool TREE>
+  SVG_DEV static void thick_tile(const Item& it, int t, const char* kt, bool bad, const u32x4 (&q)[RT][NC][NQ], Row (&row)[RT],
+                                 const u32 (&seen)[RT], u32 broken) {
+    f32x4 s[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const u32x4 k0 = *reinterpret_cast<const u32x4*>(kt + c * 1024);
+      const u32x4 k1 = *reinterpret_cast<const u32x4*>(kt + (NC + c) * 1024);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          s[rt][0] = O::mfma(k0, q[rt][c][n], s[rt][0]);
+          s[rt][1] = O::mfma(k1, q[rt][c][n], s[rt][1]);
+        }
+      if (D == 256) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (bad) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) row[rt].l = __builtin_nanf("");
+    }
+    const char* vt = kt + 2 * NC * 1024;
+    auto val = [&](int d) { return *reinterpret_cast<const u32x4*>(vt + d * 1024); };
+    u32x4 p[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p[rt]);
+    if constexpr (TREE) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) gather_tree(val, token_mask(it, t), p[rt], row[rt]);
+    } else {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const u32x4 v = val(d);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) row[rt].o[d] = O::mfma(v, p[rt][i], row[rt].o[d]);
+        if (D == 256 && (d & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // Tiles t .. last, of each step the one that is this wave's; the first STEPS - 1 steps are on their way, bad: fetch()'s
+  // answers for them, TW bits a step.  live: the wave has rows.
+  SVG_DEV static void walk_thick(const Item& it, int t, int last, const char* ring, Pages& pages, u32 bad, int wave, bool live,
+                                 const u32x4 (&q)[RT][NC][NQ], Row (&row)[RT], const u32 (&seen)[RT], u32 broken) {
+    const char* mine = ring + wave / RW * TILE + (threadIdx.x & 63u) * 16u;
+    const u32 ring_at = lds_at(ring);
+    const int tw = wave / RW;
+    int here = 0;
+    if (wave < kWaves / 2) __builtin_amdgcn_s_setprio(2);
+    auto next = [&] {
+      const int stale = here == 0 ? STEPS - 1 : here - 1;
+      wait_loads<SHARE * (STEPS - 2)>();  // this wave's share of the step has arrived; after the barrier all of it has,
+      barrier();                          // and nobody reads the place of the step before any more
+      bad |= fetch(it, pages, t + TW * (STEPS - 1), last, ring_at + stale * (TW * TILE), wave) << (TW * (STEPS - 1));
+    };
+    auto done = [&] {
+      t += TW;
+      bad >>= TW;
+      here = here == STEPS - 1 ? 0 : here + 1;
+    };
+    while (t <= last && (t + TW) * 32 <= it.len) {
+      next();
+      if (live && t + tw <= last)
+        thick_tile<false>(it, t + tw, mine + here * (TW * TILE), (bad >> tw) & 1u, q, row, seen, broken);
+      done();
+    }
+    while (t <= last) {
+      next();
+      if (live && t + tw <= last)
+        thick_tile<true>(it, t + tw, mine + here * (TW * TILE), (bad >> tw) & 1u, q, row, seen, broken);
+      done();
+    }
+    __builtin_amdgcn_s_setprio(0);
+    wait_loads<0>();  // what was requested behind the last tile has landed before the ring is anything else
+    barrier();
+  }
+
+  // |q| < 4 in the parts: the exponent of the power of two that a row is divided by (0 and what is not finite: none).
+  SVG_DEV static int exponent_of(float top) {
+    const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
+    return top == 0.f || e == 128 ? 0 : (e > 126 ? 126 : (e < -126 ? -126 : e));
+  }
+  SVG_DEV static float two_to(int e) { return __uint_as_float((u32)(127 + e) << 23); }
+  // Eight values of q times a power of two, in parts.
+  SVG_DEV static void split8(const f32x4 a, const f32x4 b, float by, u32x4 (&q)[NQ]) {
+    u32 w[4][NQ];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      split2<BF, NQ>(a[2 * i] * by, a[2 * i + 1] * by, w[i]);
+      split2<BF, NQ>(b[2 * i] * by, b[2 * i + 1] * by, w[2 + i]);
+    }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) q[n] = u32x4{w[0][n], w[1][n], w[2][n], w[3][n]};
+  }
 };
 
-template <int D, bool BF, int RT>
-__global__ __launch_bounds__(kThreads, (D * RT <= 128 ? 2 : 1)) void k_tree_attention(AttnArgs a) {
+// RTHIN: row tiles of the thin way, 0: the thick way.
+template <int D, bool BF, int RTHIN>
+__global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
+  constexpr bool THIN = RTHIN > 0;
+  constexpr int RT = THIN ? RTHIN : 1;
   using A = Attn<D, BF, RT>;
   constexpr int NC = A::NC, ND = A::ND, NQ = A::NQ;
   __shared__ Plan plan;
-  __shared__ f32x4 join[A::kJoin];
+  __shared__ __attribute__((aligned(1024))) char lds[THIN ? (A::QBYTES > kWaves * A::JOIN ? A::QBYTES : kWaves * A::JOIN) : A::RING];
   __shared__ float stat[kWaves][RT][2][16];
-  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads, RT);
-  make_plan(a, sh, plan);
-  const long wg = blockIdx.x;
-  if (wg >= plan.groups || plan.total == 0) return;
+  __shared__ float factor[RT][16];
+  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads);
+  const Deal deal = make_plan(a, sh, plan);
+  const int wg = blockIdx.x;
+  Span* spans = reinterpret_cast<Span*>(a.ws + sh.spans_at());
+  float* stats = reinterpret_cast<float*>(a.ws + sh.stats_at());
+  float* parts = reinterpret_cast<float*>(a.ws + sh.parts_at());
+  if (wg == 0 && threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = deal.prefix;
+  if (wg >= deal.groups || deal.total == 0) return;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long end = (wg + 1) * plan.total / plan.groups;
-  for (long u = wg * plan.total / plan.groups; u < end;) {
-    // the item at unit u, and the tiles of it that are this workgroup's
-    int s, h, rb, t0, tiles;
-    long place;
-    const bool prefix = u < plan.units_p;
-    if (prefix) {
-      tiles = plan.prefix >> 5;
-      const long j = u / tiles;
-      t0 = (int)(u - j * tiles);
-      rb = (int)(j % sh.rb_p);
-      h = (int)(j / sh.rb_p);
-      s = plan.first;
-      place = sh.slot_p(wg, j);
+  const float sign = a.scale < 0.f ? -1.f : 1.f;
+  const float unit = fabsf(a.scale) * 1.44269504088896341f;
+  const long end = deal.start(wg + 1);
+  long u = deal.start(wg);
+  // the first item: its slot (a prefix item: -1), head, row block and the unit of it that u is
+  int s = -1, h, rb, off;
+  {
+    int j;
+    if (u < deal.units_p) {
+      j = (int)divide(u, (deal.prefix >> 5) + a.item_cost, off);
+      rb = j % sh.rb_p;
+      h = j / sh.rb_p;
     } else {
-      const long per = (long)a.c.heads * sh.rb_s, v = u - plan.units_p;
-      int lo = 0, hi = a.c.n_slots;  // the slot: cum[lo] * per <= v < cum[hi] * per
+      const int per = a.c.heads * sh.rb_s;
+      int rest;
+      const int v = (int)divide(u - deal.units_p, per, rest);
+      int lo = 0, hi = a.c.n_slots;  // cum[lo] <= v < cum[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (plan.cum[mid] * per <= v) lo = mid;
+        if (plan.cum[mid] <= v) lo = mid;
         else hi = mid;
       }
-      s = lo;
-      tiles = (int)(plan.cum[s + 1] - plan.cum[s]);
-      const long rest = v - plan.cum[s] * per, j = rest / tiles;
-      t0 = (int)(rest - j * tiles);
-      rb = (int)(j % sh.rb_s);
-      h = (int)(j / sh.rb_s);
-      place = sh.slot_s(wg, s * per + j);
+      s = __builtin_amdgcn_readfirstlane(lo);
+      j = (int)divide(u - deal.units_p - plan.cum[s] * (long)per, plan.cum[s + 1] - plan.cum[s], off);
+      rb = j % sh.rb_s;
+      h = j / sh.rb_s;
     }
-    s = __builtin_amdgcn_readfirstlane(s);
     h = __builtin_amdgcn_readfirstlane(h);
     rb = __builtin_amdgcn_readfirstlane(rb);
-    t0 = __builtin_amdgcn_readfirstlane(t0);
-    tiles = __builtin_amdgcn_readfirstlane(tiles);
-    const int t1 = __builtin_amdgcn_readfirstlane((int)(t0 + (end - u) < tiles ? t0 + (end - u) : tiles));
-    u += t1 - t0;
+    off = __builtin_amdgcn_readfirstlane(off);
+  }
+  bool more = false;
+  for (; u < end; more = true) {
+    if (more) {  // the next item in order: row blocks, heads, then the next slot that has units
+      off = 0;
+      if (++rb == (s < 0 ? sh.rb_p : sh.rb_s)) {
+        rb = 0;
+        if (++h == a.c.heads) {
+          h = 0;
+          do ++s;
+          while (plan.cum[s + 1] == plan.cum[s]);
+          s = __builtin_amdgcn_readfirstlane(s);
+        }
+      }
+    }
+    const bool prefix = s < 0;
+    const int slot = prefix ? deal.first : s;
+    const int tiles = __builtin_amdgcn_readfirstlane(prefix ? deal.prefix >> 5 : plan.cum[s + 1] - plan.cum[s] - a.item_cost);
+    const int units = tiles + a.item_cost;
+    const long left = end - u;
+    const int stop = left < units - off ? off + (int)left : units;
+    const int t0 = off > a.item_cost ? off - a.item_cost : 0, t1 = stop - a.item_cost;
+    const long base_unit = u - off;
+    u += stop - off;
+    if (t1 <= t0) continue;  // the units of its start only
+    const long j = prefix ? (long)h * sh.rb_p + rb : ((long)s * a.c.heads + h) * sh.rb_s + rb;
+    const long place = prefix ? sh.slot_p(wg, j) : sh.slot_s(wg, j);
+    if (t0 == 0 && threadIdx.x == 0)
+      spans[prefix ? j : sh.items_p + j] = Span{wg, stop == units ? 1 : group_of(base_unit + units - 1, deal) - wg + 1};
 
-    const int nodes = plan.nodes[s];
+    const int nodes = plan.nodes[slot];
     const int block = prefix ? sh.block_p : sh.block_s;
     const int all_rows = prefix ? a.c.n_slots * a.T * a.G : nodes * a.G;
     const int rows = __builtin_amdgcn_readfirstlane(all_rows - rb * block < block ? all_rows - rb * block : block);
     if (rows <= 0) continue;  // a row block behind a small tree's rows
     const int row_tiles = (rows + 15) >> 4;
-    const int rw = row_tiles <= RT ? 1 : (row_tiles <= 2 * RT ? 2 : 4), tw = kWaves / rw;
-    const int my_r = wave % rw, my_t = wave / rw;
-    int nrt = row_tiles - my_r * RT;
-    nrt = nrt < 0 ? 0 : (nrt < RT ? nrt : RT);
 
-    typename A::Item it;
+    Item it;
     const size_t head = (size_t)a.c.page * D * 2;
     it.stride = head * a.c.heads;
-    const size_t base = (size_t)a.layer * a.c.n_pages * it.stride + (size_t)h * head;
-    it.k = static_cast<const char*>(a.c.k) + base + lane * 16;
-    it.v = static_cast<const char*>(a.c.v) + base + lane * 16;
-    const int log_tp = a.c.page == 32 ? 0 : (a.c.page == 64 ? 1 : 2);
-    const int skip = prefix ? 0 : plan.prefix >> 5;  // tiles of the prefix, in front of the slot's own
-    it.table = a.c.table + (size_t)s * a.c.width;
-    it.log_tp = log_tp;
+    const size_t base = (size_t)a.layer * a.c.n_pages * it.stride + (size_t)h * head + lane * 16;
+    it.k = static_cast<const char*>(a.c.k) + base;
+    it.v = static_cast<const char*>(a.c.v) + base;
+    const int skip = prefix ? 0 : deal.prefix >> 5;  // tiles of the prefix, in front of the slot's own
+    it.table = a.c.table + (size_t)slot * a.c.width;
+    it.log_tp = a.c.page == 32 ? 0 : (a.c.page == 64 ? 1 : 2);
     it.n_pages = a.c.n_pages;
-    it.len = prefix ? 0x7FFFFFFF : plan.len[s];
-    it.total = prefix ? 0x7FFFFFFF : plan.len[s] + nodes;
-    it.len = __builtin_amdgcn_readfirstlane(it.len);
-    it.total = __builtin_amdgcn_readfirstlane(it.total);
+    it.len = __builtin_amdgcn_readfirstlane(prefix ? 0x7FFFFFFF : plan.len[slot]);
+    it.total = __builtin_amdgcn_readfirstlane(prefix ? 0x7FFFFFFF : plan.len[slot] + nodes);
+    const int first = t0 + skip, last = t1 - 1 + skip;
 
     // the tree's root paths: lane j < 32 holds node j's, by doubling
     u32 path = 0, broken = 0;
-    if (!prefix && (t1 + skip) * 32l > it.len) {
+    auto root_paths = [&] {
+      if (prefix || (last + 1) * 32l <= it.len) return;
       const int j = lane & 31;
       int up = j - 1;
       if (a.parent != nullptr && j < nodes) up = a.parent[(size_t)s * a.T + j];
@@ -536,203 +828,330 @@ __global__ __launch_bounds__(kThreads, (D * RT <= 128 ? 2 : 1)) void k_tree_atte
         up = __shfl(up, up, 32);
       }
       broken |= (u32)__shfl((int)broken, 0, 32);
-    }
-
-    // the rows: q split into 16-bit parts in the order of the matrix operand
-    u32x4 q[RT][NC][NQ];
-    typename A::Row row[RT];
-    u32 seen[RT], bad = 0;
+    };
+    // q of row idx of the block (its values 8 g .. of every 32), and its node
+    auto node_of = [&](int idx) { return (rb * block + (idx < rows ? idx : 0)) / a.G; };
+    auto q_of = [&](int idx) {
+      const int all = rb * block + (idx < rows ? idx : 0), node = all / a.G;
+      return a.q + ((size_t)(prefix ? 0 : s) * a.T + node) * a.ld_q + (size_t)(h * a.G + all % a.G) * D + 8 * g;
+    };
+    auto at4 = [](const float* p) { return *reinterpret_cast<const f32x4*>(p); };
+    auto top8 = [&](const float* p, float top) {
+      const f32x4 x = at4(p), y = at4(p + 4);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int idx = (my_r * RT + rt) * 16 + n;
-      const bool live = idx < rows;
-      const int all = rb * block + (live ? idx : 0);
-      const int node = all / a.G;  // of the slot, or of all slots
-      const float* qp = a.q + ((size_t)(prefix ? 0 : s) * a.T + node) * a.ld_q + (size_t)(h * a.G + all % a.G) * D + 8 * g;
-      float x[NC][8], top = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(qp + 32 * c), hi = *reinterpret_cast<const f32x4*>(qp + 32 * c + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[c][i] = live ? (i < 4 ? lo[i] : hi[i - 4]) : 0.f;
-          top = fmaxf(top, fabsf(x[c][i]));
-        }
-      }
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(x[i]), fabsf(y[i])));
+      return top;
+    };
+    auto row_max = [](float top) {
       top = fmaxf(top, lane_xorf<16>(top));
-      top = fmaxf(top, lane_xorf<32>(top));
-      // |q| < 2 in the parts; the power of two goes into the factor (0 and what is not finite: none)
-      int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-      if (top == 0.f || e == 128) e = 0;
-      const float down = __uint_as_float((u32)(127 - (e > 126 ? 126 : e)) << 23);
-      const float sign = a.scale < 0.f ? -1.f : 1.f;
+      return fmaxf(top, lane_xorf<32>(top));
+    };
+
+    // The rows' q first, then the first tiles: loads arrive in order, and q is worked on while the tiles come.
+    if constexpr (THIN) {
+      const int mine = first + wave;  // this wave's first tile
+      Pages pages;
+      if (mine <= last) pages.start(it, mine, last);
+      // each wave splits one chunk of 32 values of one row tile
+      const int my_rt = wave / NC, my_c = wave % NC, my_idx = my_rt * 16 + n;
+      const bool splits = wave < RT * NC;
+      f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+      float largest = 0.f;
+      if (splits) {
+        const float* qp = q_of(my_idx);
+        x = at4(qp + 32 * my_c);
+        y = at4(qp + 32 * my_c + 4);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        u32 w[4][NQ];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) split2<BF, NQ>(x[c][2 * i] * down * sign, x[c][2 * i + 1] * down * sign, w[i]);
-#pragma unroll
-        for (int p = 0; p < NQ; ++p) q[rt][c][p] = u32x4{w[0][p], w[1][p], w[2][p], w[3][p]};
+        for (int i = 0; i < NC; ++i) largest = top8(qp + 32 * i, largest);
       }
-      typename A::Row& r = row[rt];
-      r.f = fabsf(a.scale) * 1.44269504088896341f / down;
-      r.m = kLow;
-      r.thr = kLow;
-      r.bias = kLift - kLow * r.f;
-      r.l = 0.f;
-      r.far = 0;
+      typename A::Regs regs;
+      int my_page = 0;
+      if (mine <= last) {
+        my_page = pages.at(it, mine);
+        const size_t at = A::tile_at(it, mine, my_page);
+        A::load_k(it, at, regs);
+        A::load_v(it, at, regs);
+      }
+      root_paths();
+      if (splits) {
+        const int e = A::exponent_of(row_max(largest));
+        u32x4 parts_of[NQ];
+        A::split8(x, y, my_idx < rows ? A::two_to(-e) * sign : 0.f, parts_of);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) r.o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-      seen[rt] = (u32)__shfl((int)path, node & 31);
-      if (__shfl((int)broken, node & 31)) bad |= 1u << rt;
-      __builtin_amdgcn_sched_barrier(0);
-    }
-
-    const int last = t1 - 1 + skip, t = t0 + my_t + skip;
-    if (nrt > 0 && t <= last) A::walk(it, t, tw, last, q, row, nrt, seen, bad);
-
-    // sums over the lanes of a row; maxima in powers of two from here on
-    float top[RT];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      typename A::Row& r = row[rt];
-      r.l += lane_xorf<16>(r.l);
-      r.l += lane_xorf<32>(r.l);
-      top[rt] = r.m = r.top();
-    }
-    // join the token waves of a row wave
-    if (tw > 1) {
-      if (g == 0) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) stat[wave][rt][0][n] = row[rt].m;
+        for (int p = 0; p < NQ; ++p)
+          *reinterpret_cast<u32x4*>(lds + ((my_rt * NC + my_c) * NQ + p) * 1024 + lane * 16) = parts_of[p];
+        if (my_c == 0 && g == 0) factor[my_rt][n] = unit * A::two_to(e);
       }
       __syncthreads();
+      typename A::Row row[RT];
+      u32 seen[RT], bad = 0;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        for (int i = 0; i < tw; ++i) top[rt] = fmaxf(top[rt], stat[i * rw + my_r][rt][0][n]);
-        const float w = __builtin_amdgcn_exp2f(row[rt].m - top[rt]);
-        row[rt].l *= w;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) row[rt].o[d] *= w;
-        if (g == 0) stat[wave][rt][1][n] = row[rt].l;
+        row[rt].start(factor[rt][n]);
+        const int node = node_of(rt * 16 + n) & 31;
+        seen[rt] = (u32)__shfl((int)path, node);
+        if (__shfl((int)broken, node)) bad |= 1u << rt;
       }
-      for (int i = 1; i < tw; ++i) {
-        __syncthreads();
-        if (my_t == i) {
+      if (mine <= last) A::walk_thin(it, mine, last, regs, pages, my_page, lds, row, row_tiles, seen, bad);
+
+      // join the waves: maxima first, then every thread adds the waves' values of its places
+      float top[RT];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+      for (int rt = 0; rt < RT; ++rt) {
+        typename A::Row& r = row[rt];
+        r.l += lane_xorf<16>(r.l);
+        r.l += lane_xorf<32>(r.l);
+        top[rt] = r.top();
+        if (g == 0) stat[wave][rt][0][n] = top[rt];
+      }
+      __syncthreads();
+      f32x4* join = reinterpret_cast<f32x4*>(lds);  // q is not needed any more
 #pragma unroll
-            for (int d = 0; d < ND; ++d) join[((my_r * RT + rt) * ND + d) * 64 + lane] = row[rt].o[d];
+      for (int rt = 0; rt < RT; ++rt) {
+        if (rt < row_tiles) {
+          typename A::Row& r = row[rt];
+          const float own = top[rt];
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) top[rt] = fmaxf(top[rt], stat[w][rt][0][n]);
+          const float w = __builtin_amdgcn_exp2f(own - top[rt]);
+          if (g == 0) stat[wave][rt][1][n] = r.l * w;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) join[((wave * RT + rt) * ND + d) * 64 + lane] = r.o[d] * w;
         }
-        __syncthreads();
-        if (my_t == 0) {
+      }
+      __syncthreads();
+      for (int x = wave; x < row_tiles * ND; x += kWaves) {  // the wave's lanes: 16 columns of a row tile
+        const int rt = x / ND, d = x - rt * ND, idx = rt * 16 + n;
+        f32x4 o = join[x * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) o += join[(w * RT * ND + x) * 64 + lane];
+        if (idx < rows) {
+          *reinterpret_cast<f32x4*>(parts + (size_t)(place + idx) * D + 16 * d + 4 * g) = o;
+          if (d == 0 && g == 0) {
+            float l = 0.f, t = kLow;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+              l += stat[w][rt][1][n];
+              t = fmaxf(t, stat[w][rt][0][n]);
+            }
+            stats[2 * (place + idx)] = t;
+            stats[2 * (place + idx) + 1] = l;
+          }
+        }
+      }
+      __syncthreads();  // LDS is free again
+    } else {
+      // row tiles of this wave: as even shares as they make
+      const int each = (row_tiles + A::RW - 1) / A::RW, rw = wave % A::RW, rt0 = rw * each;
+      int nrt = row_tiles - rt0;
+      nrt = nrt < 0 ? 0 : (nrt < each ? nrt : each);
+      Pages pages;
+      pages.start(it, first, last);
+      u32x4 q[RT][NC][NQ];
+      typename A::Row row[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int idx = (rt0 + rt) * 16 + n;
+        if (rt < nrt) {
+          const float* qp = q_of(idx);
+          float top = 0.f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) top = top8(qp + 32 * c, top);
+          const int e = A::exponent_of(row_max(top));
+          const float by = idx < rows ? A::two_to(-e) * sign : 0.f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) A::split8(at4(qp + 32 * c), at4(qp + 32 * c + 4), by, q[rt][c]);
+          row[rt].start(unit * A::two_to(e));
+        } else {
+          row[rt].start(0.f);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int p = 0; p < NQ; ++p) q[rt][c][p] = u32x4{0, 0, 0, 0};
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      u32 outside = 0;
+#pragma unroll
+      for (int i = 0; i < A::STEPS - 1; ++i)
+        outside |= A::fetch(it, pages, first + i * A::TW, last, lds_at(lds) + i * (A::TW * A::TILE), wave) << (A::TW * i);
+      root_paths();
+      u32 seen[RT], bad = 0;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int node = node_of((rt0 + rt) * 16 + n) & 31;
+        seen[rt] = (u32)__shfl((int)path, node);
+        if (__shfl((int)broken, node)) bad |= 1u << rt;
+      }
+      A::walk_thick(it, first, last, lds, pages, outside, wave, nrt > 0, q, row, seen, bad);
+
+      // join the token waves, then write
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        row[rt].l += lane_xorf<16>(row[rt].l);
+        row[rt].l += lane_xorf<32>(row[rt].l);
+      }
+      f32x4* join = reinterpret_cast<f32x4*>(lds);
+      if constexpr (A::TW > 1) {
+        if (wave >= A::RW) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            row[rt].l += stat[i * rw + my_r][rt][1][n];
+            if (g == 0) {
+              stat[rw][rt][0][n] = row[rt].top();
+              stat[rw][rt][1][n] = row[rt].l;
+            }
 #pragma unroll
-            for (int d = 0; d < ND; ++d) row[rt].o[d] += join[((my_r * RT + rt) * ND + d) * 64 + lane];
+            for (int d = 0; d < ND; ++d) join[((rw * RT + rt) * ND + d) * 64 + lane] = row[rt].o[d];
+          }
+        }
+        __syncthreads();
+      }
+      if (wave < A::RW) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int idx = (rt0 + rt) * 16 + n;
+          float top = row[rt].top(), l = row[rt].l, w0 = 1.f, w1 = 0.f;
+          if constexpr (A::TW > 1) {
+            const float own = top, other = stat[rw][rt][0][n];
+            top = fmaxf(own, other);
+            w0 = __builtin_amdgcn_exp2f(own - top);
+            w1 = __builtin_amdgcn_exp2f(other - top);
+            l = l * w0 + stat[rw][rt][1][n] * w1;
+          }
+          if (rt < nrt && idx < rows) {
+            float* po = parts + (size_t)(place + idx) * D + 4 * g;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              f32x4 o = row[rt].o[d];
+              if constexpr (A::TW > 1) o = o * w0 + join[((rw * RT + rt) * ND + d) * 64 + lane] * w1;
+              *reinterpret_cast<f32x4*>(po + 16 * d) = o;
+            }
+            if (g == 0) {
+              stats[2 * (place + idx)] = top;
+              stats[2 * (place + idx) + 1] = l;
+            }
           }
         }
       }
-      __syncthreads();  // stat and join are free again
-    }
-    if (my_t == 0) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int idx = (my_r * RT + rt) * 16 + n;
-        if (idx < rows) {
-          float* po = a.part + 2 * sh.rows() + (size_t)(place + idx) * D + 4 * g;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(po + 16 * d) = row[rt].o[d];
-          if (g == 0) {
-            float* ps = a.part + 2 * (size_t)(place + idx);
-            ps[0] = top[rt];
-            ps[1] = row[rt].l;
-          }
-        }
-      }
+      __syncthreads();  // LDS is free again
     }
   }
 }
 
-// The workgroup that holds unit u of `total` dealt over `groups`.
-SVG_DEV long group_of(long u, long total, int groups) { return ((u + 1) * groups - 1) / total; }
+// One wave per output row (slot, node, query head) joins its partials, in the order of the workgroups: D / 4 lanes
+// read one partial's O, the wave 256 / D of them at a time.
+constexpr int kJoinThreads = 256;
 
-// One wave per output row (slot, node, query head): its partials, joined in the
-// order of the workgroups.
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_tree_attention_join(AttnArgs a, int rt) {
-  __shared__ Plan plan;
-  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads, rt);
-  make_plan(a, sh, plan);
-  constexpr int E = D / 64;
+__global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a) {
+  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads);
+  constexpr int L = D / 4, NP = 64 / L;  // lanes of a partial, partials at a time
   const int lane = threadIdx.x & 63;
   const int heads = a.c.heads * a.G;
-  const long x = (long)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const long x = (long)blockIdx.x * (kJoinThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (x >= (long)a.c.n_slots * a.T * heads) return;
   const int head = (int)(x % heads), i = (int)(x / heads) % a.T, s = (int)(x / heads / a.T);
-  if (i >= plan.nodes[s]) return;  // no such node: the row stays as it was
-  float* out = a.out + x * D + lane * E;
   const int h = head / a.G, gq = head % a.G;
-  if (plan.len[s] < 0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = __builtin_nanf("");
+  const Span* spans = reinterpret_cast<const Span*>(a.ws + sh.spans_at());
+  const float* stats = reinterpret_cast<const float*>(a.ws + sh.stats_at());
+  const float* parts = reinterpret_cast<const float*>(a.ws + sh.parts_at());
+  const long r_p = ((long)s * a.T + i) * a.G + gq, j_p = (long)h * sh.rb_p + r_p / sh.block_p;
+  const long r_s = (long)i * a.G + gq, j_s = ((long)s * a.c.heads + h) * sh.rb_s + r_s / sh.block_s;
+  const int nodes = node_count(a, s), len = valid_len(a, s, nodes);
+  const int prefix = *reinterpret_cast<const int*>(a.ws);
+  const Span sp = spans[j_p], ss = spans[sh.items_p + j_s];
+  if (i >= nodes) return;  // no such node: the row stays as it was
+  float* out = a.out + x * D + 4 * (lane % L);
+  if (len < 0) {
+    const float nan = __builtin_nanf("");
+    if (lane < L) *reinterpret_cast<f32x4*>(out) = f32x4{nan, nan, nan, nan};
     return;
   }
-  float m = kLow, l = 0.f, o[E];
+  const int np = prefix > 0 ? sp.count : 0, all = np + ss.count;
+  const long at_p = sh.slot_p(sp.first, j_p) + r_p % sh.block_p, at_s = sh.slot_s(ss.first, j_s) + r_s % sh.block_s;
+  auto row_of = [&](int k) { return k < np ? at_p + (long)k * sh.block_p : at_s + (long)(k - np) * sh.block_s; };
+  float m = kLow, l = 0.f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  constexpr int U = 8;  // requests in flight a lane
+  for (int k0 = lane / L; k0 < all; k0 += NP * U) {
+    float pm[U], pl[U];
+    f32x4 po[U];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const float* stats = a.part;
-  const float* parts = a.part + 2 * sh.rows();
-  auto take = [&](long row) {
-    const float pm = stats[2 * row], pl = stats[2 * row + 1];
-    const float top = fmaxf(m, pm);
-    const float w0 = __builtin_amdgcn_exp2f(m - top), w1 = __builtin_amdgcn_exp2f(pm - top);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * NP;
+      const long row = row_of(k < all ? k : k0);
+      pm[u] = stats[2 * row];
+      pl[u] = stats[2 * row + 1];
+      po[u] = *reinterpret_cast<const f32x4*>(parts + row * D + 4 * (lane % L));
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (k0 + u * NP >= all) { pm[u] = kLow; pl[u] = 0.f; po[u] = f32x4{0.f, 0.f, 0.f, 0.f}; }
+      top = fmaxf(top, pm[u]);
+    }
+    const float w0 = __builtin_amdgcn_exp2f(m - top);
+    l *= w0;
+    o *= w0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float w = __builtin_amdgcn_exp2f(pm[u] - top);
+      l += pl[u] * w;
+      o += po[u] * w;
+    }
     m = top;
-    l = l * w0 + pl * w1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * w0 + parts[row * D + lane * E + e] * w1;
-  };
-  if (plan.prefix > 0) {
-    const long r = ((long)s * a.T + i) * a.G + gq;
-    const long tiles = plan.prefix >> 5, j = (long)h * sh.rb_p + r / sh.block_p;
-    const long w1 = group_of((j + 1) * tiles - 1, plan.total, plan.groups);
-    for (long w = group_of(j * tiles, plan.total, plan.groups); w <= w1; ++w) take(sh.slot_p(w, j) + r % sh.block_p);
   }
-  const long r = (long)i * a.G + gq, tiles = plan.cum[s + 1] - plan.cum[s], per = (long)a.c.heads * sh.rb_s;
-  const long jj = (long)h * sh.rb_s + r / sh.block_s, u = plan.units_p + plan.cum[s] * per + jj * tiles;
-  const long w1 = group_of(u + tiles - 1, plan.total, plan.groups);
-  for (long w = group_of(u, plan.total, plan.groups); w <= w1; ++w) take(sh.slot_s(w, s * per + jj) + r % sh.block_s);
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = o[e] / l;
+  for (int off = L; off < 64; off <<= 1) {
+    const float m2 = __shfl_xor(m, off), l2 = __shfl_xor(l, off), top = fmaxf(m, m2);
+    const float w1 = __builtin_amdgcn_exp2f(m - top), w2 = __builtin_amdgcn_exp2f(m2 - top);
+    l = l * w1 + l2 * w2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = o[e] * w1 + __shfl_xor(o[e], off) * w2;
+    m = top;
+  }
+  if (lane < L) *reinterpret_cast<f32x4*>(out) = o / l;
 }
 
-// Row tiles of a wave: two where an item has more than one and the registers hold them (dim 256: one).
-int row_tiles(const svg_kv_cache& c, int T, int G) { return c.dim < 256 && (long)c.n_slots * T * G > 16 ? 2 : 1; }
+template <int D, bool BF>
+void launch_items(AttnArgs a, int kinds, long rows, hipStream_t stream) {
+  a.kinds = kinds;
+  const bool thin = rows <= 16 * kThinTiles<D>;
+  a.min_units = thin ? kMinThin : kMinThick;
+  a.item_cost = thin ? kItemThin : kItemThick;
+  const dim3 grid(a.groups), threads(kThreads);
+  if (rows <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1>), grid, threads, 0, stream, a);
+  else if (thin) hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((k_tree_attention<D, BF, 0>), grid, threads, 0, stream, a);
+}
 
 template <int D, bool BF>
 void launch(const AttnArgs& a, hipStream_t stream) {
-  const int rt = row_tiles(a.c, a.T, a.G);
-  if (D < 256 && rt == 2) hipLaunchKernelGGL((k_tree_attention<D, BF, (D < 256 ? 2 : 1)>), dim3(a.groups), dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((k_tree_attention<D, BF, 1>), dim3(a.groups), dim3(kThreads), 0, stream, a);
+  // the shared prefix and the slots' own tokens: one launch where both are walked the same way
+  const long rows_s = (long)a.T * a.G, rows_p = a.shared != nullptr ? a.c.n_slots * rows_s : rows_s;
+  if (rows_s <= 16 * kThinTiles<D> && rows_p > 16 * kThinTiles<D>) {
+    launch_items<D, BF>(a, kPrefix, rows_p, stream);
+    launch_items<D, BF>(a, kSlots, rows_s, stream);
+  } else {
+    launch_items<D, BF>(a, kPrefix | kSlots, rows_p, stream);
+  }
   const long rows = (long)a.c.n_slots * a.T * a.c.heads * a.G;
-  hipLaunchKernelGGL((k_tree_attention_join<D>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream, a,
-                     rt);
+  constexpr int per = kJoinThreads / 64;
+  hipLaunchKernelGGL((k_tree_attention_join<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
 
 uint64_t svg_tree_attention_bytes(const svg_kv_cache& c, int T, int G) {
-  const Shape sh(c.n_slots, T, G, c.heads, row_tiles(c, T, G));
-  return (uint64_t)sh.rows() * (c.dim + 2) * 4;
+  return Shape(c.n_slots, T, G, c.heads).bytes(c.dim);
 }
 
 hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const float* q, int64_t ld_q, int G,
                                      const int32_t* parent, int T, const int32_t* n_nodes, const int32_t* shared,
                                      float scale, float* out, void* workspace, hipStream_t stream) {
   const int cus = svg_cu_count();
-  const AttnArgs a{c, q, parent, n_nodes, shared, out, static_cast<float*>(workspace), (long)ld_q, layer, T, G,
-                   cus < kMaxGroups ? cus : kMaxGroups, scale};
+  const AttnArgs a{c, q, parent, n_nodes, shared, out, static_cast<char*>(workspace), (long)ld_q, layer, T, G,
+                   cus < kMaxGroups ? cus : kMaxGroups, 0, 0, 0, scale};
   const bool bf = c.type == SVG_BF16;
   if (c.dim == 64) {
     if (bf) launch<64, true>(a, stream);
