@@ -200,8 +200,8 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *  NaN rows: a node whose root path breaks the rule above; a row that reads a page number outside the cache; all of a
  *  slot whose pages do not cover len + n_nodes.
  *  Reads table, pages, len.  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the
- *  cache or a scale that is not finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads
- *  or ld_q; SVG_EALIGN.
+ *  cache or a scale that is not finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads,
+ *  ld_q, or a table so large that n_slots * width * page * heads times the blocks of 128 rows of an item nears 2^36; SVG_EALIGN.
  *
  * tree_attention_workspace -- the bytes of that workspace (host only).
  */

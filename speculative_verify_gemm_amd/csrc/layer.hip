@@ -136,6 +136,8 @@ static svg_status check_heads(const char* fn, const svg_kv_cache* c, int q_heads
   if (T > SVG_TREE_MAX_NODES) return svg_fail(SVG_EUNSUPPORTED, fn, "T > SVG_TREE_MAX_NODES");
   if (q_heads % c->heads || q_heads > 4096)
     return svg_fail(SVG_EUNSUPPORTED, fn, "q_heads must be a multiple of the cache's heads, at most 4096");
+  if (c->n_slots && !svg_tree_attention_fits(*c, T, q_heads / c->heads))
+    return svg_fail(SVG_EUNSUPPORTED, fn, "too much work for one call: n_slots * width * page * heads * row blocks of 128 past 2^36");
   return SVG_OK;
 }
 

@@ -80,7 +80,9 @@ hipError_t svg_launch_kv_copy(const svg_kv_cache& c, const int32_t* src, const i
                               hipStream_t stream);
 
 // Attention over the paged cache (tree_attention.hip); G query heads share a
-// key/value head.  bytes: the workspace.
+// key/value head.  fits: whether the work of the largest lengths can be counted
+// in 31 bits; bytes: the workspace.
+bool svg_tree_attention_fits(const svg_kv_cache& c, int T, int G);
 uint64_t svg_tree_attention_bytes(const svg_kv_cache& c, int T, int G);
 hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const float* q, int64_t ld_q, int G,
                                      const int32_t* parent, int T, const int32_t* n_nodes, const int32_t* shared,

@@ -52,17 +52,49 @@ constexpr int kThreads = 512, kWaves = 8;
 constexpr int kMaxGroups = SVG_ATTN_MAX_GROUPS;
 constexpr int kMaxSlots = 1024;
 constexpr float kLift = 9.f, kSlack = 6.f;
-constexpr float kLow = -1e30f;  // below every score: no token seen yet
+constexpr float kLow = -3e38f;       // the maximum before any token
+constexpr float kLowest = -3.402823466e38f;
 // A probability is 2^(f s + bias), bias = kLift - f m: one operation, off by half a step of f m.  Beyond
 // kFar that step would be felt as a factor, and far beyond it would overflow: 2^(f (s - m) + kLift) then.
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
 // takes.  A workgroup gets kMinThin / kMinThick units at least.
-constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 16, kMinThick = 6;
+constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 12, kMinThick = 6;
 
 // Row tiles of an item that is walked the thin way.
 template <int D>
 constexpr int kThinTiles = D < 256 ? 2 : 1;  // (dim 256: the accumulators of two do not fit)
+
+// What the second launch has to know of an item: the workgroups that wrote partials of it.
+struct Span {
+  int first, count;
+};
+
+// Rows of an item block and the workspace's parts: a header (the prefix that was used), a Span for each item, (M, sum) and
+// O of every row of partials.
+constexpr int kBlock = 16 * kWaves;  // rows of an item at most
+struct Shape {
+  int block_p, block_s;     // rows of a prefix item, of a slot item: kBlock where there are several row blocks
+  int rb_p, rb_s;           // row blocks
+  int items_p, items_s;
+  Shape(int S, int T, int G, int heads) {
+    const int rows_p = S * T * G, rows_s = T * G;
+    block_p = rows_p < kBlock ? (rows_p + 15) / 16 * 16 : kBlock;
+    block_s = rows_s < kBlock ? (rows_s + 15) / 16 * 16 : kBlock;
+    rb_p = (rows_p + block_p - 1) / block_p;
+    rb_s = (rows_s + block_s - 1) / block_s;
+    items_p = heads * rb_p;
+    items_s = heads * rb_s * S;
+  }
+  // first row of partials of workgroup w in item j (prefix items, then slot items): either number rising by one
+  // is another place, and the pairs that occur rise in both
+  __host__ __device__ long slot_p(int w, int j) const { return (long)(w + j) * block_p; }
+  __host__ __device__ long slot_s(int w, int j) const { return (long)(kMaxGroups + items_p) * block_p + (long)(w + j) * block_s; }
+  long rows() const { return (long)(kMaxGroups + items_p) * block_p + (long)(kMaxGroups + items_s) * block_s; }
+  size_t stats_at() const { return (256 + (size_t)(items_p + items_s) * sizeof(Span) + 255) / 256 * 256; }
+  size_t parts_at() const { return (stats_at() + (size_t)rows() * 8 + 255) / 256 * 256; }
+  size_t bytes(int dim) const { return parts_at() + (size_t)rows() * dim * 4; }
+};
 
 enum { kPrefix = 1, kSlots = 2 };
 
@@ -73,48 +105,24 @@ struct AttnArgs {
   const int32_t* n_nodes;
   const int32_t* shared;
   float* out;
-  char* ws;           // see Shape
+  int* header;        // the workspace, see Shape
+  Span* spans;
+  float* stats;
+  float* parts;
   long ld_q;
   int layer, T, G, groups;
   int min_units, item_cost;
   int kinds;          // items of this launch: kPrefix, kSlots
+  u32 over_g;         // 2^32 / G, rounded up (0: G = 1)
+  Shape sh;
   float scale;
-};
 
-// What the second launch has to know of an item: the workgroups that wrote partials of it.
-struct Span {
-  int first, count;
-};
-
-// Rows of an item block and the workspace's parts, the same on host and device:
-// a header (the prefix that was used), a Span for each item, (M, sum) and O of every row of partials.
-struct Shape {
-  int block_p, block_s;   // rows of a prefix item, of a slot item
-  int rb_p, rb_s;         // row blocks
-  long items_p, items_s;
-  __host__ __device__ Shape(int S, int T, int G, int heads) {
-    const int most = 16 * kWaves;
-    const long rows_p = (long)S * T * G, rows_s = (long)T * G;
-    block_p = (int)(rows_p < most ? (rows_p + 15) / 16 * 16 : most);
-    block_s = (int)(rows_s < most ? (rows_s + 15) / 16 * 16 : most);
-    rb_p = (int)((rows_p + block_p - 1) / block_p);
-    rb_s = (int)((rows_s + block_s - 1) / block_s);
-    items_p = (long)heads * rb_p;
-    items_s = (long)heads * rb_s * S;
+  // row / G
+  SVG_DEV int node_of(int row) const {
+    if (over_g == 0) return row;
+    const int n = (int)__umulhi((u32)row, over_g);  // the quotient or one more
+    return n * G > row ? n - 1 : n;
   }
-  // first row of partials of workgroup w in item j (prefix items, then slot items): either number rising by one
-  // is another place, and the pairs that occur rise in both
-  __host__ __device__ long slot_p(long w, long j) const { return (w + j) * block_p; }
-  __host__ __device__ long slot_s(long w, long j) const {
-    return (long)(kMaxGroups + items_p) * block_p + (w + j) * block_s;
-  }
-  __host__ __device__ long rows() const {
-    return (long)(kMaxGroups + items_p) * block_p + (long)(kMaxGroups + items_s) * block_s;
-  }
-  __host__ __device__ size_t spans_at() const { return 256; }
-  __host__ __device__ size_t stats_at() const { return (spans_at() + (size_t)(items_p + items_s) * sizeof(Span) + 255) / 256 * 256; }
-  __host__ __device__ size_t parts_at() const { return (stats_at() + (size_t)rows() * 8 + 255) / 256 * 256; }
-  __host__ __device__ size_t bytes(int dim) const { return parts_at() + (size_t)rows() * dim * 4; }
 };
 
 // How the launch's work is dealt out; the same in every workgroup.
@@ -124,14 +132,13 @@ struct Plan {
   int nodes[kMaxSlots];
   int red[4][kWaves];
 };
-// The part of it that every wave keeps in scalar registers.
+// The part of it that every wave keeps in scalar registers.  (Units are below 2^31: the host has seen to that.)
 struct Deal {
   int prefix, first;        // shared tokens (a multiple of 32), a slot whose row names their pages
-  long total, units_p;      // units of the launch, of the prefix items
-  int groups;               // workgroups that take part: w has the units from start(w) on
-  long quot;                // total / groups, and the rest
-  int rest;
-  SVG_DEV long start(int w) const { return w * quot + (u32)(w * rest) / (u32)groups; }
+  u32 total, units_p;       // units of the launch, of the prefix items
+  u32 groups;               // workgroups that take part: w has the units from start(w) on
+  u32 quot, rest;           // total / groups
+  SVG_DEV u32 start(u32 w) const { return w * quot + w * rest / groups; }
 };
 
 SVG_DEV int node_count(const AttnArgs& a, int s) {
@@ -145,23 +152,7 @@ SVG_DEV int valid_len(const AttnArgs& a, int s, int nodes) {
   return len < 0 || held < 0 || held > a.c.width || (long)len + nodes > (long)held * a.c.page ? -1 : len;
 }
 
-// u / d and the rest, 0 <= u < 2^48: the estimate is off by one at most.
-SVG_DEV long divide(long u, int d, int& rest) {
-  const double y = (double)d;
-  double x = __builtin_amdgcn_rcp(y);
-  x = __builtin_fma(__builtin_fma(-y, x, 1.0), x, x);
-  x = __builtin_fma(__builtin_fma(-y, x, 1.0), x, x);
-  long q = (long)((double)u * x);
-  long r = u - q * d;
-  if (r < 0) { --q; r += d; }
-  if (r >= d) { ++q; r -= d; }
-  rest = (int)r;
-  return q;
-}
-SVG_DEV long uniform(long v) {
-  return (long)(((unsigned long)(u32)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
-                (u32)__builtin_amdgcn_readfirstlane((int)v));
-}
+SVG_DEV u32 uniform(u32 v) { return (u32)__builtin_amdgcn_readfirstlane((int)v); }
 
 // Minimum and sum over the wave, the same in every lane; the sum of the lanes up to this one.
 template <int CTRL>
@@ -187,7 +178,7 @@ SVG_DEV int wave_scan(int v) {
   return v + (lane < 16 ? 0 : (lane < 32 ? a : (lane < 48 ? b : c)));
 }
 
-SVG_DEV Deal make_plan(const AttnArgs& a, const Shape& sh, Plan& p) {
+SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
   const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int said = a.shared != nullptr ? a.shared[0] : 0;
   // a slot with nodes whose tokens lie inside its pages is active; the others take no part.  Two slots a thread
@@ -250,25 +241,23 @@ SVG_DEV Deal make_plan(const AttnArgs& a, const Shape& sh, Plan& p) {
   if (2 * tid < S) p.cum[2 * tid] = before;
   if (2 * tid + 1 < S) p.cum[2 * tid + 1] = before + t0;
   if (tid == 0) p.cum[S] = all;
-  d.units_p = (a.kinds & kPrefix) && d.prefix > 0 ? sh.items_p * ((d.prefix >> 5) + a.item_cost) : 0;
-  d.total = uniform(d.units_p + (a.kinds & kSlots ? all * (long)a.c.heads * sh.rb_s : 0));
-  int left;
-  const long want = divide(d.total + a.min_units - 1, a.min_units, left);
-  d.groups = __builtin_amdgcn_readfirstlane(want < 1 ? 1 : (want < a.groups ? (int)want : a.groups));
-  d.quot = uniform(divide(d.total, d.groups, left));
-  d.rest = __builtin_amdgcn_readfirstlane(left);
+  d.units_p = (a.kinds & kPrefix) && d.prefix > 0 ? (u32)(a.sh.items_p * ((d.prefix >> 5) + a.item_cost)) : 0u;
+  d.total = uniform(d.units_p + (a.kinds & kSlots ? (u32)(all * a.c.heads * a.sh.rb_s) : 0u));
+  const u32 want = (d.total + a.min_units - 1) / (u32)a.min_units;
+  d.groups = uniform(want < 1 ? 1 : (want < (u32)a.groups ? want : (u32)a.groups));
+  d.quot = uniform(d.total / d.groups);
+  d.rest = d.total - d.quot * d.groups;
   __syncthreads();
   return d;
 }
 static_assert(2 * kThreads >= kMaxSlots, "two slots a thread");
 
-// The workgroup that holds unit u (an estimate, put right: it is off by one at most).
-SVG_DEV int group_of(long u, const Deal& p) {
-  int w = (int)((double)u * __builtin_amdgcn_rcp((double)p.total) * p.groups);
+// The workgroup that holds unit u: an estimate that is not below it (and at most a few above), put right.
+SVG_DEV int group_of(u32 u, const Deal& p) {
+  u32 w = (u32)((float)u * __builtin_amdgcn_rcpf((float)p.total) * (float)p.groups) + 2u;
   w = w < p.groups ? w : p.groups - 1;
   while (p.start(w) > u) --w;
-  while (w + 1 < p.groups && p.start(w + 1) <= u) ++w;
-  return w;
+  return (int)w;
 }
 
 // ------------------------------------------------------------ 16-bit operands
@@ -296,6 +285,24 @@ struct Ops<true> {
   static constexpr u32 kOne = 0x3F80u;
 };
 
+// Two probabilities in two parts, packed: fp16 parts are cut off (what the first leaves, the second takes; the rest
+// is below 2^-21), bf16 parts are rounded.
+template <bool BF>
+SVG_DEV void split_pair(float x, float y, u32& hi, u32& lo) {
+  if constexpr (BF) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    hi = __builtin_bit_cast(u32, __builtin_convertvector(f32x2{x, y}, bf16x2));
+    lo = __builtin_bit_cast(u32, __builtin_convertvector(
+                                     f32x2{x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u)}, bf16x2));
+  } else {
+    typedef __fp16 f16x2 __attribute__((ext_vector_type(2)));
+    const f16x2 h = __builtin_amdgcn_cvt_pkrtz(x, y);
+    hi = __builtin_bit_cast(u32, h);
+    lo = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)h[0], -1.f, x), __builtin_fmaf((float)h[1], -1.f, y)));
+  }
+}
+
 // A pair of fp32 values split into N 16-bit parts each (part n: the rounding of what the parts
 // before left over), packed two to a word.
 template <bool BF, int N>
@@ -322,17 +329,18 @@ SVG_DEV void barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
-// 1 KiB from global memory (16 bytes a lane) straight into LDS at byte `to` (the same for the wave).  In asm: the compiler
-// would wait for all of them before it reads any LDS; here wait_loads() and the barrier say what has arrived.
-SVG_DEV void load_to_lds(const char* from, u32 to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(from) : "memory");
+// 1 KiB from global memory at `from` (lane16: this lane's 16 bytes) straight into LDS at byte `to`; both the same for the
+// wave.  In asm: the compiler would wait for all of them before it reads any LDS; here wait_loads() and the
+// barrier say what has arrived.
+SVG_DEV void load_to_lds(const char* from, u32 lane16, u32 to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane16), "s"(from) : "memory");
 }
 // Bytes of LDS before p.
 SVG_DEV u32 lds_at(const char* p) { return (u32)(uintptr_t)(const __attribute__((address_space(3))) char*)p; }
 
 // This item: one head of one layer, the pages of one table row.
 struct Item {
-  const char *k, *v;         // page 0 of the head, this lane's 16 bytes
+  const char *k, *v;         // page 0 of the head
   const int32_t* table;
   size_t stride;             // bytes of a page of all heads
   int log_tp;                // log2(tiles of a page)
@@ -370,20 +378,18 @@ struct Attn {
   static constexpr int QBYTES = RT * NC * NQ * 1024;  // thin: q's parts in LDS
   static constexpr int JOIN = RT * ND * 1024;         // O of a wave in LDS
   // thick: TW waves for each share of the rows, tiles of a step; RW shares of RT row tiles; STEPS steps in LDS
-  static constexpr int TW = 1, RW = kWaves / TW, STEPS = D < 256 ? 4 : 3;
+  static constexpr int TW = D < 256 ? 2 : 1, RW = kWaves / TW, STEPS = 3;
   static constexpr int RING = STEPS * TW * TILE;
   static_assert(RT * NC <= kWaves, "a wave splits one chunk of q");
   static_assert(RW * JOIN <= RING || TW == 1, "the join of the token waves takes the ring's place");
 
   struct Row {                 // per lane: row n = lane % 16 of a row tile
     f32x4 o[ND];
-    float m, thr, bias, l, f;  // maximum (in units of q . k), when to raise it, exponent's offset, sum, factor
-    float slack;               // kSlack in units of q . k
+    float m, bias, l, f;       // maximum (in units of q . k), exponent's offset, sum, factor
     int far;                   // (the same for the wave) maxima beyond kFar: the offset is not used
     SVG_DEV void start(float factor) {
       f = factor;
-      slack = kSlack * __builtin_amdgcn_rcpf(f);
-      m = thr = kLow;
+      m = kLow;
       bias = kLift - kLow * f;
       l = 0.f;
       far = 0;
@@ -391,7 +397,7 @@ struct Attn {
       for (int d = 0; d < ND; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // the maximum in powers of two that o and l are relative to
-    SVG_DEV float top() const { return m == kLow ? kLow : (far ? m * f : kLift - bias); }
+    SVG_DEV float top() const { return fmaxf(far ? m * f : kLift - bias, kLowest); }
   };
 
   // Bytes before a tile's keys (and values); a page number outside the cache gives page 0 (and NaN rows).
@@ -407,9 +413,8 @@ struct Attn {
     const float m = fmaxf(r.m, top);
     const float bias = kLift - m * r.f;
     r.far = __any(fabsf(bias) > kFar);
-    const float w = __builtin_amdgcn_exp2f(r.far ? (r.m - m) * r.f : bias - r.bias);
+    const float w = m == r.m ? 1.f : __builtin_amdgcn_exp2f(r.far ? (r.m - m) * r.f : bias - r.bias);
     r.m = m;
-    r.thr = m + r.slack;
     r.bias = bias;
     r.l *= w;
 #pragma unroll
@@ -436,13 +441,29 @@ struct Attn {
         }
       }
     }
-    const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    if (__any(top > r.thr)) raise(r, top);
-    const float less = r.far ? r.m : 0.f, more = r.far ? kLift : r.bias;
+    // exponents; if one passes the slack the maximum is raised, and they are taken again
+    float y[8];
+    auto exponents = [&] {
+      float more = r.bias;
+      if (r.far) {
+        more = kLift;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __builtin_fmaf(x[j] - less, r.f, more);
+        for (int j = 0; j < 8; ++j) y[j] = x[j] - r.m;
+      } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(x[j]);
+        for (int j = 0; j < 8; ++j) y[j] = x[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __builtin_fmaf(y[j], r.f, more);
+    };
+    exponents();
+    const float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+    if (__any(top > kLift + kSlack)) {
+      raise(r, fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))));
+      exponents();
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __builtin_amdgcn_exp2f(y[j]);
     if constexpr (TREE) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -453,10 +474,10 @@ struct Attn {
     r.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      u32 h[2];
-      split2<BF, 2>(x[2 * w], x[2 * w + 1], h);
-      p[0][w] = h[0];
-      p[1][w] = h[1];
+      u32 hi, lo;
+      split_pair<BF>(x[2 * w], x[2 * w + 1], hi, lo);
+      p[0][w] = hi;
+      p[1][w] = lo;
     }
   }
 
@@ -523,11 +544,11 @@ struct Attn {
   };
   SVG_DEV static void load_k(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-    for (int i = 0; i < 2 * NC; ++i) g.k[i / NC][i % NC] = *reinterpret_cast<const u32x4*>(it.k + off + 1024 * i);
+    for (int i = 0; i < 2 * NC; ++i) g.k[i / NC][i % NC] = *reinterpret_cast<const u32x4*>(it.k + off + (threadIdx.x & 63u) * 16u + 1024 * i);
   }
   SVG_DEV static void load_v(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-    for (int i = 0; i < ND; ++i) g.v[i] = *reinterpret_cast<const u32x4*>(it.v + off + 1024 * i);
+    for (int i = 0; i < ND; ++i) g.v[i] = *reinterpret_cast<const u32x4*>(it.v + off + (threadIdx.x & 63u) * 16u + 1024 * i);
   }
   // Tile t for all row tiles (nrt of them): it is in g or on its way, and the next one (t2, on `page2`) follows: its keys
   // are requested as soon as this one's are used, its values likewise: one set of registers of each, always a
@@ -586,27 +607,18 @@ struct Attn {
   }
 
   // ------------------------------------------------------------------ thick
-  // This wave's share of step i (tiles TW i ..) of a run on its way into the step's place at byte `to` of LDS.  Tiles behind the
-  // last one are the last one again.  Returns bit j for a page number outside the cache at tile j.
-  static constexpr int SHARE = TW * TILE / 1024 / kWaves;
+  // This wave's share of a step on its way into the step's place at byte `to` of LDS: a run of KiB of the keys or of the
+  // values of the tile that it will work on (RW waves bring a tile).  Returns 1 for a page number outside the cache.
+  static constexpr int SHARE = TILE / 1024 / RW;
   SVG_DEV static u32 fetch(const Item& it, Pages& pages, int tile, int last, u32 to, int wave) {
-    u32 bad = 0;
-    size_t off[TW];
+    const int t = tile + wave / RW, mine = t <= last ? t : last, page = pages.at(it, mine);
+    const int part = wave % RW;
+    const size_t off = tile_at(it, mine, page) + (size_t)(part % (RW / 2) * SHARE) * 1024;
+    const char* from = (part < RW / 2 ? it.k : it.v) + off;
+    to += (u32)(wave / RW * TILE + part * SHARE * 1024);
 #pragma unroll
-    for (int j = 0; j < TW; ++j) {
-      const int t = tile + j <= last ? tile + j : last, page = pages.at(it, t);
-      if (it.bad(page)) bad |= 1u << j;
-      off[j] = tile_at(it, t, page);
-    }
-#pragma unroll
-    for (int i = 0; i < SHARE; ++i) {
-      constexpr int per = TILE / 1024;
-      const int x = wave * SHARE + i;                 // KiB of the step
-      const int j = TW == 1 ? 0 : x / per, y = x - j * per;  // of tile j: keys, then values
-      const size_t o = off[0] + (TW > 1 && j ? off[TW - 1] - off[0] : 0);
-      load_to_lds(y < 2 * NC ? it.k + o + 1024 * y : it.v + o + 1024 * (y - 2 * NC), to + 1024 * x);
-    }
-    return bad;
+    for (int i = 0; i < SHARE; ++i) load_to_lds(from + 1024 * i, (threadIdx.x & 63u) * 16u, to + 1024 * i);
+    return it.bad(page) ? 1u : 0u;
   }
   // Tile t, whose keys and values begin at kt (this lane's 16 bytes) in LDS, for this wave's row tiles (nrt of them).
   template <bool TREE>
@@ -615,10 +627,17 @@ struct Attn {
     f32x4 s[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // (fragments are read one ahead of the products that use them)
+    auto key = [&](int i) { return *reinterpret_cast<const u32x4*>(kt + (i & 1 ? NC + i / 2 : i / 2) * 1024); };
+    u32x4 k0 = key(0), k1 = key(1);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const u32x4 k0 = *reinterpret_cast<const u32x4*>(kt + c * 1024);
-      const u32x4 k1 = *reinterpret_cast<const u32x4*>(kt + (NC + c) * 1024);
+      u32x4 n0 = k0, n1 = k1;
+      if (c + 1 < NC) {
+        n0 = key(2 * c + 2);
+        n1 = key(2 * c + 3);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -626,7 +645,9 @@ struct Attn {
           s[rt][0] = O::mfma(k0, q[rt][c][n], s[rt][0]);
           s[rt][1] = O::mfma(k1, q[rt][c][n], s[rt][1]);
         }
-      if (D == 256) __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_sched_barrier(0);
+      k0 = n0;
+      k1 = n1;
     }
     if (bad) {
 #pragma unroll
@@ -634,6 +655,7 @@ struct Attn {
     }
     const char* vt = kt + 2 * NC * 1024;
     auto val = [&](int d) { return *reinterpret_cast<const u32x4*>(vt + d * 1024); };
+    const u32x4 first = val(0);
     u32x4 p[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p[rt]);
@@ -641,19 +663,23 @@ struct Attn {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) gather_tree(val, token_mask(it, t), p[rt], row[rt]);
     } else {
+      u32x4 v = first;
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        const u32x4 v = val(d);
+        u32x4 ahead = v;
+        if (d + 1 < ND) ahead = val(d + 1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) row[rt].o[d] = O::mfma(v, p[rt][i], row[rt].o[d]);
-        if (D == 256 && (d & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
+        v = ahead;
       }
     }
   }
   // Tiles t .. last, of each step the one that is this wave's; the first STEPS - 1 steps are on their way, bad: fetch()'s
-  // answers for them, TW bits a step.  live: the wave has rows.
+  // answers for them, a bit a step.  live: the wave has rows.
   SVG_DEV static void walk_thick(const Item& it, int t, int last, const char* ring, Pages& pages, u32 bad, int wave, bool live,
                                  const u32x4 (&q)[RT][NC][NQ], Row (&row)[RT], const u32 (&seen)[RT], u32 broken) {
     const char* mine = ring + wave / RW * TILE + (threadIdx.x & 63u) * 16u;
@@ -665,23 +691,23 @@ struct Attn {
       const int stale = here == 0 ? STEPS - 1 : here - 1;
       wait_loads<SHARE * (STEPS - 2)>();  // this wave's share of the step has arrived; after the barrier all of it has,
       barrier();                          // and nobody reads the place of the step before any more
-      bad |= fetch(it, pages, t + TW * (STEPS - 1), last, ring_at + stale * (TW * TILE), wave) << (TW * (STEPS - 1));
+      bad |= fetch(it, pages, t + TW * (STEPS - 1), last, ring_at + stale * (TW * TILE), wave) << (STEPS - 1);
     };
     auto done = [&] {
       t += TW;
-      bad >>= TW;
+      bad >>= 1;
       here = here == STEPS - 1 ? 0 : here + 1;
     };
     while (t <= last && (t + TW) * 32 <= it.len) {
       next();
       if (live && t + tw <= last)
-        thick_tile<false>(it, t + tw, mine + here * (TW * TILE), (bad >> tw) & 1u, q, row, seen, broken);
+        thick_tile<false>(it, t + tw, mine + here * (TW * TILE), bad & 1u, q, row, seen, broken);
       done();
     }
     while (t <= last) {
       next();
       if (live && t + tw <= last)
-        thick_tile<true>(it, t + tw, mine + here * (TW * TILE), (bad >> tw) & 1u, q, row, seen, broken);
+        thick_tile<true>(it, t + tw, mine + here * (TW * TILE), bad & 1u, q, row, seen, broken);
       done();
     }
     __builtin_amdgcn_s_setprio(0);
@@ -712,53 +738,49 @@ struct Attn {
 template <int D, bool BF, int RTHIN>
 __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   constexpr bool THIN = RTHIN > 0;
-  constexpr int RT = THIN ? RTHIN : 1;
+  constexpr int RT = THIN ? RTHIN : (D < 256 ? 2 : 1);
   using A = Attn<D, BF, RT>;
   constexpr int NC = A::NC, ND = A::ND, NQ = A::NQ;
   __shared__ Plan plan;
   __shared__ __attribute__((aligned(1024))) char lds[THIN ? (A::QBYTES > kWaves * A::JOIN ? A::QBYTES : kWaves * A::JOIN) : A::RING];
   __shared__ float stat[kWaves][RT][2][16];
   __shared__ float factor[RT][16];
-  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads);
-  const Deal deal = make_plan(a, sh, plan);
+  const Shape& sh = a.sh;
+  const Deal deal = make_plan(a, plan);
   const int wg = blockIdx.x;
-  Span* spans = reinterpret_cast<Span*>(a.ws + sh.spans_at());
-  float* stats = reinterpret_cast<float*>(a.ws + sh.stats_at());
-  float* parts = reinterpret_cast<float*>(a.ws + sh.parts_at());
-  if (wg == 0 && threadIdx.x == 0) *reinterpret_cast<int*>(a.ws) = deal.prefix;
-  if (wg >= deal.groups || deal.total == 0) return;
+  float* const stats = a.stats;
+  float* const parts = a.parts;
+  if (wg == 0 && threadIdx.x == 0) *a.header = deal.prefix;
+  if ((u32)wg >= deal.groups || deal.total == 0) return;
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float sign = a.scale < 0.f ? -1.f : 1.f;
   const float unit = fabsf(a.scale) * 1.44269504088896341f;
-  const long end = deal.start(wg + 1);
-  long u = deal.start(wg);
+  const u32 end = deal.start(wg + 1);
+  u32 u = deal.start(wg);
   // the first item: its slot (a prefix item: -1), head, row block and the unit of it that u is
   int s = -1, h, rb, off;
   {
-    int j;
-    if (u < deal.units_p) {
-      j = (int)divide(u, (deal.prefix >> 5) + a.item_cost, off);
-      rb = j % sh.rb_p;
-      h = j / sh.rb_p;
-    } else {
-      const int per = a.c.heads * sh.rb_s;
-      int rest;
-      const int v = (int)divide(u - deal.units_p, per, rest);
-      int lo = 0, hi = a.c.n_slots;  // cum[lo] <= v < cum[hi]
+    u32 v = u, j, units = (u32)((deal.prefix >> 5) + a.item_cost);
+    int blocks = sh.rb_p;
+    if (u >= deal.units_p) {
+      v -= deal.units_p;
+      blocks = sh.rb_s;
+      const u32 per = (u32)(a.c.heads * sh.rb_s), at = v / per;
+      int lo = 0, hi = a.c.n_slots;  // cum[lo] <= at < cum[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (plan.cum[mid] <= v) lo = mid;
+        if ((u32)plan.cum[mid] <= at) lo = mid;
         else hi = mid;
       }
-      s = __builtin_amdgcn_readfirstlane(lo);
-      j = (int)divide(u - deal.units_p - plan.cum[s] * (long)per, plan.cum[s + 1] - plan.cum[s], off);
-      rb = j % sh.rb_s;
-      h = j / sh.rb_s;
+      s = (int)uniform(lo);
+      v -= (u32)plan.cum[s] * per;
+      units = (u32)(plan.cum[s + 1] - plan.cum[s]);
     }
-    h = __builtin_amdgcn_readfirstlane(h);
-    rb = __builtin_amdgcn_readfirstlane(rb);
-    off = __builtin_amdgcn_readfirstlane(off);
+    j = v / units;
+    off = (int)uniform(v - j * units);
+    h = (int)uniform(blocks == 1 ? j : j / (u32)blocks);
+    rb = (int)uniform(j) - h * blocks;
   }
   bool more = false;
   for (; u < end; more = true) {
@@ -778,16 +800,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
     const int slot = prefix ? deal.first : s;
     const int tiles = __builtin_amdgcn_readfirstlane(prefix ? deal.prefix >> 5 : plan.cum[s + 1] - plan.cum[s] - a.item_cost);
     const int units = tiles + a.item_cost;
-    const long left = end - u;
-    const int stop = left < units - off ? off + (int)left : units;
+    const int left = (int)(end - u), stop = left < units - off ? off + left : units;
     const int t0 = off > a.item_cost ? off - a.item_cost : 0, t1 = stop - a.item_cost;
-    const long base_unit = u - off;
+    const u32 item_end = u - off + units;
     u += stop - off;
     if (t1 <= t0) continue;  // the units of its start only
-    const long j = prefix ? (long)h * sh.rb_p + rb : ((long)s * a.c.heads + h) * sh.rb_s + rb;
+    const int j = prefix ? h * sh.rb_p + rb : (s * a.c.heads + h) * sh.rb_s + rb;
     const long place = prefix ? sh.slot_p(wg, j) : sh.slot_s(wg, j);
     if (t0 == 0 && threadIdx.x == 0)
-      spans[prefix ? j : sh.items_p + j] = Span{wg, stop == units ? 1 : group_of(base_unit + units - 1, deal) - wg + 1};
+      a.spans[prefix ? j : sh.items_p + j] = Span{wg, stop == units ? 1 : group_of(item_end - 1, deal) - wg + 1};
 
     const int nodes = plan.nodes[slot];
     const int block = prefix ? sh.block_p : sh.block_s;
@@ -799,7 +820,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
     Item it;
     const size_t head = (size_t)a.c.page * D * 2;
     it.stride = head * a.c.heads;
-    const size_t base = (size_t)a.layer * a.c.n_pages * it.stride + (size_t)h * head + lane * 16;
+    const size_t base = (size_t)a.layer * a.c.n_pages * it.stride + (size_t)h * head;
     it.k = static_cast<const char*>(a.c.k) + base;
     it.v = static_cast<const char*>(a.c.v) + base;
     const int skip = prefix ? 0 : deal.prefix >> 5;  // tiles of the prefix, in front of the slot's own
@@ -830,10 +851,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
       broken |= (u32)__shfl((int)broken, 0, 32);
     };
     // q of row idx of the block (its values 8 g .. of every 32), and its node
-    auto node_of = [&](int idx) { return (rb * block + (idx < rows ? idx : 0)) / a.G; };
+    auto node_of = [&](int idx) { return a.node_of(rb * block + (idx < rows ? idx : 0)); };
     auto q_of = [&](int idx) {
-      const int all = rb * block + (idx < rows ? idx : 0), node = all / a.G;
-      return a.q + ((size_t)(prefix ? 0 : s) * a.T + node) * a.ld_q + (size_t)(h * a.G + all % a.G) * D + 8 * g;
+      const int all = rb * block + (idx < rows ? idx : 0), node = a.node_of(all);
+      return a.q + (size_t)((prefix ? 0 : s * a.T) + node) * a.ld_q + (h * a.G + all - node * a.G) * D + 8 * g;
     };
     auto at4 = [](const float* p) { return *reinterpret_cast<const f32x4*>(p); };
     auto top8 = [&](const float* p, float top) {
@@ -928,7 +949,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
         if (idx < rows) {
           *reinterpret_cast<f32x4*>(parts + (size_t)(place + idx) * D + 16 * d + 4 * g) = o;
           if (d == 0 && g == 0) {
-            float l = 0.f, t = kLow;
+            float l = 0.f, t = kLowest;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
               l += stat[w][rt][1][n];
@@ -947,34 +968,41 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
       nrt = nrt < 0 ? 0 : (nrt < each ? nrt : each);
       Pages pages;
       pages.start(it, first, last);
+      // q has to be here before the tiles are asked for (the compiler does not see those loads, and would wait for them too)
+      f32x4 raw[RT][2 * NC];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float* qp = q_of((rt0 + rt) * 16 + n);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          raw[rt][2 * c] = at4(qp + 32 * c);
+          raw[rt][2 * c + 1] = at4(qp + 32 * c + 4);
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int i = 0; i < 2 * NC; ++i) asm volatile("" : "+v"(raw[rt][i]));
+      u32 outside = 0;
+#pragma unroll
+      for (int i = 0; i < A::STEPS - 1; ++i)
+        outside |= A::fetch(it, pages, first + i * A::TW, last, lds_at(lds) + i * (A::TW * A::TILE), wave) << i;
       u32x4 q[RT][NC][NQ];
       typename A::Row row[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const int idx = (rt0 + rt) * 16 + n;
-        if (rt < nrt) {
-          const float* qp = q_of(idx);
-          float top = 0.f;
+        float top = 0.f;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) top = top8(qp + 32 * c, top);
-          const int e = A::exponent_of(row_max(top));
-          const float by = idx < rows ? A::two_to(-e) * sign : 0.f;
+        for (int i = 0; i < 2 * NC; ++i)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) A::split8(at4(qp + 32 * c), at4(qp + 32 * c + 4), by, q[rt][c]);
-          row[rt].start(unit * A::two_to(e));
-        } else {
-          row[rt].start(0.f);
+          for (int j = 0; j < 4; ++j) top = fmaxf(top, fabsf(raw[rt][i][j]));
+        const int e = A::exponent_of(row_max(top));
+        const float by = rt < nrt && (rt0 + rt) * 16 + n < rows ? A::two_to(-e) * sign : 0.f;
 #pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int p = 0; p < NQ; ++p) q[rt][c][p] = u32x4{0, 0, 0, 0};
-        }
+        for (int c = 0; c < NC; ++c) A::split8(raw[rt][2 * c], raw[rt][2 * c + 1], by, q[rt][c]);
+        row[rt].start(unit * A::two_to(e));
         __builtin_amdgcn_sched_barrier(0);
       }
-      u32 outside = 0;
-#pragma unroll
-      for (int i = 0; i < A::STEPS - 1; ++i)
-        outside |= A::fetch(it, pages, first + i * A::TW, last, lds_at(lds) + i * (A::TW * A::TILE), wave) << (A::TW * i);
       root_paths();
       u32 seen[RT], bad = 0;
 #pragma unroll
@@ -1038,39 +1066,37 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   }
 }
 
-// One wave per output row (slot, node, query head) joins its partials, in the order of the workgroups: D / 4 lanes
-// read one partial's O, the wave 256 / D of them at a time.
+// One wave per output row (query head x, node y, slot z of the grid) joins its partials, in the order of the workgroups:
+// D / 4 lanes read one partial's O, the wave 256 / D of them at a time.
 constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a) {
-  const Shape sh(a.c.n_slots, a.T, a.G, a.c.heads);
+  const Shape& sh = a.sh;
   constexpr int L = D / 4, NP = 64 / L;  // lanes of a partial, partials at a time
-  const int lane = threadIdx.x & 63;
-  const int heads = a.c.heads * a.G;
-  const long x = (long)blockIdx.x * (kJoinThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (x >= (long)a.c.n_slots * a.T * heads) return;
-  const int head = (int)(x % heads), i = (int)(x / heads) % a.T, s = (int)(x / heads / a.T);
-  const int h = head / a.G, gq = head % a.G;
-  const Span* spans = reinterpret_cast<const Span*>(a.ws + sh.spans_at());
-  const float* stats = reinterpret_cast<const float*>(a.ws + sh.stats_at());
-  const float* parts = reinterpret_cast<const float*>(a.ws + sh.parts_at());
-  const long r_p = ((long)s * a.T + i) * a.G + gq, j_p = (long)h * sh.rb_p + r_p / sh.block_p;
-  const long r_s = (long)i * a.G + gq, j_s = ((long)s * a.c.heads + h) * sh.rb_s + r_s / sh.block_s;
+  const int lane = threadIdx.x & 63, i = blockIdx.y, s = blockIdx.z;
+  const int head = blockIdx.x * (kJoinThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (head >= a.c.heads * a.G) return;
+  const int h = a.node_of(head), gq = head - h * a.G;
+  const int r_p = (s * a.T + i) * a.G + gq, r_s = i * a.G + gq;           // rows of a prefix item, of the slot's
+  const int b_p = sh.rb_p == 1 ? 0 : r_p / kBlock, b_s = sh.rb_s == 1 ? 0 : r_s / kBlock;
+  const int j_p = h * sh.rb_p + b_p, j_s = (s * a.c.heads + h) * sh.rb_s + b_s;
   const int nodes = node_count(a, s), len = valid_len(a, s, nodes);
-  const int prefix = *reinterpret_cast<const int*>(a.ws);
-  const Span sp = spans[j_p], ss = spans[sh.items_p + j_s];
+  const int prefix = *a.header;
+  const Span sp = a.spans[j_p], ss = a.spans[sh.items_p + j_s];
   if (i >= nodes) return;  // no such node: the row stays as it was
-  float* out = a.out + x * D + 4 * (lane % L);
+  float* out = a.out + ((size_t)(s * a.T + i) * (a.c.heads * a.G) + head) * D + 4 * (lane % L);
   if (len < 0) {
     const float nan = __builtin_nanf("");
     if (lane < L) *reinterpret_cast<f32x4*>(out) = f32x4{nan, nan, nan, nan};
     return;
   }
   const int np = prefix > 0 ? sp.count : 0, all = np + ss.count;
-  const long at_p = sh.slot_p(sp.first, j_p) + r_p % sh.block_p, at_s = sh.slot_s(ss.first, j_s) + r_s % sh.block_s;
+  const long at_p = sh.slot_p(sp.first, j_p) + (r_p - b_p * kBlock), at_s = sh.slot_s(ss.first, j_s) + (r_s - b_s * kBlock);
   auto row_of = [&](int k) { return k < np ? at_p + (long)k * sh.block_p : at_s + (long)(k - np) * sh.block_s; };
-  float m = kLow, l = 0.f;
+  const float* const stats = a.stats;
+  const float* const parts = a.parts;
+  float m = kLowest, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   constexpr int U = 8;  // requests in flight a lane
   for (int k0 = lane / L; k0 < all; k0 += NP * U) {
@@ -1087,7 +1113,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k0 + u * NP >= all) { pm[u] = kLow; pl[u] = 0.f; po[u] = f32x4{0.f, 0.f, 0.f, 0.f}; }
+      if (k0 + u * NP >= all) { pm[u] = kLowest; pl[u] = 0.f; po[u] = f32x4{0.f, 0.f, 0.f, 0.f}; }
       top = fmaxf(top, pm[u]);
     }
     const float w0 = __builtin_amdgcn_exp2f(m - top);
@@ -1135,12 +1161,18 @@ void launch(const AttnArgs& a, hipStream_t stream) {
   } else {
     launch_items<D, BF>(a, kPrefix | kSlots, rows_p, stream);
   }
-  const long rows = (long)a.c.n_slots * a.T * a.c.heads * a.G;
   constexpr int per = kJoinThreads / 64;
-  hipLaunchKernelGGL((k_tree_attention_join<D>), dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, stream, a);
+  hipLaunchKernelGGL((k_tree_attention_join<D>), dim3((a.c.heads * a.G + per - 1) / per, a.T, a.c.n_slots), dim3(kJoinThreads), 0,
+                     stream, a);
 }
 
 }  // namespace
+
+bool svg_tree_attention_fits(const svg_kv_cache& c, int T, int G) {
+  const Shape sh(c.n_slots, T, G, c.heads);
+  const int64_t most = ((int64_t)c.width * c.page + 31) / 32 + 1 + (kItemThin > kItemThick ? kItemThin : kItemThick);
+  return most * ((int64_t)sh.items_p + sh.items_s) < (1ll << 31);
+}
 
 uint64_t svg_tree_attention_bytes(const svg_kv_cache& c, int T, int G) {
   return Shape(c.n_slots, T, G, c.heads).bytes(c.dim);
@@ -1150,8 +1182,12 @@ hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const flo
                                      const int32_t* parent, int T, const int32_t* n_nodes, const int32_t* shared,
                                      float scale, float* out, void* workspace, hipStream_t stream) {
   const int cus = svg_cu_count();
-  const AttnArgs a{c, q, parent, n_nodes, shared, out, static_cast<char*>(workspace), (long)ld_q, layer, T, G,
-                   cus < kMaxGroups ? cus : kMaxGroups, 0, 0, 0, scale};
+  const Shape sh(c.n_slots, T, G, c.heads);
+  char* ws = static_cast<char*>(workspace);
+  const AttnArgs a{c, q, parent, n_nodes, shared, out, reinterpret_cast<int*>(ws), reinterpret_cast<Span*>(ws + 256),
+                   reinterpret_cast<float*>(ws + sh.stats_at()), reinterpret_cast<float*>(ws + sh.parts_at()), (long)ld_q,
+                   layer, T, G, cus < kMaxGroups ? cus : kMaxGroups, 0, 0, 0,
+                   G == 1 ? 0u : (u32)(((1ull << 32) + G - 1) / G), sh, scale};
   const bool bf = c.type == SVG_BF16;
   if (c.dim == 64) {
     if (bf) launch<64, true>(a, stream);
