@@ -77,75 +77,82 @@ __global__ __launch_bounds__(64) void k_kv_append(svg_kv_cache c, int layer, con
 }
 
 // ------------------------------------------------------------------- commit
-// The moves of slot s: n - 1 of them, from position len + path[j] to
-// len + 1 + j; 0 if the slot keeps its tokens (and then ok says why not moved:
-// true only for a valid path with nothing to move).  Uniform over the workgroup.
+// What slot s commits: `kept` tokens, the root's and the accepted nodes' (0: the path is not valid, or its tokens are not
+// inside the slot's pages), the same in every lane of the wave; in lane j the node that moves to len + 1 + j.
 struct Moves {
-  int n;
-  bool ok;
+  int kept, len, node;
 };
 SVG_DEV Moves moves_of(const svg_kv_cache& c, int s, int T, const int32_t* path, const int32_t* n_emit) {
+  const int lane = threadIdx.x & 63;
   const int n = n_emit[s], len = c.len[s], held = c.pages[s];
+  const int p = lane < T ? path[(size_t)s * T + lane] : -1;
+  int before = __shfl_up(p, 1);
+  if (lane == 0) before = 0;
+  const bool mine = lane < n - 1;
   bool ok = n >= 1 && n <= T && len >= 0 && held >= 0 && held <= c.width;
-  int last = 0;
-  for (int j = 0; ok && j < n - 1; ++j) {
-    const int p = path[(size_t)s * T + j];
-    ok = p > last && p < T;
-    last = p;
-  }
-  // every position from len on that is read or written: two pages at most
+  ok = ok && !__any(mine && !(p > before && p < T));
+  // every position from len on that is read or written lies between the root's and the last node's: two pages at most
   if (ok) {
+    const int last = n > 1 ? __shfl(p, n - 2) : 0;
     int page;
     ok = page_of(c, s, (long)len / c.page, page) && page_of(c, s, ((long)len + last) / c.page, page);
   }
-  return {ok ? n : 0, ok};
+  return {ok ? n : 0, len, p};
 }
 
-// One workgroup per (head, layer, slot): all rows are read before any is
-// written (a row's place may be another's source).
+// One workgroup per (head, layer, slot): all rows are read before any is written (a row's place may be another's source).
+// The two pages and the places in them are looked up once, by one wave, while nothing else waits.
+// Bound by latency: a chain of the path, the table and the rows (8 slots of 16 nodes, 32 layers of 8 heads of 128: see the
+// launcher).
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void k_kv_commit(svg_kv_cache c, int T, const int32_t* __restrict__ path,
                                                        const int32_t* __restrict__ n_emit, int32_t* len_out) {
   __shared__ uint4 kb[(SVG_TREE_MAX_NODES - 1) * DIM / 8];
   __shared__ uint16_t vb[(SVG_TREE_MAX_NODES - 1) * DIM];
+  __shared__ int place[SVG_TREE_MAX_NODES][2];  // of each move: the source's (page << 7) + token, the destination's
   const int h = blockIdx.x, l = blockIdx.y, s = blockIdx.z;
   const Moves m = moves_of(c, s, T, path, n_emit);
-  const int len = c.len[s];
-  if (len_out != nullptr && h == 0 && l == 0 && threadIdx.x == 0) len_out[s] = len + m.n;
-  const int rows = m.n - 1;
+  if (len_out != nullptr && h == 0 && l == 0 && threadIdx.x == 0) len_out[s] = m.len + m.kept;
+  const int rows = m.kept - 1;
   if (rows <= 0) return;
+  if ((int)threadIdx.x < rows) {
+    const int32_t* tab = c.table + (size_t)s * c.width;
+    const int from = m.len + m.node, to = m.len + 1 + (int)threadIdx.x;
+    place[threadIdx.x][0] = (tab[from / c.page] << 7) + from % c.page;
+    place[threadIdx.x][1] = (tab[to / c.page] << 7) + to % c.page;
+  }
+  __syncthreads();
   const size_t stride = (size_t)c.heads * c.page * DIM;  // of a page
   const size_t at = (size_t)l * c.n_pages * stride + (size_t)h * c.page * DIM;
-  const int32_t* tab = c.table + (size_t)s * c.width;
   uint16_t* kl = static_cast<uint16_t*>(c.k) + at;
   uint16_t* vl = static_cast<uint16_t*>(c.v) + at;
-  const int32_t* pth = path + (size_t)s * T;
   for (int x = threadIdx.x; x < rows * (DIM / 8); x += kThreads) {
-    const int p = len + pth[x / (DIM / 8)];
-    kb[x] = *reinterpret_cast<const uint4*>(kl + (size_t)tab[p / c.page] * stride + kv_key_at(p % c.page, 8 * (x % (DIM / 8)), DIM));
+    const int p = place[x / (DIM / 8)][0];
+    kb[x] = *reinterpret_cast<const uint4*>(kl + (size_t)(p >> 7) * stride + kv_key_at(p & 127, 8 * (x % (DIM / 8)), DIM));
   }
+#pragma unroll 4
   for (int x = threadIdx.x; x < rows * DIM; x += kThreads) {
-    const int p = len + pth[x / DIM];
-    vb[x] = vl[(size_t)tab[p / c.page] * stride + kv_value_at(p % c.page, x % DIM, DIM)];
+    const int p = place[x / DIM][0];
+    vb[x] = vl[(size_t)(p >> 7) * stride + kv_value_at(p & 127, x % DIM, DIM)];
   }
   __syncthreads();
   for (int x = threadIdx.x; x < rows * (DIM / 8); x += kThreads) {
-    const int p = len + 1 + x / (DIM / 8);
-    *reinterpret_cast<uint4*>(kl + (size_t)tab[p / c.page] * stride + kv_key_at(p % c.page, 8 * (x % (DIM / 8)), DIM)) = kb[x];
+    const int p = place[x / (DIM / 8)][1];
+    *reinterpret_cast<uint4*>(kl + (size_t)(p >> 7) * stride + kv_key_at(p & 127, 8 * (x % (DIM / 8)), DIM)) = kb[x];
   }
   for (int x = threadIdx.x; x < rows * DIM; x += kThreads) {
-    const int p = len + 1 + x / DIM;
-    vl[(size_t)tab[p / c.page] * stride + kv_value_at(p % c.page, x % DIM, DIM)] = vb[x];
+    const int p = place[x / DIM][1];
+    vl[(size_t)(p >> 7) * stride + kv_value_at(p & 127, x % DIM, DIM)] = vb[x];
   }
 }
 
-// The new lengths in place, after every reader of the old ones.
+// The new lengths in place, after every reader of the old ones: a wave a slot.
 __global__ __launch_bounds__(kThreads) void k_kv_commit_len(svg_kv_cache c, int T, const int32_t* __restrict__ path,
                                                            const int32_t* __restrict__ n_emit) {
-  const int s = blockIdx.x * kThreads + threadIdx.x;
+  const int s = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
   if (s >= c.n_slots) return;
   const Moves m = moves_of(c, s, T, path, n_emit);
-  c.len[s] += m.n;
+  if ((threadIdx.x & 63) == 0) c.len[s] = m.len + m.kept;
 }
 
 // --------------------------------------------------------------------- fork
@@ -335,9 +342,10 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(svg_kv_cache c, const int3
 }
 
 // -------------------------------------------------------------------- copies
-// Pages copied in every layer, keys and values: (pair, layer, k or v) blocks of
-// `chunk` 16-byte pieces, spread over the grid.  COUNTED: the pairs and their
-// number as kv_reserve's plan left them.
+// Pages copied in every layer, keys and values: (pair, layer, k or v) blocks of kChunk 16-byte pieces, spread over the
+// grid.  COUNTED: the pairs and their number as kv_reserve's plan left them.  Bound by memory: 407 MB of pages in 162 us
+// (5.0 TB/s read and written; 166 us through the caches).  One piece of a thread at a time: with four on their way the same copy
+// took 169 us, 24 pages of forks 37 us instead of 30 us.
 constexpr int kChunk = 4096;  // pieces of a workgroup's turn (64 KiB)
 
 template <bool COUNTED>
@@ -365,7 +373,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_copy(svg_kv_cache c, const int3
     const uint4* from = base + (size_t)a * pieces;
     uint4* to = base + (size_t)b * pieces;
     const long end = (ch + 1) * kChunk < pieces ? (ch + 1) * kChunk : pieces;
-    for (long x = ch * kChunk + threadIdx.x; x < end; x += kThreads) to[x] = from[x];
+#pragma unroll 1
+    for (long x = ch * kChunk + threadIdx.x; x < end; x += kThreads) {
+      if constexpr (COUNTED) {
+        to[x] = from[x];  // one source for several forks, and what is written is read next
+      } else {
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + x));
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to + x));
+      }
+    }
   }
 }
 
@@ -392,7 +408,7 @@ hipError_t svg_launch_kv_commit(const svg_kv_cache& c, int T, const int32_t* pat
   else
     hipLaunchKernelGGL(k_kv_commit<256>, grid, dim3(kThreads), 0, stream, c, T, path, n_emit, out);
   if (out == nullptr)
-    hipLaunchKernelGGL(k_kv_commit_len, dim3((c.n_slots + kThreads - 1) / kThreads), dim3(kThreads), 0, stream, c, T,
+    hipLaunchKernelGGL(k_kv_commit_len, dim3((c.n_slots + kThreads / 64 - 1) / (kThreads / 64)), dim3(kThreads), 0, stream, c, T,
                        path, n_emit);
   return hipGetLastError();
 }

@@ -9,10 +9,16 @@ import ctypes
 
 import torch
 
+_lib = None  # the library, once the package has loaded it (_bind)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 _FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
 def _bind(lib):
+    global _lib
+    _lib = lib
     vp, i, d = ctypes.c_void_p, ctypes.c_int, ctypes.c_double
     lib.add_rmsnorm_quant_i8.argtypes = [vp, i, vp, vp, i, d, i, i, vp, i, vp, vp, vp, vp]
     lib.add_rmsnorm_quant_i8.restype = ctypes.c_int
@@ -64,10 +70,10 @@ def _device(t, name):
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with dev as the current device."""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+        stream = _raw_stream(dev.index)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if _current_device() == dev.index:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -97,7 +103,7 @@ def add_rmsnorm_quant_i8(x, residual, weight, eps, signs, xq, x_scale, y=None, b
     if ((residual is not None and residual.shape != x.shape) or (y is not None and y.shape != x.shape)
             or weight.numel() != K or signs.numel() != K or xq.numel() != M * K or x_scale.numel() != M):
         raise ValueError("need residual and y [M, K], weight and signs [K], xq of M * K codes and x_scale [M]")
-    _call(_lib().add_rmsnorm_quant_i8, dev, stream, px, kx, pr, pw, kw, eps, M, K, ps, block, py, pq, pc)
+    _call(_lib.add_rmsnorm_quant_i8, dev, stream, px, kx, pr, pw, kw, eps, M, K, ps, block, py, pq, pc)
 
 
 # ------------------------------------------------------------------ the cache
@@ -181,7 +187,7 @@ def kv_append(cache, layer, k, v, T, n_rows=None, stream=None):
     if nk != cache.n_slots * T or nv != nk:
         raise ValueError("k and v must have n_slots * T rows")
     pn = None if n_rows is None else _slots(n_rows, "n_rows", cache)
-    _call(_lib().kv_append, cache.device, stream, cache._ref, layer, pk, lk, pv, lv, T, pn)
+    _call(_lib.kv_append, cache.device, stream, cache._ref, layer, pk, lk, pv, lv, T, pn)
 
 
 def kv_commit(cache, path, n_emit, len_out=None, stream=None):
@@ -192,7 +198,7 @@ def kv_commit(cache, path, n_emit, len_out=None, stream=None):
         raise ValueError("path must be [n_slots, T]")
     T = path.shape[1]
     out = cache.len if len_out is None else len_out
-    _call(_lib().kv_commit, cache.device, stream, cache._ref, T, _slots(path, "path", cache, T),
+    _call(_lib.kv_commit, cache.device, stream, cache._ref, T, _slots(path, "path", cache, T),
           _slots(n_emit, "n_emit", cache), _slots(out, "len_out", cache))
 
 
@@ -204,7 +210,7 @@ def kv_fork(cache, src, out, stream=None):
         raise ValueError("out must be a cache over the same pages and counts")
     if out.table.shape != cache.table.shape:
         raise ValueError("out needs tables of the same shape")
-    _call(_lib().kv_fork, cache.device, stream, cache._ref, _slots(src, "src", cache), out._c.table, out._c.pages,
+    _call(_lib.kv_fork, cache.device, stream, cache._ref, _slots(src, "src", cache), out._c.table, out._c.pages,
           out._c.len)
 
 
@@ -219,7 +225,7 @@ def kv_reserve(cache, need, status, workspace, stream=None):
     pw = _tensor(workspace, "workspace", torch.int32, cache.device)
     if workspace.numel() < 2 * cache.n_slots + 4:
         raise ValueError("workspace is smaller than kv_workspace(cache)")
-    _call(_lib().kv_reserve, cache.device, stream, cache._ref, _slots(need, "need", cache),
+    _call(_lib.kv_reserve, cache.device, stream, cache._ref, _slots(need, "need", cache),
           _slots(status, "status", cache), pw)
 
 
@@ -227,7 +233,7 @@ def kv_copy_pages(cache, src, dst, stream=None):
     """Copy pages src (int32 [n]) to pages dst in every layer."""
     if src.dim() != 1 or src.shape != dst.shape:
         raise ValueError("src and dst must be [n]")
-    _call(_lib().kv_copy_pages, cache.device, stream, cache._ref, _tensor(src, "src", torch.int32, cache.device),
+    _call(_lib.kv_copy_pages, cache.device, stream, cache._ref, _tensor(src, "src", torch.int32, cache.device),
           _tensor(dst, "dst", torch.int32, cache.device), src.shape[0])
 
 
@@ -235,7 +241,7 @@ def kv_copy_pages(cache, src, dst, stream=None):
 def tree_attention_workspace(cache, q_heads, T):
     """A workspace for tree_attention calls of these sizes (one for each stream that makes them)."""
     n = ctypes.c_uint64()
-    status = _lib().tree_attention_workspace(cache._ref, q_heads, T, ctypes.byref(n))
+    status = _lib.tree_attention_workspace(cache._ref, q_heads, T, ctypes.byref(n))
     if status:
         from . import SvgError, last_error
         raise SvgError(status, last_error())
@@ -260,18 +266,13 @@ def tree_attention(cache, layer, q, parent, out, workspace, scale=None, n_nodes=
     need = cache._attn_bytes.get((heads, T))
     if need is None:
         b = ctypes.c_uint64()
-        if _lib().tree_attention_workspace(cache._ref, heads, T, ctypes.byref(b)) == 0:
+        if _lib.tree_attention_workspace(cache._ref, heads, T, ctypes.byref(b)) == 0:
             need = cache._attn_bytes[(heads, T)] = b.value
     if need is not None and workspace.numel() * workspace.element_size() < need:
         raise ValueError("workspace is smaller than tree_attention_workspace(cache, q_heads, T)")
     pp = None if parent is None else _slots(parent, "parent", cache, T)
     pn = None if n_nodes is None else _slots(n_nodes, "n_nodes", cache)
     ps = None if shared is None else _tensor(shared, "shared", torch.int32, cache.device)
-    _call(_lib().tree_attention, cache.device, stream, cache._ref, layer, pq, ld, heads, pp, T, pn, ps,
+    _call(_lib.tree_attention, cache.device, stream, cache._ref, layer, pq, ld, heads, pp, T, pn, ps,
           D ** -0.5 if scale is None else scale, _tensor(out, "out", torch.float32, cache.device),
           _tensor(workspace, "workspace", torch.uint8, cache.device))
-
-
-def _lib():
-    from . import lib
-    return lib
