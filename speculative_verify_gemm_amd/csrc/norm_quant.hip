@@ -143,11 +143,20 @@ __global__ __launch_bounds__(NT) void k_norm_quant(NormArgs a) {
   act_quant_loaded<CPT, StoreGlobal, B, true>(r, K, st, red);
 }
 
+// Few rows: as many threads as the row has chunks (the chain of one row is all there is).  Many rows: a row for
+// 256 threads, so that a compute unit has several at different steps.  Measured (fp16 rows with a residual, back to back,
+// few | many): K = 4096: 256 rows 5.6 | 5.7 us, 512 rows 8.1 | 6.9 us, 4099 rows (cold) 45.7 | 39.2 us (4.7 TB/s);
+// K = 8192: 512 rows 11.1 | 11.8 us, 1024 rows 18.1 | 17.7 us.
 template <int B>
 void launch(const NormArgs& a, hipStream_t stream) {
   const int nchunk = a.K / 4;
 #define SVG_NORM(NT, CPT) hipLaunchKernelGGL((k_norm_quant<NT, CPT, B>), dim3(a.M), dim3(NT), 0, stream, a)
-  if (nchunk <= 256) SVG_NORM(256, 1);
+  if (nchunk <= 2048 && a.M >= (nchunk <= 1024 ? 512 : 1024)) {
+    if (nchunk <= 256) SVG_NORM(256, 1);
+    else if (nchunk <= 512) SVG_NORM(256, 2);
+    else if (nchunk <= 1024) SVG_NORM(256, 4);
+    else SVG_NORM(256, 8);
+  } else if (nchunk <= 256) SVG_NORM(256, 1);
   else if (nchunk <= 512) SVG_NORM(512, 1);
   else if (nchunk <= 1024) SVG_NORM(1024, 1);
   else if (nchunk <= 2048) SVG_NORM(1024, 2);

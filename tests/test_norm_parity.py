@@ -76,6 +76,8 @@ def check(x, res, w, signs, block=32, eps=EPS, want_y=True):
     (32, 4096, 32, "fp32", "fp32"), (33, 4128, 32, "bf16", "bf16"), (67, 1088, 64, "fp16", "fp16"),
     (5, 12288, 32, "fp32", "fp32"), (2, 16384, 64, "bf16", "fp32"), (3, 20000, 32, "fp32", "fp16"),
     (2, 32768, 32, "fp16", "fp32"),
+    # enough rows for the narrow workgroups, at each number of chunks a thread
+    (515, 640, 32, "fp32", "fp32"), (512, 1984, 64, "fp16", "bf16"), (513, 4096, 32, "bf16", "fp32"), (1025, 6016, 32, "fp32", "fp16"),
 ])
 def test_matches_the_oracle(M, K, block, xt, wt):
     C.say(f"add_rmsnorm_quant_i8 M={M} K={K} block={block} {xt} {wt}")
