@@ -269,7 +269,6 @@ struct Ops<false> {
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
   }
-  SVG_DEV static float wide(u32 h) { return (float)__builtin_bit_cast(_Float16, (uint16_t)h); }
   // bits 15 and 31: the halves that are not finite (their exponent, all ones, plus one)
   SVG_DEV static u32 odd(u32 w) { return ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u; }
   static constexpr u32 kOne = 0x3C00u;
@@ -280,24 +279,24 @@ struct Ops<true> {
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
   }
-  SVG_DEV static float wide(u32 h) { return __uint_as_float(h << 16); }
   SVG_DEV static u32 odd(u32 w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
   static constexpr u32 kOne = 0x3F80u;
 };
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Two probabilities in two parts, packed: fp16 parts are cut off (what the first leaves, the second takes; the rest
 // is below 2^-21), bf16 parts are rounded.
 template <bool BF>
 SVG_DEV void split_pair(float x, float y, u32& hi, u32& lo) {
   if constexpr (BF) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     hi = __builtin_bit_cast(u32, __builtin_convertvector(f32x2{x, y}, bf16x2));
     lo = __builtin_bit_cast(u32, __builtin_convertvector(
                                      f32x2{x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xFFFF0000u)}, bf16x2));
   } else {
-    typedef __fp16 f16x2 __attribute__((ext_vector_type(2)));
-    const f16x2 h = __builtin_amdgcn_cvt_pkrtz(x, y);
+    const auto h = __builtin_amdgcn_cvt_pkrtz(x, y);
     hi = __builtin_bit_cast(u32, h);
     lo = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(__builtin_fmaf((float)h[0], -1.f, x), __builtin_fmaf((float)h[1], -1.f, y)));
   }
@@ -309,19 +308,25 @@ template <bool BF, int N>
 SVG_DEV void split2(float x, float y, u32 (&w)[N]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    const u32 hx = kv_round<BF>(x), hy = kv_round<BF>(y);
-    w[n] = hx | (hy << 16);
-    x -= Ops<BF>::wide(hx);
-    y -= Ops<BF>::wide(hy);
+    if constexpr (BF) {
+      w[n] = __builtin_bit_cast(u32, __builtin_convertvector(f32x2{x, y}, bf16x2));
+      x -= __uint_as_float(w[n] << 16);
+      y -= __uint_as_float(w[n] & 0xFFFF0000u);
+    } else {
+      const f16x2 h = __builtin_convertvector(f32x2{x, y}, f16x2);
+      w[n] = __builtin_bit_cast(u32, h);
+      x -= (float)h[0];
+      y -= (float)h[1];
+    }
   }
 }
 
 // ----------------------------------------------------------------- the kernel
-// vmcnt(N), the other counters left alone.
+// All but the last N loads of this wave have arrived, and everything it has read from LDS.
 template <int N>
 SVG_DEV void wait_loads() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
   asm volatile("" ::: "memory");
 }
 SVG_DEV void barrier() {

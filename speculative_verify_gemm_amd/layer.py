@@ -41,23 +41,28 @@ class KVCacheC(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("table", "pages", "len", "refs")])
 
 
-def _tensor(t, name, dtype, dev):
-    """A contiguous tensor of dtype on dev: its address."""
+def _bad(t, name, dtype, dev):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _tensor(t, name, dtype, dev):
+    """A contiguous tensor of dtype on dev: its address."""
+    if t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    _bad(t, name, dtype, dev)
 
 
 def _float_tensor(t, name, dev):
     """As _tensor, of any of the element types: (address, type number)."""
-    kind = _FLOATS.get(t.dtype)
+    dtype = t.dtype
+    kind = _FLOATS.get(dtype)
     if kind is None:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    return _tensor(t, name, t.dtype, dev), kind
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
+    return _tensor(t, name, dtype, dev), kind
 
 
 def _device(t, name):
@@ -272,6 +277,8 @@ def tree_attention(cache, layer, q, parent, out, workspace, scale=None, n_nodes=
         raise ValueError("workspace is smaller than tree_attention_workspace(cache, q_heads, T)")
     pp = None if parent is None else _slots(parent, "parent", cache, T)
     pn = None if n_nodes is None else _slots(n_nodes, "n_nodes", cache)
+    if shared is not None and shared.numel() < 1:
+        raise ValueError("shared needs 1 element")
     ps = None if shared is None else _tensor(shared, "shared", torch.int32, cache.device)
     _call(_lib.tree_attention, cache.device, stream, cache._ref, layer, pq, ld, heads, pp, T, pn, ps,
           D ** -0.5 if scale is None else scale, _tensor(out, "out", torch.float32, cache.device),

@@ -97,7 +97,8 @@ CASES = [  # lens, T, H, G, dim, page, kind
     ([257], 32, 2, 4, 128, 128, "bf16"), ([2049], 32, 1, 8, 64, 64, "fp16"), ([700], 7, 2, 8, 256, 32, "bf16"),
     ([5, 0, 64, 333], 3, 2, 2, 128, 64, "bf16"), ([100] * 9, 1, 1, 5, 64, 32, "fp16"), ([63, 65, 64], 32, 1, 2, 256, 64, "fp16"),
     ([4100, 3, 900], 5, 3, 7, 128, 128, "fp16"), ([40], 17, 1, 16, 128, 32, "bf16"), ([90, 20], 32, 2, 12, 64, 32, "bf16"),
-    ([300] * 40, 2, 4, 1, 64, 32, "fp16"),
+    ([300] * 40, 2, 4, 1, 64, 32, "fp16"), ([513, 31], 8, 2, 4, 128, 64, "fp16"), ([100, 1], 5, 2, 4, 64, 32, "bf16"),
+    ([1290], 4, 3, 8, 128, 32, "bf16"), ([(7 * s) % 90 for s in range(300)], 2, 1, 2, 64, 32, "bf16"), ([3] * 1024, 1, 1, 1, 64, 32, "fp16"),
 ]
 
 
@@ -319,3 +320,35 @@ def test_two_streams_with_their_own_workspaces():
     ref = torch.zeros((8, 8, 64), device=C.DEV)
     svg.tree_attention(cache, 0, qd, None, ref, wss[0])
     assert all(np.array_equal(C.host(o), C.host(ref)) for o in outs)
+
+
+def test_the_binding_checks_its_tensors():
+    """What the C call cannot see: devices, types, shapes, strides, the workspace's size."""
+    c = K.make(1, [5, 9], 4, H=2, dim=64)
+    cache = K.to_library(svg, c)
+    q = torch.zeros((8, 4, 64), device=C.DEV)
+    out, ws, par = torch.zeros_like(q), svg.tree_attention_workspace(cache, 4, 4), i32(np.zeros((2, 4)))
+    ok = dict(q=q, parent=par, out=out, workspace=ws)
+    svg.tree_attention(cache, 0, **ok)
+    for kw, err in ((dict(q=q.half()), TypeError), (dict(q=q[:7]), ValueError), (dict(q=q.cpu()), ValueError),
+                    (dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), ValueError), (dict(out=out[:, :2]), ValueError),
+                    (dict(out=out.double()), TypeError), (dict(workspace=ws[:-1]), ValueError), (dict(parent=par.long()), TypeError),
+                    (dict(parent=par[:1]), ValueError), (dict(n_nodes=i32([1])), ValueError),
+                    (dict(shared=torch.zeros(0, dtype=torch.int32, device=C.DEV)), ValueError)):
+        with pytest.raises(err):
+            svg.tree_attention(cache, 0, **{**ok, **kw})
+    with pytest.raises(svg.SvgError):
+        svg.tree_attention(cache, 1, **ok)
+    with pytest.raises(svg.SvgError):    # rows that do not begin on 16 bytes
+        svg.tree_attention(cache, 0, **{**ok, "q": torch.zeros((8, 257), device=C.DEV)[:, 1:].unflatten(1, (4, 64))})
+    k = torch.zeros((8, 2, 64), device=C.DEV)
+    with pytest.raises(ValueError):
+        svg.kv_append(cache, 0, k, k[:4], 4)
+    with pytest.raises(ValueError):
+        svg.kv_commit(cache, i32(np.zeros((3, 4))), i32([1, 1]))
+    with pytest.raises(ValueError):
+        svg.kv_fork(cache, i32([0, 0]), K.to_library(svg, c))
+    with pytest.raises(svg.SvgError):
+        svg.kv_fork(cache, i32([0, 0]), cache)
+    with pytest.raises(ValueError):
+        svg.kv_reserve(cache, i32([1, 1]), i32([0, 0]), svg.kv_workspace(cache)[:-1])
