@@ -59,7 +59,7 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
 // takes.  A workgroup gets kMinThin / kMinThick units at least.
-constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 12, kMinThick = 6;
+constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 9, kMinThick = 5;
 
 // Row tiles of an item that is walked the thin way.
 template <int D>
@@ -581,7 +581,8 @@ struct Attn {
     }
     const size_t at2 = tile_at(it, t2, page2);
     __builtin_amdgcn_sched_barrier(0);  // the next keys take these keys' registers, not others
-    load_k(it, at2, g);
+    constexpr bool kLate = TREE && D == 256;  // (no registers for both there: the last tiles, one after the other)
+    if constexpr (!kLate) load_k(it, at2, g);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt < nrt) {
@@ -593,6 +594,7 @@ struct Attn {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    if constexpr (kLate) load_k(it, at2, g);
     load_v(it, at2, g);
   }
   // Tiles t, t + kWaves, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
@@ -892,13 +894,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
       }
       typename A::Regs regs;
       int my_page = 0;
-      if (mine <= last) {
-        my_page = pages.at(it, mine);
-        const size_t at = A::tile_at(it, mine, my_page);
-        A::load_k(it, at, regs);
-        A::load_v(it, at, regs);
-      }
-      root_paths();
+      auto request = [&] {
+        if (mine <= last) {
+          my_page = pages.at(it, mine);
+          const size_t at = A::tile_at(it, mine, my_page);
+          A::load_k(it, at, regs);
+          A::load_v(it, at, regs);
+        }
+      };
+      if constexpr (D < 256) request();
       if (splits) {
         const int e = A::exponent_of(row_max(largest));
         u32x4 parts_of[NQ];
@@ -908,6 +912,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
           *reinterpret_cast<u32x4*>(lds + ((my_rt * NC + my_c) * NQ + p) * 1024 + lane * 16) = parts_of[p];
         if (my_c == 0 && g == 0) factor[my_rt][n] = unit * A::two_to(e);
       }
+      if constexpr (D == 256) {  // (no registers for a tile beside q)
+        __builtin_amdgcn_sched_barrier(0);
+        request();
+      }
+      root_paths();
       __syncthreads();
       typename A::Row row[RT];
       u32 seen[RT], bad = 0;
