@@ -59,7 +59,7 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
 // takes.  A workgroup gets kMinThin / kMinThick units at least.
-constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 9, kMinThick = 5;
+constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 9, kMinThick = 2;
 
 // Row tiles of an item that is walked the thin way.
 template <int D>
@@ -497,17 +497,7 @@ struct Attn {
     }
     return keep;
   }
-  // O += V^T P^T, val(d) the values of columns 16 d ..
-  template <class F>
-  SVG_DEV static void gather(F val, const u32x4 (&p)[2], Row& r) {
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const u32x4 v = val(d);
-      r.o[d] = O::mfma(v, p[0], r.o[d]);
-      r.o[d] = O::mfma(v, p[1], r.o[d]);
-    }
-  }
-  // The same for a tile with tree tokens.  Values that are not finite are left out of the product (0 times them
+  // O += V^T P^T for a tile with tree tokens, val(d) the values of columns 16 d ..  Values that are not finite are left out of the product (0 times them
   // would be NaN in every row) and make NaN where a row has a share of them.
   template <class F>
   SVG_DEV static void gather_tree(F val, const u32x4 keep, const u32x4 (&p)[2], Row& r) {
@@ -544,24 +534,31 @@ struct Attn {
   }
 
   // ------------------------------------------------------------------- thin
+  // dim 256 has registers for one of them: values are requested as the keys are used, keys as the values are
+  static constexpr bool kOne = D == 256;
   struct Regs {
     u32x4 k[2][NC], v[ND];
   };
+  SVG_DEV static u32x4 piece(const char* base, size_t off, int i) {
+    return *reinterpret_cast<const u32x4*>(base + off + (threadIdx.x & 63u) * 16u + 1024 * i);
+  }
   SVG_DEV static void load_k(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-    for (int i = 0; i < 2 * NC; ++i) g.k[i / NC][i % NC] = *reinterpret_cast<const u32x4*>(it.k + off + (threadIdx.x & 63u) * 16u + 1024 * i);
+    for (int i = 0; i < 2 * NC; ++i) g.k[i & 1][i >> 1] = piece(it.k, off, (i & 1) * NC + (i >> 1));
   }
   SVG_DEV static void load_v(const Item& it, size_t off, Regs& g) {
 #pragma unroll
-    for (int i = 0; i < ND; ++i) g.v[i] = *reinterpret_cast<const u32x4*>(it.v + off + (threadIdx.x & 63u) * 16u + 1024 * i);
+    for (int i = 0; i < ND; ++i) g.v[i] = piece(it.v, off, i);
   }
-  // Tile t for all row tiles (nrt of them): it is in g or on its way, and the next one (t2, on `page2`) follows: its keys
-  // are requested as soon as this one's are used, its values likewise: one set of registers of each, always a
-  // request in flight.
+  // Tile t for all row tiles (nrt of them): its keys are in g or on their way (kOne: the values are not), and the next tile
+  // (t2, on `page2`) follows: its keys are requested as soon as this one's are used, its values likewise: one
+  // set of registers of each, always a request in flight.
   template <bool TREE>
   SVG_DEV static void thin_tile(const Item& it, int t, int t2, Regs& g, int page, int page2, const char* ql, Row (&row)[RT], int nrt,
                                 const u32 (&seen)[RT], u32 broken) {
+    static_assert(!kOne || RT == 1, "the keys are given up by the only row tile");
     asm volatile("" : "+v"(ql));  // q is read again for every tile, not kept
+    const size_t at = tile_at(it, t, page);
     f32x4 s[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -574,28 +571,49 @@ struct Attn {
             const u32x4 q = *reinterpret_cast<const u32x4*>(ql + ((rt * NC + c) * NQ + n) * 1024);
             s[rt][0] = O::mfma(g.k[0][c], q, s[rt][0]);
             s[rt][1] = O::mfma(g.k[1][c], q, s[rt][1]);
-            if (D == 256) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kOne) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (n == NQ - 1) {
+                g.v[2 * c] = piece(it.v, at, 2 * c);
+                g.v[2 * c + 1] = piece(it.v, at, 2 * c + 1);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
           }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     const size_t at2 = tile_at(it, t2, page2);
     __builtin_amdgcn_sched_barrier(0);  // the next keys take these keys' registers, not others
-    constexpr bool kLate = TREE && D == 256;  // (no registers for both there: the last tiles, one after the other)
-    if constexpr (!kLate) load_k(it, at2, g);
+    if constexpr (!kOne) load_k(it, at2, g);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt < nrt) {
         if (it.bad(page)) row[rt].l = __builtin_nanf("");
         u32x4 p[2];
         soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p);
-        if constexpr (TREE) gather_tree([&](int d) { return g.v[d]; }, token_mask(it, t), p, row[rt]);
-        else gather([&](int d) { return g.v[d]; }, p, row[rt]);
+        if constexpr (TREE) {
+          gather_tree([&](int d) { return g.v[d]; }, token_mask(it, t), p, row[rt]);
+        } else {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            row[rt].o[d] = O::mfma(g.v[d], p[0], row[rt].o[d]);
+            row[rt].o[d] = O::mfma(g.v[d], p[1], row[rt].o[d]);
+            if constexpr (kOne) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (d & 1) {
+                g.k[0][d >> 1] = piece(it.k, at2, d >> 1);
+                g.k[1][d >> 1] = piece(it.k, at2, NC + (d >> 1));
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (kLate) load_k(it, at2, g);
-    load_v(it, at2, g);
+    if constexpr (!kOne) load_v(it, at2, g);
+    else if constexpr (TREE) load_k(it, at2, g);
   }
   // Tiles t, t + kWaves, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
   SVG_DEV static void walk_thin(const Item& it, int t, int last, Regs& g, Pages& pages, int page, const char* qs, Row (&row)[RT],
@@ -894,15 +912,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
       }
       typename A::Regs regs;
       int my_page = 0;
-      auto request = [&] {
-        if (mine <= last) {
-          my_page = pages.at(it, mine);
-          const size_t at = A::tile_at(it, mine, my_page);
-          A::load_k(it, at, regs);
-          A::load_v(it, at, regs);
-        }
-      };
-      if constexpr (D < 256) request();
+      if (mine <= last) {
+        my_page = pages.at(it, mine);
+        const size_t at = A::tile_at(it, mine, my_page);
+        A::load_k(it, at, regs);
+        if constexpr (!A::kOne) A::load_v(it, at, regs);
+      }
       if (splits) {
         const int e = A::exponent_of(row_max(largest));
         u32x4 parts_of[NQ];
@@ -911,10 +926,6 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
         for (int p = 0; p < NQ; ++p)
           *reinterpret_cast<u32x4*>(lds + ((my_rt * NC + my_c) * NQ + p) * 1024 + lane * 16) = parts_of[p];
         if (my_c == 0 && g == 0) factor[my_rt][n] = unit * A::two_to(e);
-      }
-      if constexpr (D == 256) {  // (no registers for a tile beside q)
-        __builtin_amdgcn_sched_barrier(0);
-        request();
       }
       root_paths();
       __syncthreads();
