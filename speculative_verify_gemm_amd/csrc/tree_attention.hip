@@ -535,7 +535,7 @@ struct Attn {
 
   // ------------------------------------------------------------------- thin
   // dim 256 has registers for one of them: values are requested as the keys are used, keys as the values are
-  static constexpr bool kOne = D == 256;
+  static constexpr bool kOne = D * RT >= 256;
   struct Regs {
     u32x4 k[2][NC], v[ND];
   };
@@ -556,64 +556,85 @@ struct Attn {
   template <bool TREE>
   SVG_DEV static void thin_tile(const Item& it, int t, int t2, Regs& g, int page, int page2, const char* ql, Row (&row)[RT], int nrt,
                                 const u32 (&seen)[RT], u32 broken) {
-    static_assert(!kOne || RT == 1, "the keys are given up by the only row tile");
     asm volatile("" : "+v"(ql));  // q is read again for every tile, not kept
-    const size_t at = tile_at(it, t, page);
+    const size_t at = tile_at(it, t, page), at2 = tile_at(it, t2, page2);
     f32x4 s[RT][2];
+    auto scores = [&](int rt, int c) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (rt < nrt) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            const u32x4 q = *reinterpret_cast<const u32x4*>(ql + ((rt * NC + c) * NQ + n) * 1024);
-            s[rt][0] = O::mfma(g.k[0][c], q, s[rt][0]);
-            s[rt][1] = O::mfma(g.k[1][c], q, s[rt][1]);
-            if constexpr (kOne) {
-              __builtin_amdgcn_sched_barrier(0);
-              if (n == NQ - 1) {
-                g.v[2 * c] = piece(it.v, at, 2 * c);
-                g.v[2 * c + 1] = piece(it.v, at, 2 * c + 1);
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            }
-          }
+      for (int n = 0; n < NQ; ++n) {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(ql + ((rt * NC + c) * NQ + n) * 1024);
+        s[rt][0] = O::mfma(g.k[0][c], q, s[rt][0]);
+        s[rt][1] = O::mfma(g.k[1][c], q, s[rt][1]);
+        if constexpr (kOne) __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    const size_t at2 = tile_at(it, t2, page2);
-    __builtin_amdgcn_sched_barrier(0);  // the next keys take these keys' registers, not others
-    if constexpr (!kOne) load_k(it, at2, g);
+    };
+    u32x4 p[RT][2];
+    auto weights = [&](int rt) {
+      if (it.bad(page)) row[rt].l = __builtin_nanf("");
+      soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p[rt]);
+    };
+    auto sum = [&](int rt, int d) {
+      row[rt].o[d] = O::mfma(g.v[d], p[rt][0], row[rt].o[d]);
+      row[rt].o[d] = O::mfma(g.v[d], p[rt][1], row[rt].o[d]);
+    };
+    auto sum_tree = [&](int rt) { gather_tree([&](int d) { return g.v[d]; }, token_mask(it, t), p[rt], row[rt]); };
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      if (rt < nrt) {
-        if (it.bad(page)) row[rt].l = __builtin_nanf("");
-        u32x4 p[2];
-        soften<TREE>(it, t, s[rt], row[rt], seen[rt], (broken >> rt) & 1u, p);
-        if constexpr (TREE) {
-          gather_tree([&](int d) { return g.v[d]; }, token_mask(it, t), p, row[rt]);
-        } else {
+    for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (kOne) {
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            row[rt].o[d] = O::mfma(g.v[d], p[0], row[rt].o[d]);
-            row[rt].o[d] = O::mfma(g.v[d], p[1], row[rt].o[d]);
-            if constexpr (kOne) {
-              __builtin_amdgcn_sched_barrier(0);
-              if (d & 1) {
-                g.k[0][d >> 1] = piece(it.k, at2, d >> 1);
-                g.k[1][d >> 1] = piece(it.k, at2, NC + (d >> 1));
-                __builtin_amdgcn_sched_barrier(0);
-              }
-            }
-          }
+      for (int c = 0; c < NC; ++c) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) scores(rt, c);
+        g.v[2 * c] = piece(it.v, at, 2 * c);
+        g.v[2 * c + 1] = piece(it.v, at, 2 * c + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        weights(rt);
+        if constexpr (TREE) sum_tree(rt);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (TREE) {
+        load_k(it, at2, g);
+        return;
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sum(rt, d);
+        __builtin_amdgcn_sched_barrier(0);
+        if (d & 1) {
+          g.k[0][d >> 1] = piece(it.k, at2, d >> 1);
+          g.k[1][d >> 1] = piece(it.k, at2, NC + (d >> 1));
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
+    } else {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (rt < nrt) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) scores(rt, c);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_k(it, at2, g);  // (these keys' registers, not others)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        if (rt < nrt) {
+          weights(rt);
+          if constexpr (TREE) {
+            sum_tree(rt);
+          } else {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) sum(rt, d);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      load_v(it, at2, g);
     }
-    if constexpr (!kOne) load_v(it, at2, g);
-    else if constexpr (TREE) load_k(it, at2, g);
   }
   // Tiles t, t + kWaves, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
   SVG_DEV static void walk_thin(const Item& it, int t, int last, Regs& g, Pages& pages, int page, const char* qs, Row (&row)[RT],
