@@ -59,7 +59,9 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
 // takes.  A workgroup gets kMinThin / kMinThick units at least.
-constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 9, kMinThick = 2;
+constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 7, kMinThick = 2;
+
+constexpr int kAloneFrom = 256, kAloneItem = 5, kAloneGain = 15, kAloneRow = 2048;
 
 // Row tiles of an item that is walked the thin way.
 template <int D>
@@ -130,7 +132,7 @@ struct Plan {
   int cum[kMaxSlots + 1];   // units of an item of each slot before s (own tokens), added up
   int len[kMaxSlots];       // committed tokens; -1: not a valid slot
   int nodes[kMaxSlots];
-  int red[4][kWaves];
+  int red[5][kWaves];
 };
 // The part of it that every wave keeps in scalar registers.  (Units are below 2^31: the host has seen to that.)
 struct Deal {
@@ -138,6 +140,7 @@ struct Deal {
   u32 total, units_p;       // units of the launch, of the prefix items
   u32 groups;               // workgroups that take part: w has the units from start(w) on
   u32 quot, rest;           // total / groups
+  u32 alone;                // units of a slot item that one wave works on alone (0: a workgroup does)
   SVG_DEV u32 start(u32 w) const { return w * quot + w * rest / groups; }
 };
 
@@ -178,6 +181,7 @@ SVG_DEV int wave_scan(int v) {
   return v + (lane < 16 ? 0 : (lane < 32 ? a : (lane < 48 ? b : c)));
 }
 
+template <bool ALONE>
 SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
   const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int said = a.shared != nullptr ? a.shared[0] : 0;
@@ -230,19 +234,35 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
   const int t1 = n[1] > 0 ? ((len[1] + n[1] - d.prefix + 31) >> 5) + a.item_cost : 0;
   const int upto = wave_scan(t0 + t1);
   if (lane == 63) p.red[3][wave] = upto;
+  if constexpr (ALONE) {
+    const int longest = -wave_min(t0 > t1 ? -t0 : -t1);
+    if (lane == 0) p.red[4][wave] = longest;
+  }
   __syncthreads();
-  int before = upto - t0 - t1, all = 0;
+  int before = upto - t0 - t1, all = 0, longest = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     const int t = p.red[3][w];
     if (w < wave) before += t;
     all += t;
+    if constexpr (ALONE) longest = longest > p.red[4][w] ? longest : p.red[4][w];
   }
   if (2 * tid < S) p.cum[2 * tid] = before;
   if (2 * tid + 1 < S) p.cum[2 * tid + 1] = before + t0;
   if (tid == 0) p.cum[S] = all;
   d.units_p = (a.kinds & kPrefix) && d.prefix > 0 ? (u32)(a.sh.items_p * ((d.prefix >> 5) + a.item_cost)) : 0u;
-  d.total = uniform(d.units_p + (a.kinds & kSlots ? (u32)(all * a.c.heads * a.sh.rb_s) : 0u));
+  u32 own = a.kinds & kSlots ? (u32)(all * a.c.heads * a.sh.rb_s) : 0u;
+  d.alone = 0;
+  if constexpr (ALONE) {
+    const int items = S * a.c.heads;
+    if (own > 0 && kAloneItem * ((items + kAloneRow - 1) / kAloneRow) + longest - a.item_cost <=
+                       items * kAloneGain / 256 + all * a.c.heads / kAloneRow) {
+      const int each = (all + S - 1) / S - a.item_cost + kAloneItem;
+      d.alone = uniform(each > 1 ? (u32)each : 1u);
+      own = (u32)items * d.alone;
+    }
+  }
+  d.total = uniform(d.units_p + own);
   const u32 want = (d.total + a.min_units - 1) / (u32)a.min_units;
   d.groups = uniform(want < 1 ? 1 : (want < (u32)a.groups ? want : (u32)a.groups));
   d.quot = uniform(d.total / d.groups);
@@ -329,6 +349,13 @@ SVG_DEV void wait_loads() {
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
   asm volatile("" ::: "memory");
 }
+// What the wave's lanes have written to LDS is there for its other lanes, and what they have read is read.
+SVG_DEV void wave_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
 SVG_DEV void barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
@@ -386,6 +413,7 @@ struct Attn {
   static constexpr int TW = D < 256 ? 2 : 1, RW = kWaves / TW, STEPS = 3;
   static constexpr int RING = STEPS * TW * TILE;
   static_assert(RT * NC <= kWaves, "a wave splits one chunk of q");
+  static constexpr int SOLO = QBYTES * kWaves <= 128 * 1024 ? kWaves : 128 * 1024 / QBYTES;  // thin: waves that work alone
   static_assert(RW * JOIN <= RING || TW == 1, "the join of the token waves takes the ring's place");
 
   struct Row {                 // per lane: row n = lane % 16 of a row tile
@@ -636,17 +664,17 @@ struct Attn {
       load_v(it, at2, g);
     }
   }
-  // Tiles t, t + kWaves, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
-  SVG_DEV static void walk_thin(const Item& it, int t, int last, Regs& g, Pages& pages, int page, const char* qs, Row (&row)[RT],
+  // Tiles t, t + step, ... up to `last`: the committed tokens' tiles, then those with tree tokens.
+  SVG_DEV static void walk_thin(const Item& it, int t, int step, int last, Regs& g, Pages& pages, int page, const char* qs, Row (&row)[RT],
                                 int nrt, const u32 (&seen)[RT], u32 broken) {
     const char* ql = qs + (threadIdx.x & 63u) * 16u;
-    for (; t <= last && t * 32 + 32 <= it.len; t += kWaves) {
-      const int t2 = t + kWaves <= last ? t + kWaves : last, page2 = pages.at(it, t2);
+    for (; t <= last && t * 32 + 32 <= it.len; t += step) {
+      const int t2 = t + step <= last ? t + step : last, page2 = pages.at(it, t2);
       thin_tile<false>(it, t, t2, g, page, page2, ql, row, nrt, seen, broken);
       page = page2;
     }
-    for (; t <= last; t += kWaves) {
-      const int t2 = t + kWaves <= last ? t + kWaves : last, page2 = pages.at(it, t2);
+    for (; t <= last; t += step) {
+      const int t2 = t + step <= last ? t + step : last, page2 = pages.at(it, t2);
       thin_tile<true>(it, t, t2, g, page, page2, ql, row, nrt, seen, broken);
       page = page2;
     }
@@ -780,19 +808,24 @@ struct Attn {
   }
 };
 
-// RTHIN: row tiles of the thin way, 0: the thick way.
-template <int D, bool BF, int RTHIN>
+template <bool X>
+struct Is {
+  static constexpr bool value = X;
+};
+
+// RTHIN: row tiles of the thin way, 0: the thick way.  ALONE: slot items may be worked on by single waves.
+template <int D, bool BF, int RTHIN, bool ALONE>
 __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   constexpr bool THIN = RTHIN > 0;
   constexpr int RT = THIN ? RTHIN : (D < 256 ? 2 : 1);
   using A = Attn<D, BF, RT>;
   constexpr int NC = A::NC, ND = A::ND, NQ = A::NQ;
   __shared__ Plan plan;
-  __shared__ __attribute__((aligned(1024))) char lds[THIN ? (A::QBYTES > kWaves * A::JOIN ? A::QBYTES : kWaves * A::JOIN) : A::RING];
+  __shared__ __attribute__((aligned(1024))) char lds[THIN ? (A::SOLO * A::QBYTES > kWaves * A::JOIN ? A::SOLO * A::QBYTES : kWaves * A::JOIN) : A::RING];
   __shared__ float stat[kWaves][RT][2][16];
   __shared__ float factor[RT][16];
   const Shape& sh = a.sh;
-  const Deal deal = make_plan(a, plan);
+  const Deal deal = make_plan<ALONE>(a, plan);
   const int wg = blockIdx.x;
   float* const stats = a.stats;
   float* const parts = a.parts;
@@ -802,11 +835,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float sign = a.scale < 0.f ? -1.f : 1.f;
   const float unit = fabsf(a.scale) * 1.44269504088896341f;
-  const u32 end = deal.start(wg + 1);
+  const u32 till = deal.start(wg + 1), end = ALONE && deal.alone && till > deal.units_p ? deal.units_p : till;
   u32 u = deal.start(wg);
   // the first item: its slot (a prefix item: -1), head, row block and the unit of it that u is
-  int s = -1, h, rb, off;
-  {
+  int s = -1, h = 0, rb = 0, off = 0;
+  if (u < end) {
     u32 v = u, j, units = (u32)((deal.prefix >> 5) + a.item_cost);
     int blocks = sh.rb_p;
     if (u >= deal.units_p) {
@@ -828,39 +861,29 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
     h = (int)uniform(blocks == 1 ? j : j / (u32)blocks);
     rb = (int)uniform(j) - h * blocks;
   }
-  bool more = false;
-  for (; u < end; more = true) {
-    if (more) {  // the next item in order: row blocks, heads, then the next slot that has units
-      off = 0;
-      if (++rb == (s < 0 ? sh.rb_p : sh.rb_s)) {
-        rb = 0;
-        if (++h == a.c.heads) {
-          h = 0;
-          do ++s;
-          while (plan.cum[s + 1] == plan.cum[s]);
-          s = __builtin_amdgcn_readfirstlane(s);
-        }
-      }
-    }
+  // An item, from its unit `off` on: by the workgroup, or (ALONE) a slot's by one wave alone.
+  auto work = [&](auto by_one) {
+    constexpr bool alone = decltype(by_one)::value;
     const bool prefix = s < 0;
     const int slot = prefix ? deal.first : s;
     const int tiles = __builtin_amdgcn_readfirstlane(prefix ? deal.prefix >> 5 : plan.cum[s + 1] - plan.cum[s] - a.item_cost);
     const int units = tiles + a.item_cost;
-    const int left = (int)(end - u), stop = left < units - off ? off + left : units;
+    const int left = (int)(end - u), stop = alone || left >= units - off ? units : off + left;
     const int t0 = off > a.item_cost ? off - a.item_cost : 0, t1 = stop - a.item_cost;
     const u32 item_end = u - off + units;
-    u += stop - off;
-    if (t1 <= t0) continue;  // the units of its start only
+    if (!alone) u += stop - off;
+    if (t1 <= t0) return;  // the units of its start only
     const int j = prefix ? h * sh.rb_p + rb : (s * a.c.heads + h) * sh.rb_s + rb;
-    const long place = prefix ? sh.slot_p(wg, j) : sh.slot_s(wg, j);
-    if (t0 == 0 && threadIdx.x == 0)
-      a.spans[prefix ? j : sh.items_p + j] = Span{wg, stop == units ? 1 : group_of(item_end - 1, deal) - wg + 1};
+    const int who = alone ? 0 : wg;
+    const long place = prefix ? sh.slot_p(who, j) : sh.slot_s(who, j);
+    if (t0 == 0 && (alone ? lane == 0 : threadIdx.x == 0))
+      a.spans[prefix ? j : sh.items_p + j] = Span{who, stop == units ? 1 : group_of(item_end - 1, deal) - wg + 1};
 
     const int nodes = plan.nodes[slot];
     const int block = prefix ? sh.block_p : sh.block_s;
     const int all_rows = prefix ? a.c.n_slots * a.T * a.G : nodes * a.G;
     const int rows = __builtin_amdgcn_readfirstlane(all_rows - rb * block < block ? all_rows - rb * block : block);
-    if (rows <= 0) continue;  // a row block behind a small tree's rows
+    if (rows <= 0) return;  // a row block behind a small tree's rows
     const int row_tiles = (rows + 15) >> 4;
 
     Item it;
@@ -916,50 +939,106 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
 
     // The rows' q first, then the first tiles: loads arrive in order, and q is worked on while the tiles come.
     if constexpr (THIN) {
-      const int mine = first + wave;  // this wave's first tile
+      const int mine = alone ? first : first + wave;  // this wave's first tile
       Pages pages;
       if (mine <= last) pages.start(it, mine, last);
-      // each wave splits one chunk of 32 values of one row tile
-      const int my_rt = wave / NC, my_c = wave % NC, my_idx = my_rt * 16 + n;
-      const bool splits = wave < RT * NC;
-      f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
-      float largest = 0.f;
-      if (splits) {
-        const float* qp = q_of(my_idx);
-        x = at4(qp + 32 * my_c);
-        y = at4(qp + 32 * my_c + 4);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) largest = top8(qp + 32 * i, largest);
-      }
       typename A::Regs regs;
       int my_page = 0;
-      if (mine <= last) {
-        my_page = pages.at(it, mine);
-        const size_t at = A::tile_at(it, mine, my_page);
-        A::load_k(it, at, regs);
-        if constexpr (!A::kOne) A::load_v(it, at, regs);
-      }
-      if (splits) {
-        const int e = A::exponent_of(row_max(largest));
+      auto request = [&] {
+        if (mine <= last) {
+          my_page = pages.at(it, mine);
+          const size_t at = A::tile_at(it, mine, my_page);
+          A::load_k(it, at, regs);
+          if constexpr (!A::kOne) A::load_v(it, at, regs);
+        }
+      };
+      char* const qs = lds + (alone ? wave * A::QBYTES : 0);
+      float scale[RT];
+      auto put = [&](int rt, int c, const f32x4 x, const f32x4 y, float by) {
         u32x4 parts_of[NQ];
-        A::split8(x, y, my_idx < rows ? A::two_to(-e) * sign : 0.f, parts_of);
+        A::split8(x, y, by, parts_of);
 #pragma unroll
-        for (int p = 0; p < NQ; ++p)
-          *reinterpret_cast<u32x4*>(lds + ((my_rt * NC + my_c) * NQ + p) * 1024 + lane * 16) = parts_of[p];
-        if (my_c == 0 && g == 0) factor[my_rt][n] = unit * A::two_to(e);
+        for (int p = 0; p < NQ; ++p) *reinterpret_cast<u32x4*>(qs + ((rt * NC + c) * NQ + p) * 1024 + lane * 16) = parts_of[p];
+      };
+      if constexpr (alone) {  // a row tile of q after the other
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int idx = rt * 16 + n;
+          const float* qp = q_of(idx);
+          f32x4 raw[2 * NC];
+#pragma unroll
+          for (int i = 0; i < NC; ++i) {
+            raw[2 * i] = at4(qp + 32 * i);
+            raw[2 * i + 1] = at4(qp + 32 * i + 4);
+          }
+          if (rt == RT - 1) request();
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2 * NC; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(raw[i][k]));
+          const int e = A::exponent_of(row_max(top));
+          scale[rt] = unit * A::two_to(e);
+          const float by = idx < rows ? A::two_to(-e) * sign : 0.f;
+#pragma unroll
+          for (int i = 0; i < NC; ++i) put(rt, i, raw[2 * i], raw[2 * i + 1], by);
+        }
+        root_paths();
+        wave_sync();
+      } else {
+        // each wave splits one chunk of 32 values of one row tile
+        const int my_rt = wave / NC, my_c = wave % NC, my_idx = my_rt * 16 + n;
+        const bool splits = wave < RT * NC;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x;
+        float largest = 0.f;
+        if (splits) {
+          const float* qp = q_of(my_idx);
+          x = at4(qp + 32 * my_c);
+          y = at4(qp + 32 * my_c + 4);
+#pragma unroll
+          for (int i = 0; i < NC; ++i) largest = top8(qp + 32 * i, largest);
+        }
+        request();
+        if (splits) {
+          const int e = A::exponent_of(row_max(largest));
+          put(my_rt, my_c, x, y, my_idx < rows ? A::two_to(-e) * sign : 0.f);
+          if (my_c == 0 && g == 0) factor[my_rt][n] = unit * A::two_to(e);
+        }
+        root_paths();
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) scale[rt] = factor[rt][n];
       }
-      root_paths();
-      __syncthreads();
       typename A::Row row[RT];
       u32 seen[RT], bad = 0;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        row[rt].start(factor[rt][n]);
+        row[rt].start(scale[rt]);
         const int node = node_of(rt * 16 + n) & 31;
         seen[rt] = (u32)__shfl((int)path, node);
         if (__shfl((int)broken, node)) bad |= 1u << rt;
       }
-      if (mine <= last) A::walk_thin(it, mine, last, regs, pages, my_page, lds, row, row_tiles, seen, bad);
+      if (mine <= last) A::walk_thin(it, mine, alone ? 1 : kWaves, last, regs, pages, my_page, qs, row, row_tiles, seen, bad);
+      if constexpr (alone) {  // nothing to join
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          typename A::Row& r = row[rt];
+          const int idx = rt * 16 + n;
+          r.l += lane_xorf<16>(r.l);
+          r.l += lane_xorf<32>(r.l);
+          if (idx < rows) {
+            float* po = parts + (size_t)(place + idx) * D + 4 * g;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(po + 16 * d) = r.o[d];
+            if (g == 0) {
+              stats[2 * (place + idx)] = r.top();
+              stats[2 * (place + idx) + 1] = r.l;
+            }
+          }
+        }
+        wave_sync();
+        return;
+      }
 
       // join the waves: maxima first, then every thread adds the waves' values of its places
       float top[RT];
@@ -1109,6 +1188,33 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
       }
       __syncthreads();  // LDS is free again
     }
+  };
+  for (bool more = false; u < end; more = true) {
+    if (more) {  // the next item in order: row blocks, heads, then the next slot that has units
+      off = 0;
+      if (++rb == (s < 0 ? sh.rb_p : sh.rb_s)) {
+        rb = 0;
+        if (++h == a.c.heads) {
+          h = 0;
+          do ++s;
+          while (plan.cum[s + 1] == plan.cum[s]);
+          s = __builtin_amdgcn_readfirstlane(s);
+        }
+      }
+    }
+    work(Is<false>{});
+  }
+  if constexpr (ALONE) {
+    if (deal.alone == 0 || wave >= A::SOLO) return;
+    // the items whose first unit is this workgroup's
+    const u32 from = deal.start(wg) > deal.units_p ? deal.start(wg) - deal.units_p : 0u, to = till > deal.units_p ? till - deal.units_p : 0u;
+    const int behind = (int)uniform((to + deal.alone - 1) / deal.alone);
+    rb = off = 0;
+    for (int next = (int)uniform((from + deal.alone - 1) / deal.alone) + wave; next < behind; next += A::SOLO) {
+      s = (int)uniform((u32)next / (u32)a.c.heads);
+      h = next - s * a.c.heads;
+      work(Is<true>{});
+    }
   }
 }
 
@@ -1192,9 +1298,12 @@ void launch_items(AttnArgs a, int kinds, long rows, hipStream_t stream) {
   a.min_units = thin ? kMinThin : kMinThick;
   a.item_cost = thin ? kItemThin : kItemThick;
   const dim3 grid(a.groups), threads(kThreads);
-  if (rows <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1>), grid, threads, 0, stream, a);
-  else if (thin) hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>>), grid, threads, 0, stream, a);
-  else hipLaunchKernelGGL((k_tree_attention<D, BF, 0>), grid, threads, 0, stream, a);
+  const bool many = (kinds & kSlots) && a.c.n_slots * a.c.heads >= kAloneFrom;
+  if (!thin) hipLaunchKernelGGL((k_tree_attention<D, BF, 0, false>), grid, threads, 0, stream, a);
+  else if (rows <= 16 && many) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, true>), grid, threads, 0, stream, a);
+  else if (rows <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, false>), grid, threads, 0, stream, a);
+  else if (many) hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>, false>), grid, threads, 0, stream, a);
 }
 
 template <int D, bool BF>
