@@ -1218,16 +1218,20 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   }
 }
 
-// One wave per output row (query head x, node y, slot z of the grid) joins its partials, in the order of the workgroups:
-// D / 4 lanes read one partial's O, the wave 256 / D of them at a time.
-constexpr int kJoinThreads = 256;
+// W waves per output row (query head, node y, slot z of the grid) join its partials, in an order that the launch alone
+// decides: D / 4 lanes read one partial's O, a wave 256 / D of them at a time.
+constexpr int kJoinMany = 40;
 
-template <int D>
-__global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a) {
+template <int W>
+constexpr int kJoinThreads = W > 1 ? 64 * W : 256;
+
+template <int D, int W>
+__global__ __launch_bounds__(kJoinThreads<W>) void k_tree_attention_join(AttnArgs a) {
   const Shape& sh = a.sh;
   constexpr int L = D / 4, NP = 64 / L;  // lanes of a partial, partials at a time
   const int lane = threadIdx.x & 63, i = blockIdx.y, s = blockIdx.z;
-  const int head = blockIdx.x * (kJoinThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int head = W > 1 ? blockIdx.x : blockIdx.x * (kJoinThreads<1> / 64) + wave;
   if (head >= a.c.heads * a.G) return;
   const int h = a.node_of(head), gq = head - h * a.G;
   const int r_p = (s * a.T + i) * a.G + gq, r_s = i * a.G + gq;           // rows of a prefix item, of the slot's
@@ -1240,7 +1244,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a
   float* out = a.out + ((size_t)(s * a.T + i) * (a.c.heads * a.G) + head) * D + 4 * (lane % L);
   if (len < 0) {
     const float nan = __builtin_nanf("");
-    if (lane < L) *reinterpret_cast<f32x4*>(out) = f32x4{nan, nan, nan, nan};
+    if (lane < L && (W == 1 || wave == 0)) *reinterpret_cast<f32x4*>(out) = f32x4{nan, nan, nan, nan};
     return;
   }
   const int np = prefix > 0 ? sp.count : 0, all = np + ss.count;
@@ -1251,12 +1255,13 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a
   float m = kLowest, l = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
   constexpr int U = 8;  // requests in flight a lane
-  for (int k0 = lane / L; k0 < all; k0 += NP * U) {
+  constexpr int STEP = NP * W;
+  for (int k0 = (W > 1 ? wave * NP : 0) + lane / L; k0 < all; k0 += STEP * U) {
     float pm[U], pl[U];
     f32x4 po[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * NP;
+      const int k = k0 + u * STEP;
       const long row = row_of(k < all ? k : k0);
       pm[u] = stats[2 * row];
       pl[u] = stats[2 * row + 1];
@@ -1265,7 +1270,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (k0 + u * NP >= all) { pm[u] = kLowest; pl[u] = 0.f; po[u] = f32x4{0.f, 0.f, 0.f, 0.f}; }
+      if (k0 + u * STEP >= all) { pm[u] = kLowest; pl[u] = 0.f; po[u] = f32x4{0.f, 0.f, 0.f, 0.f}; }
       top = fmaxf(top, pm[u]);
     }
     const float w0 = __builtin_amdgcn_exp2f(m - top);
@@ -1287,6 +1292,27 @@ __global__ __launch_bounds__(kJoinThreads) void k_tree_attention_join(AttnArgs a
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = o[e] * w1 + __shfl_xor(o[e], off) * w2;
     m = top;
+  }
+  if constexpr (W > 1) {
+    __shared__ float stat[W][2];
+    __shared__ f32x4 part[W][L];
+    if (lane < L) part[wave][lane] = o;
+    if (lane == 0) {
+      stat[wave][0] = m;
+      stat[wave][1] = l;
+    }
+    __syncthreads();
+    if (wave > 0 || lane >= L) return;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, stat[w][0]);
+    l = 0.f;
+    o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float by = __builtin_amdgcn_exp2f(stat[w][0] - m);
+      l += stat[w][1] * by;
+      o += part[w][lane] * by;
+    }
   }
   if (lane < L) *reinterpret_cast<f32x4*>(out) = o / l;
 }
@@ -1316,9 +1342,15 @@ void launch(const AttnArgs& a, hipStream_t stream) {
   } else {
     launch_items<D, BF>(a, kPrefix | kSlots, rows_p, stream);
   }
-  constexpr int per = kJoinThreads / 64;
-  hipLaunchKernelGGL((k_tree_attention_join<D>), dim3((a.c.heads * a.G + per - 1) / per, a.T, a.c.n_slots), dim3(kJoinThreads), 0,
-                     stream, a);
+  // partials that a row of the longest items may have: as many as the device has workgroups for an item, as the table has tiles for
+  const int items = a.c.heads * (a.shared != nullptr ? a.sh.rb_p : a.c.n_slots * a.sh.rb_s), q_heads = a.c.heads * a.G;
+  const long tiles = (long)a.c.width * a.c.page / 32, few = rows_p <= 16 * kThinTiles<D> ? kMinThin : kMinThick;
+  constexpr int per = kJoinThreads<1> / 64;
+  if (a.groups >= kJoinMany * items && tiles >= kJoinMany * few)
+    hipLaunchKernelGGL((k_tree_attention_join<D, 8>), dim3(q_heads, a.T, a.c.n_slots), dim3(kJoinThreads<8>), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_tree_attention_join<D, 1>), dim3((q_heads + per - 1) / per, a.T, a.c.n_slots), dim3(kJoinThreads<1>), 0,
+                       stream, a);
 }
 
 }  // namespace
