@@ -352,3 +352,81 @@ def test_the_binding_checks_its_tensors():
         svg.kv_fork(cache, i32([0, 0]), cache)
     with pytest.raises(ValueError):
         svg.kv_reserve(cache, i32([1, 1]), i32([0, 0]), svg.kv_workspace(cache)[:-1])
+
+
+@pytest.mark.parametrize("lens,common,T,H,G,dim,page,kind", [
+    ([(5 * s) % 70 for s in range(64)], 0, 1, 8, 4, 128, 64, "fp16"),         # a row tile, tokens in one to three tiles
+    ([(7 * s) % 50 for s in range(300)], 0, 1, 8, 2, 64, 32, "bf16"),         # more heads of slots than the device has waves
+    ([(11 * s) % 120 for s in range(40)], 0, 5, 8, 4, 128, 32, "bf16"),       # two row tiles
+    ([(3 * s) % 90 for s in range(64)], 0, 2, 4, 8, 256, 32, "bf16"),
+    ([130 + s for s in range(32)], 128, 1, 8, 1, 64, 32, "fp16"),             # branches with the prefix in the same launch
+    ([64 + s % 3 for s in range(70)], 64, 2, 4, 4, 128, 64, "fp16"),          # and in a launch of its own
+    ([2500] + [3] * 63, 0, 1, 4, 4, 64, 128, "fp16"),                         # one long slot among short ones
+    ([0] * 256, 0, 1, 1, 8, 128, 32, "fp16"),
+])
+def test_many_slots_of_few_tokens(lens, common, T, H, G, dim, page, kind):
+    C.say(f"tree_attention {len(lens)} slots, shared {common} T={T} H={H} G={G} dim={dim} {kind}")
+    rng = np.random.default_rng(dim + T + len(lens))
+    S = len(lens)
+    c = K.make(S, lens, T, H=H, dim=dim, page=page)
+    fill(c, rng, kind)
+    share(c, 1, common)
+    parent = trees(rng, S, T)
+    q, qd = queries(rng, S, T, H * G, dim)
+    n = [T - (s % 3 if s % 4 == 2 else 0) for s in range(S)]
+    n = [max(x, 0) for x in n]
+    n[7] = 0
+    ref, spread = AO.attention(c, wide(kind), 0, q, parent, T, n, dim ** -0.5)
+    tol = bound(c, kind, spread, max(lens) + T)
+    d = K.copy_of(c)
+    d["pages"][3] = 0                                # a slot without pages, one with a page outside the cache
+    ref[3] = np.nan
+    last = (lens[9] + n[9] - 1) // page
+    d["table"][9, last] = 10 ** 8
+    ref[9, :n[9]] = np.nan
+    if T > 1:
+        parent[10, 1] = 1
+        ref[10, [i for i in range(T) if i == 1 or path_has(parent[10], i, 1)]] = np.nan
+    cache = K.to_library(svg, d, kind)
+    ws = svg.tree_attention_workspace(cache, H * G, T).fill_(0xFF)
+    for _ in range(2):                               # the second time over the first one's workspace
+        got = run(cache, qd, parent, T, n_nodes=n, shared=common or None, workspace=ws)
+        for s in range(S):
+            assert np.all(got[s, n[s]:] == 7.0), s
+            close(got[s, :n[s]], ref[s, :n[s]], tol[s, :n[s]])
+
+
+def path_has(parent, i, node):
+    """Whether node i's path meets `node` before it ends."""
+    for _ in range(len(parent)):
+        if i == node:
+            return True
+        if i < 0 or parent[i] >= i:
+            return False
+        i = parent[i]
+    return False
+
+
+@pytest.mark.parametrize("lens,common,T,H,G,dim,page,kind", [
+    ([12000], 0, 1, 1, 4, 128, 128, "fp16"), ([9500], 0, 2, 1, 8, 256, 64, "bf16"), ([5000], 0, 16, 2, 8, 128, 64, "bf16"),
+    ([9100, 9000, 9300, 40], 0, 1, 1, 1, 64, 64, "fp16"), ([4200, 4101, 4300], 4096, 9, 1, 4, 256, 32, "fp16"),
+])
+def test_long_lists_of_partials(lens, common, T, H, G, dim, page, kind):
+    """Few heads and many tokens: every workgroup of the device holds a part of the same rows."""
+    C.say(f"tree_attention lens={lens} shared {common} T={T} H={H} G={G} dim={dim} {kind}")
+    rng = np.random.default_rng(dim + T)
+    c = K.make(dim, lens, T, H=H, dim=dim, page=page)
+    fill(c, rng, kind)
+    share(c, 0, common)
+    parent = trees(rng, len(lens), T)
+    q, qd = queries(rng, len(lens), T, H * G, dim)
+    ref, spread = AO.attention(c, wide(kind), 0, q, parent, T, None, dim ** -0.5)
+    tol = bound(c, kind, spread, max(lens) + T)
+    cache = K.to_library(svg, c, kind)
+    close(run(cache, qd, parent, T, shared=common or None), ref, tol)
+    if len(lens) > 1:
+        n = [T] * len(lens)
+        n[1], c["len"][2] = 0, -1
+        got = run(K.to_library(svg, c, kind), qd, parent, T, n_nodes=n, shared=common or None)
+        assert np.all(got[1] == 7.0) and np.isnan(got[2]).all()
+        close(got[0], ref[0], tol[0])
