@@ -59,7 +59,7 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
 // takes.  A workgroup gets kMinThin / kMinThick units at least.
-constexpr int kItemThin = 8, kItemThick = 4, kMinThin = 7, kMinThick = 2;
+constexpr int kItemThin = 12, kItemThick = 4, kMinThin = 7, kMinThick = 2;
 
 constexpr int kAloneFrom = 256, kAloneItem = 5, kAloneGain = 15, kAloneRow = 2048;
 
