@@ -63,6 +63,8 @@ constexpr int kItemThin = 12, kItemThick = 4, kMinThin = 7, kMinThick = 2;
 
 constexpr int kAloneFrom = 256, kAloneItem = 5, kAloneGain = 15, kAloneRow = 2048;
 
+constexpr int item_cost(bool thin) { return thin ? kItemThin : kItemThick; }
+
 // Row tiles of an item that is walked the thin way.
 template <int D>
 constexpr int kThinTiles = D < 256 ? 2 : 1;  // (dim 256: the accumulators of two do not fit)
@@ -98,8 +100,6 @@ struct Shape {
   size_t bytes(int dim) const { return parts_at() + (size_t)rows() * dim * 4; }
 };
 
-enum { kPrefix = 1, kSlots = 2 };
-
 struct AttnArgs {
   svg_kv_cache c;
   const float* q;
@@ -113,8 +113,6 @@ struct AttnArgs {
   float* parts;
   long ld_q;
   int layer, T, G, groups;
-  int min_units, item_cost;
-  int kinds;          // items of this launch: kPrefix, kSlots
   u32 over_g;         // 2^32 / G, rounded up (0: G = 1)
   Shape sh;
   float scale;
@@ -181,8 +179,10 @@ SVG_DEV int wave_scan(int v) {
   return v + (lane < 16 ? 0 : (lane < 32 ? a : (lane < 48 ? b : c)));
 }
 
-template <bool ALONE>
-SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
+template <int RTHIN, bool ALONE, bool BOTH>
+SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
+  constexpr int cost = item_cost(RTHIN > 0), cost_p = BOTH ? kItemThick : cost;
+  constexpr u32 least = RTHIN > 0 ? kMinThin : kMinThick, least_p = kMinThick;
   const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int said = a.shared != nullptr ? a.shared[0] : 0;
   // a slot with nodes whose tokens lie inside its pages is active; the others take no part.  Two slots a thread
@@ -230,8 +230,8 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
     d.first = __builtin_amdgcn_readfirstlane(first < S ? first : 0);
   }
   // units before each slot
-  const int t0 = n[0] > 0 ? ((len[0] + n[0] - d.prefix + 31) >> 5) + a.item_cost : 0;
-  const int t1 = n[1] > 0 ? ((len[1] + n[1] - d.prefix + 31) >> 5) + a.item_cost : 0;
+  const int t0 = n[0] > 0 ? ((len[0] + n[0] - d.prefix + 31) >> 5) + cost : 0;
+  const int t1 = n[1] > 0 ? ((len[1] + n[1] - d.prefix + 31) >> 5) + cost : 0;
   const int upto = wave_scan(t0 + t1);
   if (lane == 63) p.red[3][wave] = upto;
   if constexpr (ALONE) {
@@ -250,21 +250,44 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p) {
   if (2 * tid < S) p.cum[2 * tid] = before;
   if (2 * tid + 1 < S) p.cum[2 * tid + 1] = before + t0;
   if (tid == 0) p.cum[S] = all;
-  d.units_p = (a.kinds & kPrefix) && d.prefix > 0 ? (u32)(a.sh.items_p * ((d.prefix >> 5) + a.item_cost)) : 0u;
-  u32 own = a.kinds & kSlots ? (u32)(all * a.c.heads * a.sh.rb_s) : 0u;
+  d.units_p = uniform(d.prefix > 0 ? (u32)(a.sh.items_p * ((d.prefix >> 5) + cost_p)) : 0u);
+  u32 own = uniform((u32)(all * a.c.heads * a.sh.rb_s));
   d.alone = 0;
   if constexpr (ALONE) {
     const int items = S * a.c.heads;
-    if (own > 0 && kAloneItem * ((items + kAloneRow - 1) / kAloneRow) + longest - a.item_cost <=
+    if (own > 0 && kAloneItem * ((items + kAloneRow - 1) / kAloneRow) + longest - cost <=
                        items * kAloneGain / 256 + all * a.c.heads / kAloneRow) {
-      const int each = (all + S - 1) / S - a.item_cost + kAloneItem;
+      const int each = (all + S - 1) / S - cost + kAloneItem;
       d.alone = uniform(each > 1 ? (u32)each : 1u);
       own = (u32)items * d.alone;
     }
   }
+  u32 groups = (u32)a.groups, at_least = least;
+  if constexpr (BOTH) {
+    // the device is shared out between the prefix and the slots' own tokens by what either takes
+    u32 front = 0;
+    if (d.units_p > 0) {
+      const float w = (float)d.units_p * (RTHIN == 1 && a.c.dim < 256 ? 2.f : 1.5f);
+      front = (u32)((float)groups * w * __builtin_amdgcn_rcpf(w + (float)own) + 0.5f);
+      const u32 most = (d.units_p + least_p - 1) / least_p, room = own > 0 ? groups - 1 : groups;
+      front = front < most ? front : most;
+      front = front < room ? front : room;
+      front = uniform(front > 0 ? front : 1u);
+    }
+    if ((u32)wg < front) {
+      groups = front;
+      at_least = least_p;
+      own = 0;
+      d.alone = 0;
+    } else {
+      wg -= (int)front;
+      groups -= front;
+      d.units_p = 0;
+    }
+  }
   d.total = uniform(d.units_p + own);
-  const u32 want = (d.total + a.min_units - 1) / (u32)a.min_units;
-  d.groups = uniform(want < 1 ? 1 : (want < (u32)a.groups ? want : (u32)a.groups));
+  const u32 want = (d.total + at_least - 1) / at_least;
+  d.groups = uniform(want < 1 ? 1 : (want < groups ? want : groups));
   d.quot = uniform(d.total / d.groups);
   d.rest = d.total - d.quot * d.groups;
   __syncthreads();
@@ -813,24 +836,28 @@ struct Is {
   static constexpr bool value = X;
 };
 
-// RTHIN: row tiles of the thin way, 0: the thick way.  ALONE: slot items may be worked on by single waves.
+// LDS of either way: thin: q's parts, then the waves' O; thick: the ring of tiles.
+template <int D, bool BF, int RTHIN>
+constexpr int lds_bytes() {
+  using A = Attn<D, BF, RTHIN ? RTHIN : (D < 256 ? 2 : 1)>;
+  return RTHIN == 0 ? A::RING : (A::SOLO * A::QBYTES > kWaves * A::JOIN ? A::SOLO * A::QBYTES : kWaves * A::JOIN);
+}
+
+// The items of workgroup wg.  RTHIN: row tiles of the thin way, 0: the thick way.  ALONE: slot items may be worked on by
+// single waves.
 template <int D, bool BF, int RTHIN, bool ALONE>
-__global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
+SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, const int wg, char* const lds) {
   constexpr bool THIN = RTHIN > 0;
   constexpr int RT = THIN ? RTHIN : (D < 256 ? 2 : 1);
   using A = Attn<D, BF, RT>;
   constexpr int NC = A::NC, ND = A::ND, NQ = A::NQ;
-  __shared__ Plan plan;
-  __shared__ __attribute__((aligned(1024))) char lds[THIN ? (A::SOLO * A::QBYTES > kWaves * A::JOIN ? A::SOLO * A::QBYTES : kWaves * A::JOIN) : A::RING];
   __shared__ float stat[kWaves][RT][2][16];
   __shared__ float factor[RT][16];
   const Shape& sh = a.sh;
-  const Deal deal = make_plan<ALONE>(a, plan);
-  const int wg = blockIdx.x;
   float* const stats = a.stats;
   float* const parts = a.parts;
-  if (wg == 0 && threadIdx.x == 0) *a.header = deal.prefix;
-  if ((u32)wg >= deal.groups || deal.total == 0) return;
+  int cost = item_cost(THIN);
+  asm("" : "+s"(cost));  // (as a constant it makes the compiler spill 150 registers in the thick loop of 256 dims)
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float sign = a.scale < 0.f ? -1.f : 1.f;
@@ -840,7 +867,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   // the first item: its slot (a prefix item: -1), head, row block and the unit of it that u is
   int s = -1, h = 0, rb = 0, off = 0;
   if (u < end) {
-    u32 v = u, j, units = (u32)((deal.prefix >> 5) + a.item_cost);
+    u32 v = u, j, units = (u32)((deal.prefix >> 5) + cost);
     int blocks = sh.rb_p;
     if (u >= deal.units_p) {
       v -= deal.units_p;
@@ -866,10 +893,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
     constexpr bool alone = decltype(by_one)::value;
     const bool prefix = s < 0;
     const int slot = prefix ? deal.first : s;
-    const int tiles = __builtin_amdgcn_readfirstlane(prefix ? deal.prefix >> 5 : plan.cum[s + 1] - plan.cum[s] - a.item_cost);
-    const int units = tiles + a.item_cost;
+    const int tiles = __builtin_amdgcn_readfirstlane(prefix ? deal.prefix >> 5 : plan.cum[s + 1] - plan.cum[s] - cost);
+    const int units = tiles + cost;
     const int left = (int)(end - u), stop = alone || left >= units - off ? units : off + left;
-    const int t0 = off > a.item_cost ? off - a.item_cost : 0, t1 = stop - a.item_cost;
+    const int t0 = off > cost ? off - cost : 0, t1 = stop - cost;
     const u32 item_end = u - off + units;
     if (!alone) u += stop - off;
     if (t1 <= t0) return;  // the units of its start only
@@ -1218,6 +1245,24 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
   }
 }
 
+// All items the same way, or (BOTH) the shared prefix the thick way and the slots' own tokens the thin way.
+template <int D, bool BF, int RTHIN, bool ALONE, bool BOTH>
+__global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
+  __shared__ Plan plan;
+  constexpr int thin = lds_bytes<D, BF, RTHIN>(), thick = BOTH ? lds_bytes<D, BF, 0>() : 0;
+  __shared__ __attribute__((aligned(1024))) char lds[thin > thick ? thin : thick];
+  int wg = blockIdx.x;
+  const Deal deal = make_plan<RTHIN, ALONE, BOTH>(a, plan, wg);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.header = deal.prefix;
+  if ((u32)wg >= deal.groups || deal.total == 0) return;
+  if constexpr (BOTH) {
+    if (deal.units_p > 0) walk_items<D, BF, 0, false>(a, plan, deal, wg, lds);
+    else walk_items<D, BF, RTHIN, ALONE>(a, plan, deal, wg, lds);
+  } else {
+    walk_items<D, BF, RTHIN, ALONE>(a, plan, deal, wg, lds);
+  }
+}
+
 // W waves per output row (query head, node y, slot z of the grid) join its partials, in an order that the launch alone
 // decides: D / 4 lanes read one partial's O, a wave 256 / D of them at a time.
 constexpr int kJoinMany = 40;
@@ -1317,31 +1362,22 @@ __global__ __launch_bounds__(kJoinThreads<W>) void k_tree_attention_join(AttnArg
   if (lane < L) *reinterpret_cast<f32x4*>(out) = o / l;
 }
 
-template <int D, bool BF>
-void launch_items(AttnArgs a, int kinds, long rows, hipStream_t stream) {
-  a.kinds = kinds;
-  const bool thin = rows <= 16 * kThinTiles<D>;
-  a.min_units = thin ? kMinThin : kMinThick;
-  a.item_cost = thin ? kItemThin : kItemThick;
+template <int D, bool BF, bool ALONE>
+void launch_items(const AttnArgs& a, long rows_p, long rows_s, hipStream_t stream) {
   const dim3 grid(a.groups), threads(kThreads);
-  const bool many = (kinds & kSlots) && a.c.n_slots * a.c.heads >= kAloneFrom;
-  if (!thin) hipLaunchKernelGGL((k_tree_attention<D, BF, 0, false>), grid, threads, 0, stream, a);
-  else if (rows <= 16 && many) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, true>), grid, threads, 0, stream, a);
-  else if (rows <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, false>), grid, threads, 0, stream, a);
-  else if (many) hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>, true>), grid, threads, 0, stream, a);
-  else hipLaunchKernelGGL((k_tree_attention<D, BF, kThinTiles<D>, false>), grid, threads, 0, stream, a);
+  constexpr int most = kThinTiles<D>;
+  if (rows_p <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, ALONE, false>), grid, threads, 0, stream, a);
+  else if (rows_p <= 16 * most) hipLaunchKernelGGL((k_tree_attention<D, BF, most, ALONE, false>), grid, threads, 0, stream, a);
+  else if (a.groups < 2 || rows_s > 16 * most) hipLaunchKernelGGL((k_tree_attention<D, BF, 0, false, false>), grid, threads, 0, stream, a);
+  else if (rows_s <= 16) hipLaunchKernelGGL((k_tree_attention<D, BF, 1, ALONE, true>), grid, threads, 0, stream, a);
+  else hipLaunchKernelGGL((k_tree_attention<D, BF, most, ALONE, true>), grid, threads, 0, stream, a);
 }
 
 template <int D, bool BF>
 void launch(const AttnArgs& a, hipStream_t stream) {
-  // the shared prefix and the slots' own tokens: one launch where both are walked the same way
   const long rows_s = (long)a.T * a.G, rows_p = a.shared != nullptr ? a.c.n_slots * rows_s : rows_s;
-  if (rows_s <= 16 * kThinTiles<D> && rows_p > 16 * kThinTiles<D>) {
-    launch_items<D, BF>(a, kPrefix, rows_p, stream);
-    launch_items<D, BF>(a, kSlots, rows_s, stream);
-  } else {
-    launch_items<D, BF>(a, kPrefix | kSlots, rows_p, stream);
-  }
+  if (a.c.n_slots * a.c.heads >= kAloneFrom) launch_items<D, BF, true>(a, rows_p, rows_s, stream);
+  else launch_items<D, BF, false>(a, rows_p, rows_s, stream);
   // partials that a row of the longest items may have: as many as the device has workgroups for an item, as the table has tiles for
   const int items = a.c.heads * (a.shared != nullptr ? a.sh.rb_p : a.c.n_slots * a.sh.rb_s), q_heads = a.c.heads * a.G;
   const long tiles = (long)a.c.width * a.c.page / 32, few = rows_p <= 16 * kThinTiles<D> ? kMinThin : kMinThick;
@@ -1373,7 +1409,7 @@ hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const flo
   char* ws = static_cast<char*>(workspace);
   const AttnArgs a{c, q, parent, n_nodes, shared, out, reinterpret_cast<int*>(ws), reinterpret_cast<Span*>(ws + 256),
                    reinterpret_cast<float*>(ws + sh.stats_at()), reinterpret_cast<float*>(ws + sh.parts_at()), (long)ld_q,
-                   layer, T, G, cus < kMaxGroups ? cus : kMaxGroups, 0, 0, 0,
+                   layer, T, G, cus < kMaxGroups ? cus : kMaxGroups,
                    G == 1 ? 0u : (u32)(((1ull << 32) + G - 1) / G), sh, scale};
   const bool bf = c.type == SVG_BF16;
   if (c.dim == 64) {
