@@ -10,8 +10,8 @@
 // slots share, every row of every slot of a key/value head; for a slot's own
 // tokens, the rows of its tree (nodes x query heads of the group).  An item's tokens
 // are counted in tiles of 32; all tiles of all items, in order, are dealt out
-// evenly over the workgroups, so unequal lengths and few rows both fill the device.  A workgroup
-// writes one partial (O, M, sum) for each item it meets.  The lengths are read
+// evenly over the workgroups (one a CU), so unequal lengths and few rows both fill the
+// device.  A workgroup writes one partial (O, M, sum) for each item it meets.  The lengths are read
 // on the device: the same launch serves any lengths, also from a captured graph.
 //
 // Layout.  A page is laid out in the lane order of v_mfma_f32_16x16x32: S^T = K Q^T
@@ -20,14 +20,25 @@
 // first product's result registers into the second's operand registers with no
 // exchange: O^T += V^T P^T.  A wave reads a tile as contiguous KiB.
 //
-// Two ways over an item's tiles, by the rows that the launch's largest item may have:
-//  * thin (up to 16 RT rows: plain decoding, small trees): bound by the cache's
+// Ways over an item's tiles, by the rows that the launch's largest item may have:
+//  * thin (up to 32 rows, 16 of dim 256: plain decoding, small trees): bound by the cache's
 //    bytes.  Each of the eight waves takes every eighth tile for all the rows,
 //    keys and values straight into registers, the next tile's requested as
 //    soon as the registers are free; the waves' results are joined in LDS.
+//  * alone (many slots of few tokens): a thin item is one wave's, with no barrier and
+//    nothing to join; the eight waves of a workgroup work on eight items at once.
 //  * thick (more rows: large trees, shared prefixes): every tile is used by up to eight
-//    waves of 16 rows each.  It is brought into LDS once, by loads that go there
-//    directly and run STAGES - 1 tiles ahead, one barrier a tile.
+//    waves.  It is brought into LDS once, by loads that go there
+//    directly and run STEPS - 1 steps ahead, one barrier a step.  Bound by the matrix unit.
+// A shared prefix that is walked the thick way and slots that are walked the thin way are one launch.
+//
+// Measured (kernel, then join; us):
+//   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16        9.3 + 3.8   a chain of dependent loads
+//   16 nodes, 8206 seen, 32 heads of 128, fp16                        26.9 + 4.8   bytes: 134 MB, 5.0 TB/s
+//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16               154-170 + 6.6  products: 172 GFLOP in five
+//                                                                                  parts, 1.0-1.1 PFLOP/s; 537 MB
+//   32 slots of 2000 tokens behind 32768 shared, 8 heads for 32, fp16   69.9 + 5.8   bytes: 396 MB, 5.7 TB/s
+//   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16   25.5 + 6.5   a few tiles a workgroup: its start
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
 // two and split into 16-bit parts (two of fp16: 22 bits; three of bf16: 24 bits), one
@@ -38,7 +49,8 @@
 // The running maximum is raised only when a score passes it by more than
 // 2^kSlack: until then probabilities above 1 are kept as they are (their scale
 // 2^kLift leaves fp16 room: at most 2^(kLift + kSlack) = 2^15), which takes the
-// exchange between lanes and the rescaling of O out of almost every tile.
+// exchange between lanes and the rescaling of O out of almost every tile (raised at every
+// tile, the 131033 tokens above take 186 us).
 #include "svg_cache.h"
 #include "svg_internal.h"
 
@@ -58,16 +70,25 @@ constexpr float kLowest = -3.402823466e38f;
 // kFar that step would be felt as a factor, and far beyond it would overflow: 2^(f (s - m) + kLift) then.
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
-// takes.  A workgroup gets kMinThin / kMinThick units at least.
+// takes (thin, 8 heads of 128: 32 slots of 2000 tokens 33.3 us, with 8: 35.4, with 24: 34.5, with 4: 41; 8 slots of
+// 3000 with 4 nodes 21.6, 22.9, 21.2, 24.6.  Thick: 2 to 8 are alike).  A workgroup gets kMinThin / kMinThick units at
+// least: fewer workgroups have fewer partials to join (1000 tokens 13.0 us, with 16: 14.6, with 5: 12.9; 7656 tokens of
+// dim 256 29, with 5: 36; thick, 500 tokens of 32 heads 17.6 us, with 8: 24.4).
 constexpr int kItemThin = 12, kItemThick = 4, kMinThin = 7, kMinThick = 2;
 
+// Slot items are worked on alone where that is expected to take less time (in tiles of a wave): kAloneItem and the
+// longest slot's tiles against the joins that are saved, kAloneGain for each item of a workgroup, and the item's
+// tiles over the whole device.  8 heads of 128, one token, alone / not: 64 slots of 100 tokens 14.3 / 23.2 us, 128 of
+// 400 32 / 48, 32 of 300 17.2 / 19.3, 64 of 600 29 / 32, 64 of 1000 40.4 / 39.3.  Kernels that can do it are only taken
+// from kAloneFrom items on: below, the few calls that gained (16.5 -> 15.0 us) did not outweigh 1 us that all others lost.
 constexpr int kAloneFrom = 256, kAloneItem = 5, kAloneGain = 15, kAloneRow = 2048;
 
 constexpr int item_cost(bool thin) { return thin ? kItemThin : kItemThick; }
 
-// Row tiles of an item that is walked the thin way.
+// Row tiles of an item that is walked the thin way (dim 256: the accumulators of two do not fit).  32 rows of 8 heads of
+// 128, thin / thick: 32768 tokens 36.9 / 46.8 us, 8000 tokens 22.6 / 24.8 us.
 template <int D>
-constexpr int kThinTiles = D < 256 ? 2 : 1;  // (dim 256: the accumulators of two do not fit)
+constexpr int kThinTiles = D < 256 ? 2 : 1;
 
 // What the second launch has to know of an item: the workgroups that wrote partials of it.
 struct Span {
@@ -264,7 +285,9 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   }
   u32 groups = (u32)a.groups, at_least = least;
   if constexpr (BOTH) {
-    // the device is shared out between the prefix and the slots' own tokens by what either takes
+    // The device is shared out between the prefix and the slots' own tokens by what either takes; a thick tile counts
+    // as 2 thin ones where one row tile of up to 128 dims is thin, else 1.5 (32 branches of 2000 tokens behind 32768
+    // 72.5 us, with 1.5: 74, with 3: 75, with 4: 87; 24 trees of 8 nodes and 300 tokens behind 2048, two row tiles, 45.5 us, with 3: 54)
     u32 front = 0;
     if (d.units_p > 0) {
       const float w = (float)d.units_p * (RTHIN == 1 && a.c.dim < 256 ? 2.f : 1.5f);
@@ -388,7 +411,8 @@ SVG_DEV void barrier() {
 // wave.  In asm: the compiler would wait for all of them before it reads any LDS; here wait_loads() and the
 // barrier say what has arrived.
 SVG_DEV void load_to_lds(const char* from, u32 lane16, u32 to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane16), "s"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane16), "s"(from) : "memory");
 }
 // Bytes of LDS before p.
 SVG_DEV u32 lds_at(const char* p) { return (u32)(uintptr_t)(const __attribute__((address_space(3))) char*)p; }
@@ -548,7 +572,8 @@ struct Attn {
     }
     return keep;
   }
-  // O += V^T P^T for a tile with tree tokens, val(d) the values of columns 16 d ..  Values that are not finite are left out of the product (0 times them
+  // O += V^T P^T for a tile with tree tokens, val(d) the values of columns 16 d ..  Values that are not finite are left
+  // out of the product (0 times them
   // would be NaN in every row) and make NaN where a row has a share of them.
   template <class F>
   SVG_DEV static void gather_tree(F val, const u32x4 keep, const u32x4 (&p)[2], Row& r) {
@@ -585,7 +610,8 @@ struct Attn {
   }
 
   // ------------------------------------------------------------------- thin
-  // dim 256 has registers for one of them: values are requested as the keys are used, keys as the values are
+  // Where registers do not last for both (dim 256, two row tiles of 128), one set serves: values are requested as the
+  // keys are used, keys as the values are (8192 tokens of 32 heads of 256: 54.6 us, with both and spills 72).
   static constexpr bool kOne = D * RT >= 256;
   struct Regs {
     u32x4 k[2][NC], v[ND];
@@ -1265,7 +1291,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_tree_attention(AttnArgs a) {
 
 // W waves per output row (query head, node y, slot z of the grid) join its partials, in an order that the launch alone
 // decides: D / 4 lanes read one partial's O, a wave 256 / D of them at a time.
+// From kJoinMany partials of a row on eight waves share them (one head of 256, 56 rows, 256 partials: the call 29.7 us, with
+// one wave 59; 30000 tokens of one head of 128 14.0 / 19.4; 4 heads, 32 partials 33.5 / 30.4).
 constexpr int kJoinMany = 40;
+
 
 template <int W>
 constexpr int kJoinThreads = W > 1 ? 64 * W : 256;
