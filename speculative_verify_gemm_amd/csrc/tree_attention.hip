@@ -37,7 +37,8 @@
 //   16 nodes, 8206 seen, 32 heads of 128, fp16                        26.9 + 4.8   bytes: 134 MB, 5.0 TB/s
 //   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16               154-170 + 6.6  products: 172 GFLOP in five
 //                                                                                  parts, 1.0-1.1 PFLOP/s; 537 MB
-//   32 slots of 2000 tokens behind 32768 shared, 8 heads for 32, fp16   69.9 + 5.8   bytes: 396 MB, 5.7 TB/s
+//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16    69.9 + 5.8   bytes and products side by side:
+//                                                                                  271 MB, 35 GFLOP in four parts
 //   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16   25.5 + 6.5   a few tiles a workgroup: its start
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
@@ -50,7 +51,7 @@
 // 2^kSlack: until then probabilities above 1 are kept as they are (their scale
 // 2^kLift leaves fp16 room: at most 2^(kLift + kSlack) = 2^15), which takes the
 // exchange between lanes and the rescaling of O out of almost every tile (raised at every
-// tile, the 131033 tokens above take 186 us).
+// tile, the 131033 tokens above take 183 us, the branches 77 instead of 70).
 #include "svg_cache.h"
 #include "svg_internal.h"
 
@@ -70,16 +71,16 @@ constexpr float kLowest = -3.402823466e38f;
 // kFar that step would be felt as a factor, and far beyond it would overflow: 2^(f (s - m) + kLift) then.
 constexpr float kFar = 65536.f;
 // A unit of work is a tile; an item counts as kItemThin / kItemThick tiles more, the time that starting and ending it
-// takes (thin, 8 heads of 128: 32 slots of 2000 tokens 33.3 us, with 8: 35.4, with 24: 34.5, with 4: 41; 8 slots of
-// 3000 with 4 nodes 21.6, 22.9, 21.2, 24.6.  Thick: 2 to 8 are alike).  A workgroup gets kMinThin / kMinThick units at
-// least: fewer workgroups have fewer partials to join (1000 tokens 13.0 us, with 16: 14.6, with 5: 12.9; 7656 tokens of
-// dim 256 29, with 5: 36; thick, 500 tokens of 32 heads 17.6 us, with 8: 24.4).
-constexpr int kItemThin = 12, kItemThick = 4, kMinThin = 7, kMinThick = 2;
+// takes (thin, 8 heads of 128: 32 slots of 2000 tokens 33.0 us, with 8: 37.2, with 4: 43.2, with 24: 33.0; 8 slots of
+// 3000 with 4 nodes 22.1, 22.9, 24.8, 21.6.  Thick: 2 to 8 are alike).  A workgroup gets kMinThin / kMinThick units at
+// least: fewer workgroups have fewer partials to join (1000 tokens of 8 heads 12.5 us, with 7: 12.9, with 16: 14.5, with
+// 2: 12.3; 7656 tokens of 2 heads of 256 16.6, 20.7, 20.4, 17.7; thick, 500 tokens of 32 heads 17.7 us, with 8: 24.4).
+constexpr int kItemThin = 12, kItemThick = 4, kMinThin = 4, kMinThick = 2;
 
 // Slot items are worked on alone where that is expected to take less time (in tiles of a wave): kAloneItem and the
 // longest slot's tiles against the joins that are saved, kAloneGain for each item of a workgroup, and the item's
 // tiles over the whole device.  8 heads of 128, one token, alone / not: 64 slots of 100 tokens 14.3 / 23.2 us, 128 of
-// 400 32 / 48, 32 of 300 17.2 / 19.3, 64 of 600 29 / 32, 64 of 1000 40.4 / 39.3.  Kernels that can do it are only taken
+// 400 31.8 / 48, 32 of 300 17.3 / 19.3, 64 of 600 29.6 / 32, 64 of 1000 40.3 / 39.  Kernels that can do it are only taken
 // from kAloneFrom items on: below, the few calls that gained (16.5 -> 15.0 us) did not outweigh 1 us that all others lost.
 constexpr int kAloneFrom = 256, kAloneItem = 5, kAloneGain = 15, kAloneRow = 2048;
 
