@@ -430,3 +430,66 @@ def test_long_lists_of_partials(lens, common, T, H, G, dim, page, kind):
         got = run(K.to_library(svg, c, kind), qd, parent, T, n_nodes=n, shared=common or None)
         assert np.all(got[1] == 7.0) and np.isnan(got[2]).all()
         close(got[0], ref[0], tol[0])
+
+
+@pytest.mark.parametrize("lens,common,T,H,G,dim,page,kind", [
+    ([500, 390, 420, 385], 384, 5, 2, 4, 128, 64, "bf16"),                # two row tiles of own tokens
+    ([260 + s % 40 for s in range(70)], 256, 5, 4, 4, 64, 32, "fp16"),    # and many such slots
+    ([700, 650, 641, 900, 640], 640, 2, 2, 4, 256, 64, "fp16"),
+    ([200 + s for s in range(66)], 192, 1, 4, 8, 256, 64, "bf16"),
+    ([64] * 3, 64, 7, 1, 3, 128, 64, "fp16"),                             # no own token but the nodes
+])
+def test_a_prefix_of_many_rows_beside_slots_of_few(lens, common, T, H, G, dim, page, kind):
+    C.say(f"tree_attention {len(lens)} slots behind {common} T={T} H={H} G={G} dim={dim} {kind}")
+    rng = np.random.default_rng(common + dim)
+    S = len(lens)
+    c = K.make(common, lens, T, H=H, dim=dim, page=page)
+    fill(c, rng, kind)
+    share(c, 0, common)
+    parent = trees(rng, S, T)
+    q, qd = queries(rng, S, T, H * G, dim)
+    n = [T] * S
+    n[2] = max(T - 2, 0)
+    ref, spread = AO.attention(c, wide(kind), 0, q, parent, T, n, dim ** -0.5)
+    tol = bound(c, kind, spread, max(lens) + T)
+    cache = K.to_library(svg, c, kind)
+    for said in (common, 33):
+        got = run(cache, qd, parent, T, n_nodes=n, shared=said)
+        assert np.all(got[2, n[2]:] == 7.0)
+        for s in range(S):
+            close(got[s, :n[s]], ref[s, :n[s]], tol[s, :n[s]])
+
+
+@pytest.mark.parametrize("common", [0, 64])
+def test_one_captured_graph_from_short_slots_to_long_ones(common):
+    """Which workgroups work on what is decided on the device: a graph captured over slots of few tokens serves long and
+    unequal ones, and short ones again, with the bits of an eager call each time."""
+    rng = np.random.default_rng(11)
+    S, T = 64, 2
+    c = K.make(3, [70 + s % 5 for s in range(S)], 900, H=4, dim=64, page=64)
+    fill(c, rng, "fp16")
+    share(c, 0, common)
+    cache = K.to_library(svg, c)
+    _q, qd = queries(rng, S, T, 16, 64)
+    shared = i32([common]) if common else None
+    ws, ws2 = (svg.tree_attention_workspace(cache, 16, T) for _ in range(2))
+    out, eager = torch.zeros((S * T, 16, 64), device=C.DEV), torch.zeros((S * T, 16, 64), device=C.DEV)
+    short = cache.len.clone()
+    svg.tree_attention(cache, 0, qd, None, out, ws, shared=shared)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        svg.tree_attention(cache, 0, qd, None, out, ws, shared=shared)
+    for turn, lens in enumerate((short, short + 400, short + 10 * torch.arange(S, dtype=torch.int32, device=C.DEV), short + 820, short)):
+        cache.len.copy_(lens)
+        out.zero_()
+        g.replay()
+        svg.tree_attention(cache, 0, qd, None, eager, ws2, shared=shared)
+        assert np.array_equal(C.host(out), C.host(eager)), turn
+        assert np.isfinite(C.host(eager)).all()
+    c["len"] = (short + 10 * torch.arange(S, dtype=torch.int32, device=C.DEV)).cpu().numpy()
+    cache.len.copy_(i32(c["len"]))
+    g.replay()
+    q = C.host(qd).reshape(S, T, 16, 64)
+    ref, spread = AO.attention(c, wide("fp16"), 0, q, None, T, None, 64 ** -0.5)
+    close(C.host(out).reshape(S, T, 16, 64).astype(np.float64), ref, bound(c, "fp16", spread, 1000))
