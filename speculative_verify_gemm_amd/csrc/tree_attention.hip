@@ -161,7 +161,7 @@ struct Deal {
   u32 groups;               // workgroups that take part: w has the units from start(w) on
   u32 quot, rest;           // total / groups
   u32 alone;                // units of a slot item that one wave works on alone (0: a workgroup does)
-  SVG_DEV u32 start(u32 w) const { return w * quot + w * rest / groups; }
+  SVG_DEV u32 start(u32 w) const { return w * quot + (w < rest ? w : rest); }
 };
 
 SVG_DEV int node_count(const AttnArgs& a, int s) {
@@ -201,17 +201,28 @@ SVG_DEV int wave_scan(int v) {
   return v + (lane < 16 ? 0 : (lane < 32 ? a : (lane < 48 ? b : c)));
 }
 
+// What the wave's lanes have written to LDS is there for its other lanes, and what they have read is read.
+SVG_DEV void wave_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int RTHIN, bool ALONE, bool BOTH>
 SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   constexpr int cost = item_cost(RTHIN > 0), cost_p = BOTH ? kItemThick : cost;
   constexpr u32 least = RTHIN > 0 ? kMinThin : kMinThick, least_p = kMinThick;
   const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int said = a.shared != nullptr ? a.shared[0] : 0;
-  // a slot with nodes whose tokens lie inside its pages is active; the others take no part.  Two slots a thread
+  // A slot with nodes whose tokens lie inside its pages is active; the others take no part.  Two slots a thread; up to
+  // 128 slots every wave makes the whole plan by itself, and waits for no other.
+  const bool few = S <= 128;
+  const int who = few ? lane : tid;
   int n[2], len[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int s = 2 * tid + i;
+    const int s = 2 * who + i;
     n[i] = len[i] = 0;
     if (s < S) {
       n[i] = node_count(a, s);
@@ -230,23 +241,25 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
     for (int i = 1; i >= 0; --i)
       if (n[i] > 0) {
         low = min_i(low, len[i]);
-        first = 2 * tid + i;
+        first = 2 * who + i;
       }
-    const int two = __builtin_popcountll(__ballot(n[0] > 0)) + __builtin_popcountll(__ballot(n[1] > 0));
+    int active = __builtin_popcountll(__ballot(n[0] > 0)) + __builtin_popcountll(__ballot(n[1] > 0));
     low = wave_min(low);
     first = wave_min(first);
-    if (lane == 0) {
-      p.red[0][wave] = low;
-      p.red[1][wave] = first;
-      p.red[2][wave] = two;
-    }
-    __syncthreads();
-    int active = 0;
+    if (!few) {
+      if (lane == 0) {
+        p.red[0][wave] = low;
+        p.red[1][wave] = first;
+        p.red[2][wave] = active;
+      }
+      __syncthreads();
+      active = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      low = min_i(low, p.red[0][w]);
-      first = min_i(first, p.red[1][w]);
-      active += p.red[2][w];
+      for (int w = 0; w < kWaves; ++w) {
+        low = min_i(low, p.red[0][w]);
+        first = min_i(first, p.red[1][w]);
+        active += p.red[2][w];
+      }
     }
     if (active > 1) d.prefix = __builtin_amdgcn_readfirstlane((said < 0 ? 0 : min_i(said, low)) & ~31);
     d.first = __builtin_amdgcn_readfirstlane(first < S ? first : 0);
@@ -255,23 +268,26 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   const int t0 = n[0] > 0 ? ((len[0] + n[0] - d.prefix + 31) >> 5) + cost : 0;
   const int t1 = n[1] > 0 ? ((len[1] + n[1] - d.prefix + 31) >> 5) + cost : 0;
   const int upto = wave_scan(t0 + t1);
-  if (lane == 63) p.red[3][wave] = upto;
-  if constexpr (ALONE) {
-    const int longest = -wave_min(t0 > t1 ? -t0 : -t1);
-    if (lane == 0) p.red[4][wave] = longest;
-  }
-  __syncthreads();
-  int before = upto - t0 - t1, all = 0, longest = 0;
+  int before = upto - t0 - t1, all = __builtin_amdgcn_readlane(upto, 63), longest = 0;
+  if constexpr (ALONE) longest = -wave_min(t0 > t1 ? -t0 : -t1);
+  if (!few) {
+    if (lane == 0) {
+      p.red[3][wave] = all;
+      p.red[4][wave] = longest;
+    }
+    __syncthreads();
+    all = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    const int t = p.red[3][w];
-    if (w < wave) before += t;
-    all += t;
-    if constexpr (ALONE) longest = longest > p.red[4][w] ? longest : p.red[4][w];
+    for (int w = 0; w < kWaves; ++w) {
+      const int t = p.red[3][w];
+      if (w < wave) before += t;
+      all += t;
+      if constexpr (ALONE) longest = longest > p.red[4][w] ? longest : p.red[4][w];
+    }
   }
-  if (2 * tid < S) p.cum[2 * tid] = before;
-  if (2 * tid + 1 < S) p.cum[2 * tid + 1] = before + t0;
-  if (tid == 0) p.cum[S] = all;
+  if (2 * who < S) p.cum[2 * who] = before;
+  if (2 * who + 1 < S) p.cum[2 * who + 1] = before + t0;
+  if (who == 0) p.cum[S] = all;
   d.units_p = uniform(d.prefix > 0 ? (u32)(a.sh.items_p * ((d.prefix >> 5) + cost_p)) : 0u);
   u32 own = uniform((u32)(all * a.c.heads * a.sh.rb_s));
   d.alone = 0;
@@ -314,18 +330,18 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   d.groups = uniform(want < 1 ? 1 : (want < groups ? want : groups));
   d.quot = uniform(d.total / d.groups);
   d.rest = d.total - d.quot * d.groups;
-  __syncthreads();
+  if (few) wave_sync();
+  else __syncthreads();
   return d;
 }
 static_assert(2 * kThreads >= kMaxSlots, "two slots a thread");
 
-// The workgroup that holds unit u: an estimate that is not below it (and at most a few above), put right.
+// The workgroup that holds unit u: the first `rest` have a unit more.
 SVG_DEV int group_of(u32 u, const Deal& p) {
-  u32 w = (u32)((float)u * __builtin_amdgcn_rcpf((float)p.total) * (float)p.groups) + 2u;
-  w = w < p.groups ? w : p.groups - 1;
-  while (p.start(w) > u) --w;
-  return (int)w;
+  const u32 more = p.rest * (p.quot + 1);
+  return (int)(u < more ? u / (p.quot + 1) : p.rest + (u - more) / p.quot);
 }
+
 
 // ------------------------------------------------------------ 16-bit operands
 template <bool BF>
@@ -394,13 +410,6 @@ template <int N>
 SVG_DEV void wait_loads() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
-  asm volatile("" ::: "memory");
-}
-// What the wave's lanes have written to LDS is there for its other lanes, and what they have read is read.
-SVG_DEV void wave_sync() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_wave_barrier();
   asm volatile("" ::: "memory");
 }
 SVG_DEV void barrier() {

@@ -438,6 +438,8 @@ def test_long_lists_of_partials(lens, common, T, H, G, dim, page, kind):
     ([700, 650, 641, 900, 640], 640, 2, 2, 4, 256, 64, "fp16"),
     ([200 + s for s in range(66)], 192, 1, 4, 8, 256, 64, "bf16"),
     ([64] * 3, 64, 7, 1, 3, 128, 64, "fp16"),                             # no own token but the nodes
+    ([70 + s % 9 for s in range(140)], 64, 1, 2, 2, 64, 32, "fp16"),
+    ([129] * 128, 128, 1, 1, 2, 64, 32, "bf16"), ([129] * 129, 128, 1, 1, 2, 64, 32, "bf16"),
 ])
 def test_a_prefix_of_many_rows_beside_slots_of_few(lens, common, T, H, G, dim, page, kind):
     C.say(f"tree_attention {len(lens)} slots behind {common} T={T} H={H} G={G} dim={dim} {kind}")
