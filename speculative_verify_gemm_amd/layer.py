@@ -13,6 +13,7 @@ _lib = None  # the library, once the package has loaded it (_bind)
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
+_FP32 = torch.float32
 _FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
@@ -95,9 +96,10 @@ def add_rmsnorm_quant_i8(x, residual, weight, eps, signs, xq, x_scale, y=None, b
     one slab buffer per 32 rows), x_scale [M] and, if given, the normalised
     rows y fp32 [M, K]."""
     dev = _device(x, "x")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [M, K]")
-    M, K = x.shape
+    M, K = shape
     px, kx = _float_tensor(x, "x", dev)
     pw, kw = _float_tensor(weight, "weight", dev)
     pr = None if residual is None else _tensor(residual, "residual", torch.float32, dev)
@@ -105,7 +107,7 @@ def add_rmsnorm_quant_i8(x, residual, weight, eps, signs, xq, x_scale, y=None, b
     ps = _tensor(signs, "signs", torch.int8, dev)
     pq = _tensor(xq, "xq", torch.int8, dev)
     pc = _tensor(x_scale, "x_scale", torch.float32, dev)
-    if ((residual is not None and residual.shape != x.shape) or (y is not None and y.shape != x.shape)
+    if ((residual is not None and residual.shape != shape) or (y is not None and y.shape != shape)
             or weight.numel() != K or signs.numel() != K or xq.numel() != M * K or x_scale.numel() != M):
         raise ValueError("need residual and y [M, K], weight and signs [K], xq of M * K codes and x_scale [M]")
     _call(_lib.add_rmsnorm_quant_i8, dev, stream, px, kx, pr, pw, kw, eps, M, K, ps, block, py, pq, pc)
@@ -162,18 +164,19 @@ class KVCache:
 
 def _rows(t, name, cache, width):
     """fp32 rows [n, ...] of `width` values each, a row contiguous: (address, row stride, n)."""
-    if t.dtype != torch.float32:
+    if t.dtype is not _FP32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
-    n = t.shape[0]
-    if t.dim() == 3:
-        ok = t.shape[1] * t.shape[2] == width and t.stride(2) == 1 and (t.stride(1) == t.shape[2] or t.shape[1] == 1)
+    shape, stride = t.shape, t.stride()  # (each look at a tensor costs as much as the rest of the check)
+    if len(shape) == 3:
+        ok = shape[1] * shape[2] == width and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
     else:
-        ok = t.dim() == 2 and t.shape[1] == width and t.stride(1) == 1
+        ok = len(shape) == 2 and shape[1] == width and stride[1] == 1
     if not ok:
         raise ValueError(f"{name} must be [n, {width}] or [n, heads, dim] with contiguous rows")
-    return t.data_ptr(), (t.stride(0) if n > 1 else width), n
+    n = shape[0]
+    return t.data_ptr(), (stride[0] if n > 1 else width), n
 
 
 def _slots(t, name, cache, *more):
