@@ -32,14 +32,14 @@
 //    directly and run STEPS - 1 steps ahead, one barrier a step.  Bound by the matrix unit.
 // A shared prefix that is walked the thick way and slots that are walked the thin way are one launch.
 //
-// Measured (kernel, then join; us):
-//   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16        9.3 + 3.8   a chain of dependent loads
-//   16 nodes, 8206 seen, 32 heads of 128, fp16                        26.9 + 4.8   bytes: 134 MB, 5.0 TB/s
-//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16               154-170 + 6.6  products: 172 GFLOP in five
-//                                                                                  parts, 1.0-1.1 PFLOP/s; 537 MB
-//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16    69.9 + 5.8   bytes and products side by side:
-//                                                                                  271 MB, 35 GFLOP in four parts
-//   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16   25.5 + 6.5   a few tiles a workgroup: its start
+// Measured (kernel + join, us, and what bounds it):
+//   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16            8.8 + 3.8   a chain of dependent loads
+//   16 nodes, 8206 seen, 32 heads of 128, fp16                           25.7 + 4.6   bytes: 135 MB, 5.2 TB/s
+//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16              153 to 190 + 7   products: 172 GFLOP in five parts, 1.1
+//                                                                         PFLOP/s (less as the clock falls); 538 MB
+//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16     67.9 + 5.8   bytes and products side by side:
+//                                                                                     271 MB, 35 GFLOP in four parts
+//   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16    25.3 + 6.4   a few tiles a workgroup: its start
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
 // two and split into 16-bit parts (two of fp16: 22 bits; three of bf16: 24 bits), one
@@ -304,7 +304,8 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   if constexpr (BOTH) {
     // The device is shared out between the prefix and the slots' own tokens by what either takes; a thick tile counts
     // as 2 thin ones where one row tile of up to 128 dims is thin, else 1.5 (32 branches of 2000 tokens behind 32768
-    // 72.5 us, with 1.5: 74, with 3: 75, with 4: 87; 24 trees of 8 nodes and 300 tokens behind 2048, two row tiles, 45.5 us, with 3: 54)
+    // 72.5 us, with 1.5: 74, with 3: 75, with 4: 87; 24 trees of 8 nodes and 300 tokens behind 2048, two row tiles,
+    // 45.5 us, with 3: 54)
     u32 front = 0;
     if (d.units_p > 0) {
       const float w = (float)d.units_p * (RTHIN == 1 && a.c.dim < 256 ? 2.f : 1.5f);
