@@ -37,7 +37,7 @@
 //   16 nodes, 8206 seen, 32 heads of 128, fp16                           25.7 + 4.6   bytes: 135 MB, 5.2 TB/s
 //   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16              153 to 190 + 7   products: 172 GFLOP in five parts, 1.1
 //                                                                         PFLOP/s (less as the clock falls); 538 MB
-//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16     67.9 + 5.8   bytes and products side by side:
+//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16     70.0 + 6.0   bytes and products side by side:
 //                                                                                     271 MB, 35 GFLOP in four parts
 //   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16    25.3 + 6.4   a few tiles a workgroup: its start
 //
@@ -303,12 +303,13 @@ SVG_DEV Deal make_plan(const AttnArgs& a, Plan& p, int& wg) {
   u32 groups = (u32)a.groups, at_least = least;
   if constexpr (BOTH) {
     // The device is shared out between the prefix and the slots' own tokens by what either takes; a thick tile counts
-    // as 2 thin ones where one row tile of up to 128 dims is thin, else 1.5 (32 branches of 2000 tokens behind 32768
-    // 72.5 us, with 1.5: 74, with 3: 75, with 4: 87; 24 trees of 8 nodes and 300 tokens behind 2048, two row tiles,
-    // 45.5 us, with 3: 54)
+    // as 2.5 thin ones where one row tile of up to 128 dims is thin, as 1.8 of dim 256, as 1.5 of two row tiles.  (32 slots
+    // of one token: 32 heads, 200 tokens behind 1024 36.3 us, with 2: 38.8, with 3: 34.7; 8 heads, 2000 behind 32768
+    // 68.8, 67.7, 74.1; 19 slots of 3 nodes, 32 heads, 862 behind 10496 95, 88, 116.  Two row tiles: 24 slots of 8 nodes,
+    // 300 behind 2048 45.5 us, with 3: 54)
     u32 front = 0;
     if (d.units_p > 0) {
-      const float w = (float)d.units_p * (RTHIN == 1 && a.c.dim < 256 ? 2.f : 1.5f);
+      const float w = (float)d.units_p * (RTHIN == 1 ? (a.c.dim < 256 ? 2.5f : 1.8f) : 1.5f);
       front = (u32)((float)groups * w * __builtin_amdgcn_rcpf(w + (float)own) + 0.5f);
       const u32 most = (d.units_p + least_p - 1) / least_p, room = own > 0 ? groups - 1 : groups;
       front = front < most ? front : most;
