@@ -70,7 +70,7 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
  *  pages     int32 [n_slots]: entries of each row that are in use.
  *  len       int32 [n_slots]: committed tokens of each slot.
  *  refs      int32 [n_pages]: the number of slots that hold each page; a page is
- *            free where it is 0.  A page that several slots hold is never written.
+ *            free where it is 0.  A page that several slots hold (a count above 1) is never written.
  *  (table, pages, len, refs: 4-byte aligned.  Each call names the ones it needs.)
  *
  * A page holds head after head, page * dim values each, in the lane order of
@@ -101,9 +101,10 @@ typedef struct svg_kv_cache {
  *  T         rows of each slot, >= 1.
  *  n_rows    int32 [n_slots] or NULL: rows of each slot that are written (the
  *            nearest of 0 .. T); NULL: all T.
- *  A row whose position is not inside the slot's pages, or whose page number is not one of
- *  the cache's, is not written.  The pages written have to be the slot's own (kv_reserve).
- *  Reads table, pages, len.  Errors: SVG_EINVAL for a null required pointer, T < 1 or a layer
+ *  A row whose position is not inside the slot's pages, whose page number is not one of the cache's, or whose page
+ *  other slots hold too (refs above 1: kv_reserve was not called, or refused the slot) is not written.
+ *  Reads table, pages, len, and refs where it is not NULL (without it the caller sees to it that no page written is
+ *  another slot's as well).  Errors: SVG_EINVAL for a null required pointer, T < 1 or a layer
  *  outside 0 .. n_layers - 1; SVG_EUNSUPPORTED for a cache outside the limits above, n_slots * T >= 2^31
  *  or ld_k / ld_v; SVG_EALIGN.
  */
@@ -121,9 +122,9 @@ svg_status kv_append(const svg_kv_cache* cache, int layer, const float* k, int64
  *  len_out   int32 [n_slots]: len[s] + n_emit[s] (the root and the accepted nodes are
  *            committed); may be len itself.
  *  The token of node path[s][j] moves to position len[s] + 1 + j, j < n_emit[s] - 1.  A slot with
- *  n_emit outside 1 .. T, a path that is not rising inside 1 .. T - 1, or positions outside its pages keeps
- *  its tokens, and len_out[s] = len[s].
- *  Reads table, pages, len.  Errors as for kv_append.
+ *  n_emit outside 1 .. T, a path that is not rising inside 1 .. T - 1, or positions (the root's to the last accepted
+ *  node's) outside its pages or in a page that other slots hold too keeps its tokens, and len_out[s] = len[s].
+ *  Reads table, pages, len, and refs as kv_append does.  Errors as for kv_append.
  */
 svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, const int32_t* n_emit, int32_t* len_out,
                      void* stream);
@@ -139,7 +140,8 @@ svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, cons
  *  cache     read: table, pages, len.   refs is updated (one count for each slot that holds a page).
  *  table_out, pages_out, len_out   the new tables, of the sizes of table, pages and len, and not
  *            these themselves.  Entries of table_out behind a row's pages_out are left as they were.
- *  No page is copied: kv_reserve does that for those that a fork writes to.
+ *  No page is copied: kv_reserve does that for those that a fork writes to.  A tree that has been appended is committed
+ *  before its slot is forked: the page that the fork then holds as well is not written any more, by kv_commit neither.
  *  Errors as for kv_append, and SVG_EINVAL where an output is its input.
  */
 svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table_out, int32_t* pages_out,
@@ -151,7 +153,9 @@ svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table
  *
  *  need      int32 [n_slots]; a slot with need < 1 is left as it is.
  *  status    OUTPUT int32 [n_slots]: 0 done; 1 not enough free pages; 2 more than a table row holds, or
- *            a slot whose pages, length or last page number is not valid.  A slot with 1 or 2 is left as it was.
+ *            a slot whose pages, length or last page number is not valid.  A slot with 1 or 2 is left as it was, and
+ *            takes no part in a step until it has room: its n_rows, n_nodes and n_emit are to be 0.  (Otherwise the calls
+ *            pass over what has no place of its own, and what it has room for is written and committed.)
  *  workspace SVG_KV_WORKSPACE_BYTES(n_slots) bytes, 8-byte aligned; its contents need not be kept.  Calls that
  *            may overlap need different ones (and may not share refs).
  *  The slots are served in order.  Where the page of token len - 1 is partly filled and other slots hold it too

@@ -14,6 +14,8 @@ pages [S], len [S], refs [P] (int), dim, page.
   P3. fork: slot s holds the pages of slot src[s]'s committed tokens; all slots
       change at once.
   P4. commit: node path[j]'s token moves to position len + 1 + j.
+  P5. a page that several slots hold is not written: append passes over its rows,
+      commit keeps a slot with a position of its path there.
 """
 import numpy as np
 
@@ -36,6 +38,12 @@ def page_of(c, s, pos):
     return p if 0 <= p < c["refs"].shape[0] else None
 
 
+def own_page_of(c, s, pos):
+    """The same, None also where another slot holds the page."""
+    p = page_of(c, s, pos)
+    return None if p is None or c["refs"][p] > 1 else p
+
+
 def token(c, layer, s, pos):
     """(key [H, dim], value [H, dim]) of one position."""
     p, t, d = page_of(c, s, pos), pos % c["page"], np.arange(c["dim"])
@@ -54,7 +62,7 @@ def append(c, layer, k, v, T, n_rows=None):
         n = T if n_rows is None else min(max(int(n_rows[s]), 0), T)
         for i in range(n):
             pos = int(c["len"][s]) + i
-            if c["len"][s] >= 0 and page_of(c, s, pos) is not None:
+            if c["len"][s] >= 0 and own_page_of(c, s, pos) is not None:
                 put(c, layer, s, pos, k[s, i], v[s, i])
 
 
@@ -69,7 +77,7 @@ def commit(c, path, n_emit):
         p = [0] + [int(x) for x in path[s, :n - 1]]
         if any(b <= a or b >= T for a, b in zip(p, p[1:])):
             continue
-        if base < 0 or page_of(c, s, base) is None or page_of(c, s, base + p[-1]) is None:
+        if base < 0 or own_page_of(c, s, base) is None or own_page_of(c, s, base + p[-1]) is None:
             continue
         for layer in range(c["k"].shape[0]):
             rows = [tuple(np.array(x) for x in token(c, layer, s, base + x)) for x in p[1:]]

@@ -21,6 +21,12 @@ SVG_DEV bool page_of(const svg_kv_cache& c, int s, long i, int& page) {
   return (u32)page < (u32)c.n_pages;
 }
 
+// Whether that page may be written: no other slot holds it.  (A slot that kv_reserve refused still has the page that it
+// shares.)
+SVG_DEV bool own_page_of(const svg_kv_cache& c, int s, long i, int& page) {
+  return page_of(c, s, i, page) && (c.refs == nullptr || c.refs[page] <= 1);
+}
+
 // ------------------------------------------------------------------- append
 // One wave per (four consecutive positions, head, slot): four tokens share the
 // eight-byte halves of the values' 16-byte pieces, so they are written whole.
@@ -37,7 +43,7 @@ __global__ __launch_bounds__(64) void k_kv_append(svg_kv_cache c, int layer, con
   const long p0 = (len & ~3) + 4l * blockIdx.x;  // first of the four positions
   if (p0 >= (long)len + n) return;
   int page;
-  if (!page_of(c, s, p0 / c.page, page)) return;
+  if (!own_page_of(c, s, p0 / c.page, page)) return;
   const u32 t0 = (u32)(p0 % c.page);
   const size_t base = (((size_t)layer * c.n_pages + page) * c.heads + h) * ((size_t)c.page * dim);
   uint16_t* kp = static_cast<uint16_t*>(c.k) + base;
@@ -79,7 +85,8 @@ __global__ __launch_bounds__(64) void k_kv_append(svg_kv_cache c, int layer, con
 
 // ------------------------------------------------------------------- commit
 // What slot s commits: `kept` tokens, the root's and the accepted nodes' (0: the path is not valid, or its tokens are not
-// inside the slot's pages), the same in every lane of the wave; in lane j the node that moves to len + 1 + j.
+// inside the slot's pages, or in one that others hold too), the same in every lane of the wave; in lane j the node that
+// moves to len + 1 + j.
 struct Moves {
   int kept, len, node;
 };
@@ -96,7 +103,7 @@ SVG_DEV Moves moves_of(const svg_kv_cache& c, int s, int T, const int32_t* path,
   if (ok) {
     const int last = n > 1 ? __shfl(p, n - 2) : 0;
     int page;
-    ok = page_of(c, s, (long)len / c.page, page) && page_of(c, s, ((long)len + last) / c.page, page);
+    ok = own_page_of(c, s, (long)len / c.page, page) && own_page_of(c, s, ((long)len + last) / c.page, page);
   }
   return {ok ? n : 0, len, p};
 }

@@ -189,7 +189,8 @@ def _slots(t, name, cache, *more):
 def kv_append(cache, layer, k, v, T, n_rows=None, stream=None):
     """Write T new tokens of each slot behind its committed ones, in one layer:
     k, v fp32 [n_slots * T, heads * dim] (or [.., heads, dim]; rows may lie apart,
-    as in the output of a fused projection); n_rows int32 [n_slots]: fewer of them."""
+    as in the output of a fused projection); n_rows int32 [n_slots]: fewer of them.
+    Rows without a page, or in one that other slots hold too, are passed over."""
     pk, lk, nk = _rows(k, "k", cache, cache.heads * cache.dim)
     pv, lv, nv = _rows(v, "v", cache, cache.heads * cache.dim)
     if nk != cache.n_slots * T or nv != nk:
@@ -201,7 +202,8 @@ def kv_append(cache, layer, k, v, T, n_rows=None, stream=None):
 def kv_commit(cache, path, n_emit, len_out=None, stream=None):
     """Move the accepted path of each slot's tree behind its root, in every
     layer: path int32 [n_slots, T] and n_emit [n_slots] as tree_accept_greedy
-    writes them; the new lengths go to len_out (None: into the cache's own)."""
+    writes them; the new lengths go to len_out (None: into the cache's own). A
+    slot whose path has no pages of its own keeps its tokens and length."""
     if path.dim() != 2:
         raise ValueError("path must be [n_slots, T]")
     T = path.shape[1]
@@ -229,7 +231,8 @@ def kv_workspace(cache):
 
 def kv_reserve(cache, need, status, workspace, stream=None):
     """Room for need[s] more tokens of each slot, in pages of its own; status
-    int32 [n_slots]: 0 done, 1 not enough free pages, 2 does not fit the table."""
+    int32 [n_slots]: 0 done, 1 not enough free pages, 2 does not fit the table. A
+    slot with 1 or 2 is left as it was and takes no part in a step until it has room."""
     pw = _tensor(workspace, "workspace", torch.int32, cache.device)
     if workspace.numel() < 2 * cache.n_slots + 4:
         raise ValueError("workspace is smaller than kv_workspace(cache)")

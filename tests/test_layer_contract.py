@@ -1,0 +1,109 @@
+"""What svgemm_layer.h says of the calls' edges: slots that were refused, pages
+that several slots hold, rows far from ordinary, sizes at the limits."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import cache_oracle as CO
+
+
+@pytest.fixture
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    global A, C, K, svg
+    import cache_cases as K  # noqa: F401
+    import svg_cases as C  # noqa: F401
+    import test_tree_attention_parity as A  # noqa: F401
+    import speculative_verify_gemm_amd as svg
+    A.svg, A.C, A.K = svg, C, K
+
+
+# ------------------------------------------------- pages of several holders
+def refused_forks(kind="fp16", dim=64):
+    """Slots 1 and 2, forks of one another in the middle of a page, that kv_reserve had no pages left for; slot 0 took
+    them.  The oracle's cache and the library's."""
+    c = K.make(11, [10, 40, 70], 0, L=2, H=2, dim=dim, page=32, spare=0, width=6)
+    A.fill(c, np.random.default_rng(3), kind)
+    a = K.to_library(svg, c, kind)
+    b = a.other_tables()
+    svg.kv_fork(a, A.i32([0, 1, 1]), b)
+    c = CO.fork(c, [0, 1, 1])
+    status = A.i32([9, 9, 9])
+    svg.kv_reserve(b, A.i32([118, 8, 8]), status, svg.kv_workspace(b))
+    assert list(CO.reserve(c, [118, 8, 8])) == list(C.host(status)) == [0, 1, 1]
+    K.same(b, c)
+    assert c["refs"][c["table"][1, 1]] == 2 and c["table"][1, 1] == c["table"][2, 1]
+    return c, b
+
+
+def rows(seed, S, T, kind="fp16", dim=64):
+    """fp32 rows of keys and values on the device, and their patterns."""
+    x = torch.randn((2, S * T, 2 * dim), generator=torch.Generator().manual_seed(seed))
+    pat = K.bits(x.to(K.TYPES[kind])).reshape(2, S, T, 2, dim)
+    return x[0].to(C.DEV), x[1].to(C.DEV), pat[0], pat[1]
+
+
+def test_the_oracle_leaves_pages_of_several_holders():
+    z = np.zeros((1, 3, 1, 32 * 64), np.int16)
+    c = dict(k=z.copy(), v=z.copy(), table=np.array([[0, 1], [0, 2]], np.int32), pages=np.array([2, 2], np.int32),
+             len=np.array([30, 32], np.int32), refs=np.array([2, 1, 1], np.int32), dim=64, page=32)
+    new = np.arange(2 * 4 * 64, dtype=np.int16).reshape(2, 4, 1, 64) + 1
+    CO.append(c, 0, new, new, 4)
+    assert not c["k"][0, 0].any() and not c["v"][0, 0].any()
+    assert np.array_equal(CO.token(c, 0, 0, 32)[0], new[0, 2]) and np.array_equal(CO.token(c, 0, 1, 35)[1], new[1, 3])
+    path = np.array([[2, -1, -1, -1], [2, -1, -1, -1]])
+    assert list(CO.commit(c, path, [1, 1])) == [30, 33] and list(CO.commit(c, path, [2, 2])) == [30, 34]
+    assert np.array_equal(CO.token(c, 0, 1, 33)[0], new[1, 2]) and not c["k"][0, 0].any()
+
+
+@pytest.mark.gpu
+def test_append_and_commit_leave_pages_of_several_holders(gpu):
+    T = 8
+    c, cache = refused_forks()
+    k, v, kp, vp = rows(1, 3, T)
+    for n in ([T, T, 0], [0, 0, T], [T, T, T]):  # one of the refused slots, the other, both
+        svg.kv_append(cache, 1, k, v, T, n_rows=A.i32(n))
+        CO.append(c, 1, kp, vp, T, n)
+        K.same(cache, c)
+    # the path of a refused slot stays where it is: moves, and the root alone
+    path = np.full((3, T), -1, np.int32)
+    path[:, :2] = [2, 5]
+    for n in ([3, 3, 1], [1, 1, 3]):
+        out = torch.zeros(3, dtype=torch.int32, device=C.DEV)
+        svg.kv_commit(cache, A.i32(path), A.i32(n), out)
+        new = CO.commit(c, path, n)
+        assert list(new) == list(C.host(out)) == [10 + n[0], 40, 40]
+        K.same(cache, c)
+    # one of them given up: the page is the other's own, and takes its rows
+    b = cache.other_tables()
+    svg.kv_fork(cache, A.i32([0, 1, -1]), b)
+    c = CO.fork(c, [0, 1, -1])
+    svg.kv_append(b, 0, k, v, T)
+    CO.append(c, 0, kp, vp, T)
+    svg.kv_commit(b, A.i32(path), A.i32([1, 3, 0]))
+    c["len"] = CO.commit(c, path, [1, 3, 0])
+    assert list(c["len"]) == [11, 43, 0]
+    K.same(b, c)
+
+
+@pytest.mark.gpu
+def test_a_path_that_reaches_into_a_page_of_several_holders(gpu):
+    """The root's page is the slot's own and the next one is not: what lies in the first is written, and nothing committed."""
+    c = K.make(5, [30, 30], 8, L=1, H=1, dim=64, page=32)
+    A.fill(c, np.random.default_rng(4), "fp16")
+    c["table"][1, 1] = c["table"][0, 1]
+    c["refs"] = CO.holders(c).astype(np.int32)
+    cache = K.to_library(svg, c)
+    x = torch.randn((2, 16, 64), generator=torch.Generator().manual_seed(2))
+    pat = K.bits(x.half()).reshape(2, 2, 8, 1, 64)
+    svg.kv_append(cache, 0, x[0].to(C.DEV), x[1].to(C.DEV), 8)
+    CO.append(c, 0, pat[0], pat[1], 8)
+    K.same(cache, c)
+    path = np.full((2, 8), -1, np.int32)
+    path[:, 0] = [1, 2]                  # inside the first page; in the second
+    out = torch.zeros(2, dtype=torch.int32, device=C.DEV)
+    svg.kv_commit(cache, A.i32(path), A.i32([2, 2]), out)
+    assert list(CO.commit(c, path, [2, 2])) == list(C.host(out)) == [32, 30]
+    K.same(cache, c)
