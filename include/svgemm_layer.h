@@ -201,9 +201,10 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *  len[s] + j for the nodes j of i's root path, i included.  Sums and accumulators are fp32; q and p
  *  enter the 16-bit matrix products in parts that carry at least 16 bits of each, so an output is within about 1e-5 of
  *  its row's largest of an exact one.  Keys and values of tokens that a row does not see never reach it, whatever they are.
- *  NaN rows: a node whose root path breaks the rule above; a row that reads a page number outside the cache; all of a
- *  slot whose pages do not cover len + n_nodes.
- *  Reads table, pages, len.  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the
+ *  NaN rows: a node whose root path breaks the rule above, or meets a node in a page that other slots hold too (which
+ *  kv_append has passed over); a row that reads a page number outside the cache; all of a slot whose pages do not cover
+ *  len + n_nodes.
+ *  Reads table, pages, len, and refs where it is not NULL (without it no node is passed over).  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the
  *  cache or a scale that is not finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads,
  *  ld_q, or a table so large that n_slots * width * page * heads times the blocks of 128 rows of an item nears 2^36; SVG_EALIGN.
  *

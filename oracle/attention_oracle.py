@@ -8,7 +8,8 @@ module; the HIP library shares no code with it.
       j on its root path, itself included.
   A2. Query head a reads key/value head a / (q_heads / heads).
   A3. o = sum softmax(scale q . k) v.
-A path that is no path to the root gives a NaN row.
+A path that is no path to the root, or that meets a node in a page which several
+slots hold (no token could be written there), gives a NaN row.
 """
 import numpy as np
 
@@ -58,7 +59,7 @@ def attention(c, wide, layer, q, parent, T, n_nodes, scale):
             V = wide(c["v"][layer, pg, h][np.arange(len(at))[:, None], CO.value_at(t, d, dim)])
             for i in range(n):
                 pos = positions(length, None if parent is None else parent[s], i)
-                if pos is None:
+                if pos is None or any(CO.own_page_of(c, s, x) is None for x in pos[length:]):
                     continue
                 k, v = K[pos], V[pos]
                 for a in range(h * G, h * G + G):

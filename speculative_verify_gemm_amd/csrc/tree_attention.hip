@@ -967,12 +967,23 @@ SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, c
 
     // the tree's root paths: lane j < 32 holds node j's, by doubling
     u32 path = 0, broken = 0;
-    auto root_paths = [&] {
-      if (prefix || (last + 1) * 32l <= it.len) return;
+    const bool tree = !prefix && (last + 1) * 32l > it.len;  // (the workgroup's tiles have tree tokens)
+    int up = (lane & 31) - 1, tree_page = -1, held = 0;
+    // what is asked for in memory, before the tiles are: parents and pages, then the pages' counts
+    auto look_up = [&] {
       const int j = lane & 31;
-      int up = j - 1;
-      if (a.parent != nullptr && j < nodes) up = a.parent[(size_t)s * a.T + j];
+      if (!tree || j >= nodes) return;
+      if (a.c.refs != nullptr) tree_page = it.table[(it.len + j) >> (it.log_tp + 5)];
+      if (a.parent != nullptr) up = a.parent[(size_t)s * a.T + j];
+    };
+    auto count_holders = [&] {
+      if (!it.bad(tree_page)) held = a.c.refs[tree_page];
+    };
+    auto root_paths = [&] {
+      if (!tree) return;
+      const int j = lane & 31;
       broken = j == 0 ? up != -1 : (up < 0 || up >= j);
+      broken |= held > 1;  // other slots hold the node's page too: its rows are not there
       if (j == 0 || broken || j >= nodes) up = j;  // a path ends here
       if (j >= nodes) broken = 0;
       path = 1u << j;
@@ -1006,6 +1017,7 @@ SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, c
     if constexpr (THIN) {
       const int mine = alone ? first : first + wave;  // this wave's first tile
       Pages pages;
+      look_up();
       if (mine <= last) pages.start(it, mine, last);
       typename A::Regs regs;
       int my_page = 0;
@@ -1036,7 +1048,10 @@ SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, c
             raw[2 * i] = at4(qp + 32 * i);
             raw[2 * i + 1] = at4(qp + 32 * i + 4);
           }
-          if (rt == RT - 1) request();
+          if (rt == RT - 1) {
+            count_holders();
+            request();
+          }
           float top = 0.f;
 #pragma unroll
           for (int i = 0; i < 2 * NC; ++i)
@@ -1063,6 +1078,7 @@ SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, c
 #pragma unroll
           for (int i = 0; i < NC; ++i) largest = top8(qp + 32 * i, largest);
         }
+        count_holders();
         request();
         if (splits) {
           const int e = A::exponent_of(row_max(largest));
@@ -1157,7 +1173,9 @@ SVG_DEV void walk_items(const AttnArgs& a, const Plan& plan, const Deal& deal, c
       int nrt = row_tiles - rt0;
       nrt = nrt < 0 ? 0 : (nrt < each ? nrt : each);
       Pages pages;
+      look_up();
       pages.start(it, first, last);
+      count_holders();
       // q has to be here before the tiles are asked for (the compiler does not see those loads, and would wait for them too)
       f32x4 raw[RT][2 * NC];
 #pragma unroll

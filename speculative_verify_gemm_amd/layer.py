@@ -265,7 +265,8 @@ def tree_attention(cache, layer, q, parent, out, workspace, scale=None, n_nodes=
     projection), parent int32 [n_slots, T] (None: chains; T is then q's rows per
     slot), out fp32 of q's shape, workspace from tree_attention_workspace();
     scale defaults to 1 / sqrt(dim); n_nodes int32 [n_slots]: nodes of each tree;
-    shared int32 [1]: leading tokens that are the same pages in every slot."""
+    shared int32 [1]: leading tokens that are the same pages in every slot. Nodes
+    without a place of their own in the cache give NaN rows."""
     S, D = cache.n_slots, cache.dim
     heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // D
     pq, ld, n = _rows(q, "q", cache, heads * D)

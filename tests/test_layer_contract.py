@@ -5,6 +5,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from oracle import attention_oracle as AO
 from oracle import cache_oracle as CO
 
 
@@ -107,3 +108,48 @@ def test_a_path_that_reaches_into_a_page_of_several_holders(gpu):
     svg.kv_commit(cache, A.i32(path), A.i32([2, 2]), out)
     assert list(CO.commit(c, path, [2, 2])) == list(C.host(out)) == [32, 30]
     K.same(cache, c)
+
+
+@pytest.mark.gpu
+def test_attention_of_refused_slots_is_nan(gpu):
+    """The rows that kv_append has passed over are never read as if they were the slot's."""
+    T, A_, dim = 8, 4, 64
+    c, cache = refused_forks()
+    k, v, kp, vp = rows(1, 3, T)
+    svg.kv_append(cache, 1, k, v, T)
+    CO.append(c, 1, kp, vp, T)
+    q, qd = A.queries(np.random.default_rng(7), 3, T, A_, dim)
+    ref, spread = AO.attention(c, A.wide("fp16"), 1, q, None, T, None, dim ** -0.5)
+    assert np.isnan(ref[1:]).all() and np.isfinite(ref[0]).all()
+    A.close(A.run(cache, qd, None, T, layer=1), ref, A.bound(c, "fp16", spread, 80))
+    n = [T, 0, 0]                        # as such slots are to be called: they take no part
+    got = A.run(cache, qd, None, T, layer=1, n_nodes=n)
+    assert (got[1:] == 7.0).all()
+    A.close(got[:1], ref[:1], A.bound(c, "fp16", spread, 80)[:1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S,common,T,H,G,dim,page,kind", [
+    (3, 0, 7, 2, 2, 64, 32, "fp16"), (3, 0, 32, 2, 8, 128, 32, "bf16"), (4, 0, 6, 1, 8, 256, 64, "fp16"),
+    (40, 0, 3, 8, 2, 128, 32, "bf16"), (20, 64, 4, 2, 4, 128, 64, "fp16"), (70, 64, 2, 4, 4, 64, 64, "bf16"),
+])
+def test_attention_of_trees_that_reach_into_a_page_of_several_holders(gpu, S, common, T, H, G, dim, page, kind):
+    """Every way over the tiles: some slots' trees begin in a page of their own and go on in one that others hold."""
+    C.say(f"tree_attention, shared tree pages: S={S} common={common} T={T} H={H} G={G} dim={dim} {kind}")
+    rng = np.random.default_rng(S + T)
+    lens = [common + page - 1 - s % 3 for s in range(S)]
+    c = K.make(S, lens, max(T, 4), H=H, dim=dim, page=page)
+    A.fill(c, rng, kind)
+    A.share(c, 0, common)
+    two = 1 + common // page
+    for s in range(1, S, 3):             # the page behind: the first slot's
+        c["table"][s, two] = c["table"][0, two]
+    c["refs"] = CO.holders(c).astype(np.int32)
+    parent = A.trees(rng, S, T)
+    parent[-1] = -1
+    parent[-1, 1:] = 0                   # siblings: those behind the page's end are alone in it
+    q, qd = A.queries(rng, S, T, H * G, dim)
+    ref, spread = AO.attention(c, A.wide(kind), 0, q, parent, T, None, dim ** -0.5)
+    assert np.isnan(ref).any() and np.isfinite(ref).any()
+    got = A.run(K.to_library(svg, c, kind), qd, parent, T, shared=common or None)
+    A.close(got, ref, A.bound(c, kind, spread, max(lens) + T))
