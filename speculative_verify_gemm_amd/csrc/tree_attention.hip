@@ -43,7 +43,9 @@
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
 // two and split into 16-bit parts (two of fp16: 22 bits; three of bf16: 24 bits), one
-// product each; the probabilities into two parts.  Sums, maxima and accumulators
+// product each; the probabilities into two parts.  fp16 parts end at 2^-24 whatever they belong to, so
+// a row's largest q is brought to 2^13 and more: what is small beside it is off by 2^-38 of it at most (brought to 1, by 2^-25:
+// one channel 2^13 above the others would put 2e-4 into the output).  Sums, maxima and accumulators
 // are fp32.  One product with everything rounded to 16 bits would be off by
 // 2^-9 (bf16), which the fp32 consumers of the output would see.
 //
@@ -350,7 +352,8 @@ template <bool BF>
 struct Ops;
 template <>
 struct Ops<false> {
-  static constexpr int kQ = 2;  // parts of q
+  static constexpr int kQ = 2;     // parts of q
+  static constexpr int kTop = 13;  // the power of two of a row's largest q
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
   }
@@ -361,6 +364,7 @@ struct Ops<false> {
 template <>
 struct Ops<true> {
   static constexpr int kQ = 3;
+  static constexpr int kTop = 0;
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
   }
@@ -850,10 +854,11 @@ struct Attn {
     barrier();
   }
 
-  // |q| < 4 in the parts: the exponent of the power of two that a row is divided by (0 and what is not finite: none).
+  // The exponent of the power of two that a row is divided by, so that its largest q lies in [2^kTop, 2^(kTop + 1)) (0 and
+  // what is not finite: none).
   SVG_DEV static int exponent_of(float top) {
     const int e = (int)((__float_as_uint(top) >> 23) & 255u) - 127;
-    return top == 0.f || e == 128 ? 0 : (e > 126 ? 126 : (e < -126 ? -126 : e));
+    return top == 0.f || e == 128 ? 0 : (e - O::kTop > 126 ? 126 : (e - O::kTop < -126 ? -126 : e - O::kTop));
   }
   SVG_DEV static float two_to(int e) { return __uint_as_float((u32)(127 + e) << 23); }
   // Eight values of q times a power of two, in parts.

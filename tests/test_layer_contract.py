@@ -153,3 +153,31 @@ def test_attention_of_trees_that_reach_into_a_page_of_several_holders(gpu, S, co
     assert np.isnan(ref).any() and np.isfinite(ref).any()
     got = A.run(K.to_library(svg, c, kind), qd, parent, T, shared=common or None)
     A.close(got, ref, A.bound(c, kind, spread, max(lens) + T))
+
+
+# -------------------------------------------------------- rows far from ordinary
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim,T,G", [(128, 1, 2), (64, 16, 3), (256, 5, 8)])
+@pytest.mark.parametrize("above", [2.0 ** 11, 2.0 ** 16, 2.0 ** 20])
+def test_one_channel_of_q_far_above_the_others(gpu, kind, dim, T, G, above):
+    """The keys hardly use the large channel, so the small ones decide: they keep their bits.  Beside the bound of the
+    ordinary rows, a value of q is off by 2^-38 of its row's largest at most (fp16 parts end at 2^-24, half a step of
+    which is 2^-25, and the largest is at least 2^13): a score by 2^-38 scale max|q| sum|k|."""
+    rng = np.random.default_rng(dim + T)
+    c = K.make(7, [1000], T, H=1, dim=dim, page=64)
+    A.fill(c, rng, kind)
+    cols = [3, dim - 2]
+    t = np.arange(64)
+    for d in cols:                       # 0 in the large channels
+        c["k"][0, :, 0, CO.key_at(t, d, dim)] = 0
+    q, _ = A.queries(rng, 1, T, G, dim)
+    q = q.copy()
+    q[..., cols] = np.float32(above) * np.sign(q[..., cols])
+    qd = C.to_dev(q.reshape(T, G, dim))
+    ref, spread = AO.attention(c, A.wide(kind), 0, q, None, T, None, dim ** -0.5)
+    tol = A.bound(c, kind, spread, 1000 + T)
+    if kind == "fp16":
+        most = np.abs(A.wide(kind)(c["k"][0, :, 0])).reshape(-1, 64 // 16, dim // 32, 4, 16, 8).sum((2, 3, 5)).max()
+        tol = tol + spread[..., 1] * 2 * 2.0 ** -38 * dim ** -0.5 * above * most
+    A.close(A.run(K.to_library(svg, c, kind), qd, None, T), ref, tol)
