@@ -200,8 +200,12 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *  Row (s, i, a): o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale * q . k_t), over the positions t < len[s] and
  *  len[s] + j for the nodes j of i's root path, i included.  Sums and accumulators are fp32; q and p
  *  enter the 16-bit matrix products in parts.  A value of q is off by 2^-22 of itself or 2^-38 of its row's largest,
- *  whichever is more (fp16), or 2^-24 of itself (bf16); p carries at least 16 bits, so an output is within about 1e-5 of
- *  its row's largest of an exact one.  Keys and values of tokens that a row does not see never reach it, whatever they are.
+ *  whichever is more (fp16), or 2^-24 of itself (bf16).  A p carries at least 16 bits; with an fp16 cache it also
+ *  loses up to 2^-36 of the largest that its wave has seen for the row, for each token of the wave's (long calls are
+ *  spread over 512 waves and more: 131072 tokens of 8 heads lose up to 2^-25 in all, what the whole memory holds 2^-15).  Without
+ *  that an output is within about 1e-5 of its row's largest |v| of an exact one while scores stay below about 50 (2^-22
+ *  of a score is an error of its exponential, as in fp32).
+ *  Keys and values of tokens that a row does not see never reach it, whatever they are.
  *  NaN rows: a node whose root path breaks the rule above, or meets a node in a page that other slots hold too (which
  *  kv_append has passed over); a row that reads a page number outside the cache; all of a slot whose pages do not cover
  *  len + n_nodes.

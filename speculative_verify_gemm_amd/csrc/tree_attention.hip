@@ -50,10 +50,11 @@
 // 2^-9 (bf16), which the fp32 consumers of the output would see.
 //
 // The running maximum is raised only when a score passes it by more than
-// 2^kSlack: until then probabilities above 1 are kept as they are (their scale
-// 2^kLift leaves fp16 room: at most 2^(kLift + kSlack) = 2^15), which takes the
-// exchange between lanes and the rescaling of O out of almost every tile (raised at every
-// tile, the 131033 tokens above take 183 us, the branches 77 instead of 70).
+// 2^kSlack: until then probabilities above 1 are kept as they are, which takes the
+// exchange between lanes and the rescaling of O out of almost every tile.  Probabilities are lifted by 2^kLift; fp16 has
+// room for 2^(kLift + kSlack) < 2^16.  Their low part ends at 2^-24, so each loses up to 2^-(24 + kLift) of the largest
+// that its wave has seen for the row (the sum keeps it): 2^-36 for each token of the wave's.  A wider slack is faster and loses
+// more: 32 branches behind 32768, kLift 9 and slack 6 67.7 us (2^-33), 12 and 3.9 68.4 us, 13 and 2.9 69.5 us, 14 and 1.9 71.4 us.
 #include "svg_cache.h"
 #include "svg_internal.h"
 
@@ -66,7 +67,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 512, kWaves = 8;
 constexpr int kMaxGroups = SVG_ATTN_MAX_GROUPS;
 constexpr int kMaxSlots = 1024;
-constexpr float kLift = 9.f, kSlack = 6.f;
 constexpr float kLow = -3e38f;       // the maximum before any token
 constexpr float kLowest = -3.402823466e38f;
 // A probability is 2^(f s + bias), bias = kLift - f m: one operation, off by half a step of f m.  Beyond
@@ -354,6 +354,7 @@ template <>
 struct Ops<false> {
   static constexpr int kQ = 2;     // parts of q
   static constexpr int kTop = 13;  // the power of two of a row's largest q
+  static constexpr float kLift = 12.f, kSlack = 3.875f;
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
   }
@@ -365,6 +366,7 @@ template <>
 struct Ops<true> {
   static constexpr int kQ = 3;
   static constexpr int kTop = 0;
+  static constexpr float kLift = 9.f, kSlack = 6.f;
   SVG_DEV static f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
   }
@@ -377,7 +379,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Two probabilities in two parts, packed: fp16 parts are cut off (what the first leaves, the second takes; the rest
-// is below 2^-21), bf16 parts are rounded.
+// is below 2^-21 of it or 2^-24, see above), bf16 parts are rounded.
 template <bool BF>
 SVG_DEV void split_pair(float x, float y, u32& hi, u32& lo) {
   if constexpr (BF) {
@@ -468,6 +470,7 @@ struct Pages {
 template <int D, bool BF, int RT>
 struct Attn {
   using O = Ops<BF>;
+  static constexpr float kLift = O::kLift, kSlack = O::kSlack;
   static constexpr int NQ = O::kQ, NC = D / 32, ND = D / 16;
   static constexpr int TILE = 128 * D;               // bytes of a tile: 32 keys, 32 values
   static constexpr int QBYTES = RT * NC * NQ * 1024;  // thin: q's parts in LDS

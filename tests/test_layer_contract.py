@@ -181,3 +181,51 @@ def test_one_channel_of_q_far_above_the_others(gpu, kind, dim, T, G, above):
         most = np.abs(A.wide(kind)(c["k"][0, :, 0])).reshape(-1, 64 // 16, dim // 32, 4, 16, 8).sum((2, 3, 5)).max()
         tol = tol + spread[..., 1] * 2 * 2.0 ** -38 * dim ** -0.5 * above * most
     A.close(A.run(K.to_library(svg, c, kind), qd, None, T), ref, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("low", [31.5, 33.5, 35.5, 39.5])
+def test_a_long_tail_of_small_probabilities(gpu, kind, low):
+    """One token and 2^18 others, each of them 2^-low of it: together 2^(18 - low).  256 slots over the same pages, so
+    that a workgroup has a slot and its waves an eighth of the tokens (thin) or half of them (thick).  A probability's two
+    fp16 parts lose up to 2^-36 of the largest that the wave has seen: 2^-36 for each token of a wave, which the others'
+    sums do not see.  Beside it stands the ordinary bound, relative to what it is the bound of: a score of one product
+    (q in parts; q's factor and the exponent rounded), the exponential, p in two parts, and sums of one sign over a
+    wave's tiles, eight rounded ones a tile."""
+    S, dim, page, N = 256, 64, 128, 1 << 18
+    k = torch.zeros((N, dim))
+    v = torch.zeros((N, dim))
+    at = 177777                          # the large one: not the first to be seen
+    k[at, 0] = 32.0
+    v[:, 1] = 1.0
+    v[at, 1] = 0.0
+    v[at, 2] = 1.0
+    P = N // page
+    pool = lambda: torch.zeros((1, P + S, 1, page * dim), dtype=K.TYPES[kind], device=C.DEV)  # noqa: E731
+    kp, vp = pool(), pool()
+    refs = torch.ones(P + S, dtype=torch.int32, device=C.DEV)
+    pages = torch.arange(P, dtype=torch.int32, device=C.DEV)
+    first = svg.KVCache(kp, vp, pages[None].contiguous(), A.i32([P]), A.i32([0]), refs, dim=dim, page=page)
+    svg.kv_append(first, 0, k.to(C.DEV), v.to(C.DEV), N)
+    own = torch.arange(P, P + S, dtype=torch.int32, device=C.DEV)[:, None]   # for the tree's token: a zero key and value
+    refs[:P] = S
+    cache = svg.KVCache(kp, vp, torch.cat((pages.expand(S, P), own), 1).contiguous(), A.i32([P + 1] * S), A.i32([N] * S), refs,
+                        dim=dim, page=page)
+    for G, part in ((1, N // 8), (40, N // 2)):
+        q = np.zeros((S, G, dim), np.float32)
+        q[:, :, 0] = low * np.log(2.0) / 32.0
+        got = A.run(cache, C.to_dev(q), None, 1, scale=1.0)[:, 0]
+        x = 32.0 * float(q[0, 0, 0])     # the large one's score; all others have 0
+        e = np.exp(-x)
+        total = 1 + N * e                # (N - 1 others and the tree's own)
+        u = 2.0 ** -11 if kind == "fp16" else 2.0 ** -8
+        score = x * ((u ** 2 if kind == "fp16" else u ** 3) + 3 * 2.0 ** -24)
+        tol = 2 * (score + 2.0 ** -20 + u ** 2 + (8 * part / 32 + 64) * 2.0 ** -24)
+        lost = part * 2.0 ** -36 if kind == "fp16" else 0.0
+        tail = (N - 1) * e / total
+        err = np.abs(got[:, :, 1] - tail).max()
+        print(f"{kind} 2^-{low} G={G}: tail {tail:.3e}, off by {err:.3e} of {tail * tol + lost:.3e}", flush=True)
+        assert err <= tail * tol + lost
+        assert np.abs(got[:, :, 2] - 1 / total).max() <= tol + lost
+        assert (got[:, :, 3:] == 0).all() and (got[:, :, 0] == 0).all()
