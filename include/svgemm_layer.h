@@ -205,13 +205,18 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *  spread over 512 waves and more: 131072 tokens of 8 heads lose up to 2^-25 in all, what the whole memory holds 2^-15).  Without
  *  that an output is within about 1e-5 of its row's largest |v| of an exact one while scores stay below about 50 (2^-22
  *  of a score is an error of its exponential, as in fp32).
- *  Keys and values of tokens that a row does not see never reach it, whatever they are.
+ *  Keys and values of tokens that a row does not see never reach it, whatever they are.  Of those it sees (kv_append rounds
+ *  what an fp16 cache cannot hold to infinity): a key that is not finite gives a NaN row where a score is NaN or
+ *  +infinity, and may where it is -infinity, which by the definition only leaves the token out (the parts of q decide);
+ *  a value that is not finite makes its own element of the row NaN or infinite (unless the token's p is small enough to
+ *  be lost, see above), and no other.
  *  NaN rows: a node whose root path breaks the rule above, or meets a node in a page that other slots hold too (which
  *  kv_append has passed over); a row that reads a page number outside the cache; all of a slot whose pages do not cover
  *  len + n_nodes.
- *  Reads table, pages, len, and refs where it is not NULL (without it no node is passed over).  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the
- *  cache or a scale that is not finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads,
- *  ld_q, or a table so large that n_slots * width * page * heads times the blocks of 128 rows of an item nears 2^36; SVG_EALIGN.
+ *  Reads table, pages, len, and refs where it is not NULL (without it no node is passed over).
+ *  Errors: SVG_EINVAL for a null required pointer, T < 1, q_heads < 1, a layer outside the cache or a scale that is not
+ *  finite; SVG_EUNSUPPORTED for a cache outside its limits, T > SVG_TREE_MAX_NODES, q_heads, ld_q, or a table so large that
+ *  n_slots * width * page * heads times the blocks of 128 rows of an item nears 2^36; SVG_EALIGN.
  *
  * tree_attention_workspace -- the bytes of that workspace (host only).
  */

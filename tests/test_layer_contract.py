@@ -229,3 +229,47 @@ def test_a_long_tail_of_small_probabilities(gpu, kind, low):
         assert err <= tail * tol + lost
         assert np.abs(got[:, :, 2] - 1 / total).max() <= tol + lost
         assert (got[:, :, 3:] == 0).all() and (got[:, :, 0] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("T,G,common", [(1, 4, 0), (3, 2, 64), (32, 8, 0), (20, 3, 64)])
+def test_committed_keys_and_values_that_are_not_finite(gpu, kind, T, G, common):
+    """A committed key of +-infinity or NaN: the rows of its head are NaN, or those of the definition (a score of
+    -infinity leaves the token out); a value: its own element is not finite.  No other head, slot or element has them."""
+    rng = np.random.default_rng(T + G)
+    S, H, dim, page = 2, 2, 64, 32
+    lens = [common + 40, common + 3]
+    c = K.make(3, lens, T, H=H, dim=dim, page=page)
+    A.fill(c, rng, kind)
+    A.share(c, 0, common)
+    q, qd = A.queries(rng, S, T, H * G, dim)
+    clean, spread = AO.attention(c, A.wide(kind), 0, q, None, T, None, dim ** -0.5)
+    tol = A.bound(c, kind, spread, max(lens) + T)
+    inf, nan = (0x7C00, 0x7E00) if kind == "fp16" else (0x7F80, 0x7FC0)
+    for pos in (5, lens[0] - 1):         # in a whole tile, and in the tile where the tree begins
+        hit = [0, 1] if pos < common else [0]
+        for pat in np.array([nan, inf, inf | 0x8000], np.uint16).view(np.int16):
+            d = K.copy_of(c)
+            key, value = (np.array(x) for x in CO.token(d, 0, 0, pos))
+            key[0, 7] = pat
+            CO.put(d, 0, 0, pos, key, value)
+            got = A.run(K.to_library(svg, d, kind), qd, None, T, shared=common or None)
+            with np.errstate(invalid="ignore"):
+                ref, _ = AO.attention(d, A.wide(kind), 0, q, None, T, None, dim ** -0.5)
+            for s in range(S):
+                for a in range(H * G):
+                    if s in hit and a < G:
+                        out = np.isnan(got[s, :, a]).all(-1)
+                        assert out[np.isnan(ref[s, :, a]).all(-1)].all()
+                        A.close(got[s, ~out, a], ref[s, ~out, a], tol[s, ~out, a])
+                    else:
+                        A.close(got[s, :, a], clean[s, :, a], tol[s, :, a])
+            d = K.copy_of(c)
+            key, value = (np.array(x) for x in CO.token(d, 0, 0, pos))
+            value[1, 9] = pat
+            CO.put(d, 0, 0, pos, key, value)
+            got = A.run(K.to_library(svg, d, kind), qd, None, T, shared=common or None)
+            assert not np.isfinite(got[hit][:, :, G:, 9]).any()
+            got[hit, :, G:, 9] = clean[hit, :, G:, 9]
+            A.close(got, clean, tol)
