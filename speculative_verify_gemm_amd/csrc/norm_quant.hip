@@ -78,11 +78,16 @@ SVG_DEV double wave_sum_f64(double v) {
   return (lane_f64(v, 0) + lane_f64(v, 16)) + (lane_f64(v, 32) + lane_f64(v, 48));
 }
 
+// A launch has fewer than 2^32 work-items a dimension: rows go on in y.
+constexpr int kRowsX = 1 << 20;
+static_assert(1024ull * kRowsX < (1ull << 32), "work-items of a row of the grid");
+
 template <int NT, int CPT, int B>
 __global__ __launch_bounds__(NT) void k_norm_quant(NormArgs a) {
   __shared__ double sums[16];
   __shared__ float red[16];
-  const int m = blockIdx.x, K = a.K;
+  const int m = (int)(blockIdx.y * kRowsX + blockIdx.x), K = a.K;
+  if (m >= a.M) return;
   const u32 nchunk = (u32)K >> 2, tid = threadIdx.x;
   const u32 xb = a.x_type == SVG_F32 ? 4u : 2u, wb = a.w_type == SVG_F32 ? 4u : 2u;
   const rsrc_t xr = make_rsrc(static_cast<const char*>(a.x) + (size_t)m * K * xb, (u32)K * xb);
@@ -151,7 +156,8 @@ __global__ __launch_bounds__(NT) void k_norm_quant(NormArgs a) {
 template <int B>
 void launch(const NormArgs& a, hipStream_t stream) {
   const int nchunk = a.K / 4;
-#define SVG_NORM(NT, CPT) hipLaunchKernelGGL((k_norm_quant<NT, CPT, B>), dim3(a.M), dim3(NT), 0, stream, a)
+  const dim3 grid(a.M < kRowsX ? a.M : kRowsX, (a.M + kRowsX - 1) / kRowsX);
+#define SVG_NORM(NT, CPT) hipLaunchKernelGGL((k_norm_quant<NT, CPT, B>), grid, dim3(NT), 0, stream, a)
   if (nchunk <= 2048 && a.M >= (nchunk <= 1024 ? 512 : 1024)) {
     if (nchunk <= 256) SVG_NORM(256, 1);
     else if (nchunk <= 512) SVG_NORM(256, 2);

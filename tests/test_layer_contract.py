@@ -273,3 +273,22 @@ def test_committed_keys_and_values_that_are_not_finite(gpu, kind, T, G, common):
             assert not np.isfinite(got[hit][:, :, G:, 9]).any()
             got[hit, :, G:, 9] = clean[hit, :, G:, 9]
             A.close(got, clean, tol)
+
+
+# ------------------------------------------------------------ sizes at the limits
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1 << 20, (1 << 20) + 1, (1 << 24) - 33, 1 << 24])
+def test_norm_of_as_many_rows_as_it_takes(gpu, M):
+    """Up to 2^24 rows, past what one dimension of a grid holds: the codes of the same rows in calls of 2^18."""
+    K_, part = 32, 1 << 18
+    g = torch.Generator(device=C.DEV).manual_seed(M)
+    x = torch.randn((M, K_), device=C.DEV, dtype=torch.float16, generator=g)
+    w = torch.randn(K_, device=C.DEV, generator=g)
+    signs = (torch.randint(0, 2, (K_,), device=C.DEV, generator=g) * 2 - 1).to(torch.int8)
+    new = lambda: (torch.zeros((M, K_), dtype=torch.int8, device=C.DEV), torch.zeros(M, device=C.DEV))  # noqa: E731
+    (xq, xs), (pq, ps) = new(), new()
+    svg.add_rmsnorm_quant_i8(x, None, w, 1e-5, signs, xq, xs)
+    for a in range(0, M, part):
+        b = min(a + part, M)
+        svg.add_rmsnorm_quant_i8(x[a:b], None, w, 1e-5, signs, pq[a:b], ps[a:b])
+    assert torch.equal(xq, pq) and torch.equal(xs, ps) and bool((xs > 0).all())
