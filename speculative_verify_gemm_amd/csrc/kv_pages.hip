@@ -399,7 +399,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_copy(svg_kv_cache c, const int3
 
 hipError_t svg_launch_kv_append(const svg_kv_cache& c, int layer, const float* k, int64_t ld_k, const float* v,
                                 int64_t ld_v, int T, const int32_t* n_rows, hipStream_t stream) {
-  const dim3 grid((unsigned)(((long)T + 3) / 4 + 1), c.heads, c.n_slots);
+  // no more positions than a table row has (a dimension of the grid holds fewer than 2^32 work-items; T may be 2^31 - 1)
+  const long most = (long)c.width * c.page, rows = T < most ? T : most;
+  const dim3 grid((unsigned)((rows + 3) / 4 + 1), c.heads, c.n_slots);
   if (c.type == SVG_BF16)
     hipLaunchKernelGGL(k_kv_append<true>, grid, dim3(64), 0, stream, c, layer, k, (long)ld_k, v, (long)ld_v, T, n_rows);
   else

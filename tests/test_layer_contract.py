@@ -292,3 +292,19 @@ def test_norm_of_as_many_rows_as_it_takes(gpu, M):
         b = min(a + part, M)
         svg.add_rmsnorm_quant_i8(x[a:b], None, w, 1e-5, signs, pq[a:b], ps[a:b])
     assert torch.equal(xq, pq) and torch.equal(xs, ps) and bool((xs > 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1 << 28, (1 << 31) - 1])
+def test_append_of_more_rows_than_any_table_holds(gpu, T):
+    """T itself is not limited by the table: rows without a place are passed over, however many there could be.  (The C
+    call: n_rows says that only the first rows are there.)"""
+    c = K.make(9, [5], 40, H=1, dim=64, page=32)
+    cache = K.to_library(svg, c)
+    x = torch.randn((2, 70, 64), generator=torch.Generator().manual_seed(1))
+    d, n = x.to(C.DEV), A.i32([70])
+    stream = torch.cuda.current_stream().cuda_stream
+    assert svg.lib.kv_append(cache._ref, 0, d[0].data_ptr(), 64, d[1].data_ptr(), 64, T, n.data_ptr(), stream) == 0
+    pat = K.bits(x.half()).reshape(2, 1, 70, 1, 64)
+    CO.append(c, 0, pat[0], pat[1], 70, [70])
+    K.same(cache, c)
