@@ -119,7 +119,9 @@ class KVCache:
     include/svgemm_layer.h): k, v fp16 or bf16 [n_layers, n_pages, heads, page *
     dim]; table int32 [n_slots, width], pages and len [n_slots], refs [n_pages]
     (without them only kv_copy_pages takes the cache).  The object keeps the
-    tensors; their contents are read by the calls on the device only."""
+    tensors; their contents are read by the calls on the device only.  k, v and
+    the tables may be set to other tensors of the same shape, type and device
+    (calls that a graph has captured go on with the ones they were made with)."""
 
     def __init__(self, k, v, table=None, pages=None, len=None, refs=None, *, dim, page):
         dev = _device(k, "k")
@@ -139,13 +141,24 @@ class KVCache:
                 if t is None or t.shape != (n,):
                     raise ValueError(f"{name} must have shape [{n}]")
                 setattr(c, name, _tensor(t, name, torch.int32, dev))
-        self.k, self.v, self.table, self.pages, self.len, self.refs = k, v, table, pages, len, refs
+        self._t = dict(k=k, v=v, table=table, pages=pages, len=len, refs=refs)
         self.dim, self.page, self.heads, self.device = dim, page, H, dev
         self.n_layers, self.n_pages = L, P
         self.n_slots, self.width = c.n_slots, c.width
         self._c = c
         self._ref = ctypes.byref(c)
         self._attn_bytes = {}  # workspace sizes by (q_heads, T)
+
+    def _set(self, name, t):
+        now = self._t[name]
+        if t is now:  # (also after cache.len += n)
+            return
+        if now is None:
+            raise ValueError(f"the cache has no {name}")
+        if t is None or t.shape != now.shape:
+            raise ValueError(f"{name} must have shape {list(now.shape)}")
+        setattr(self._c, name, _tensor(t, name, now.dtype, self.device))
+        self._t[name] = t
 
     @classmethod
     def empty(cls, n_layers, n_pages, heads, dim, page, n_slots, width, dtype=torch.float16, device="cuda"):
@@ -160,6 +173,10 @@ class KVCache:
         """The same pages and counts with tables of their own (empty slots): what kv_fork writes to."""
         return KVCache(self.k, self.v, torch.full_like(self.table, -1), torch.zeros_like(self.pages),
                        torch.zeros_like(self.len), self.refs, dim=self.dim, page=self.page)
+
+
+for _name in ("k", "v", "table", "pages", "len", "refs"):
+    setattr(KVCache, _name, property(lambda self, n=_name: self._t[n], lambda self, t, n=_name: self._set(n, t)))
 
 
 def _rows(t, name, cache, width):

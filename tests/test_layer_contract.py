@@ -308,3 +308,43 @@ def test_append_of_more_rows_than_any_table_holds(gpu, T):
     pat = K.bits(x.half()).reshape(2, 1, 70, 1, 64)
     CO.append(c, 0, pat[0], pat[1], 70, [70])
     K.same(cache, c)
+
+
+# ------------------------------------------------------------------ the binding
+@pytest.mark.gpu
+def test_the_caches_tensors_may_be_replaced(gpu):
+    """Lengths that alternate between two tensors, as a program keeps them that commits into the other one; tables
+    and pages likewise."""
+    T, lens = 4, [10, 33]
+    c = K.make(2, lens, 40, H=1, dim=64, page=32)
+    cache = K.to_library(svg, c)
+    other = torch.zeros_like(cache.len)
+    path = np.full((2, T), -1, np.int32)
+    path[:, 0] = 2
+    for turn in range(3):
+        k, v, kp, vp = rows(turn, 2, T)
+        k, v, kp, vp = k[:, :64].contiguous(), v[:, :64].contiguous(), kp[:, :, :1], vp[:, :, :1]
+        svg.kv_append(cache, 0, k, v, T)
+        CO.append(c, 0, kp, vp, T)
+        svg.kv_commit(cache, A.i32(path), A.i32([2, 2]), other)
+        c["len"] = CO.commit(c, path, [2, 2])
+        cache.len, other = other, cache.len
+        K.same(cache, c)
+    cache.len += A.i32([1, 0])           # in place: the same tensor
+    c["len"][0] += 1
+    table = cache.table.clone()
+    cache.table.fill_(-1)                # the old one is not looked at any more
+    cache.table = table
+    cache.k, cache.v = cache.k.clone(), cache.v.clone()
+    k, v, kp, vp = rows(7, 2, T)
+    svg.kv_append(cache, 0, k[:, :64].contiguous(), v[:, :64].contiguous(), T)
+    CO.append(c, 0, kp[:, :, :1], vp[:, :, :1], T)
+    K.same(cache, c)
+    for name, t, err in (("len", torch.zeros(3, dtype=torch.int32, device=C.DEV), ValueError), ("len", cache.len.long(), TypeError),
+                         ("len", cache.len.cpu(), ValueError), ("refs", None, ValueError), ("k", cache.k.bfloat16(), TypeError),
+                         ("table", table.t().contiguous().t(), ValueError)):
+        with pytest.raises(err):
+            setattr(cache, name, t)
+    K.same(cache, c)
+    with pytest.raises(ValueError):
+        svg.KVCache(cache.k, cache.v, dim=64, page=32).len = cache.len
