@@ -287,7 +287,7 @@ def tree_attention(cache, layer, q, parent, out, workspace, scale=None, n_nodes=
     S, D = cache.n_slots, cache.dim
     heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // D
     pq, ld, n = _rows(q, "q", cache, heads * D)
-    T = n // S if S else 1
+    T = n // S if S else (1 if parent is None or parent.dim() < 2 else parent.shape[1])  # (no slots: an empty call)
     if n != S * T:
         raise ValueError("q must have n_slots * T rows")
     if out.shape != q.shape:

@@ -348,3 +348,25 @@ def test_the_caches_tensors_may_be_replaced(gpu):
     K.same(cache, c)
     with pytest.raises(ValueError):
         svg.KVCache(cache.k, cache.v, dim=64, page=32).len = cache.len
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 5])
+def test_no_slots_are_empty_calls(gpu, T):
+    """A cache of no slots: every call of the binding is a call of nothing, whatever the trees' size."""
+    cache = svg.KVCache.empty(1, 4, 2, 64, 32, 0, 3, device=C.DEV)
+    none = lambda *s: torch.zeros((0, *s), dtype=torch.int32, device=C.DEV)  # noqa: E731
+    q = torch.zeros((0, 4, 64), device=C.DEV)
+    ws = svg.tree_attention_workspace(cache, 4, T)
+    svg.tree_attention(cache, 0, q, none(T), torch.zeros_like(q), ws)
+    svg.tree_attention(cache, 0, q, none(T), torch.zeros_like(q), ws, n_nodes=none(), shared=A.i32([32]))
+    svg.tree_attention(cache, 0, q, None, torch.zeros_like(q), ws)
+    with pytest.raises(ValueError):
+        svg.tree_attention(cache, 0, q, A.i32(np.zeros((1, T))), torch.zeros_like(q), ws)
+    kv = torch.zeros((0, 2, 64), device=C.DEV)
+    svg.kv_append(cache, 0, kv, kv, T, n_rows=none())
+    svg.kv_commit(cache, none(T), none())
+    svg.kv_fork(cache, none(), cache.other_tables())
+    svg.kv_reserve(cache, none(), none(), svg.kv_workspace(cache))
+    torch.cuda.synchronize()
+    assert not C.host(cache.refs).any()
