@@ -41,9 +41,19 @@ CFLAGS = [
 LESS_FLAGS = {"tree_attention.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
 
 
+def flags_of(src: str) -> list:
+    """The compile flags of one source."""
+    flags = list(CFLAGS)
+    less = LESS_FLAGS.get(src)
+    if less:
+        at = next(i for i in range(len(flags)) if tuple(flags[i:i + len(less)]) == less)
+        del flags[at:at + len(less)]
+    return flags
+
+
 def source_digest() -> str:
     """Digest of everything that decides the built kernels: the sources, the
-    public headers and the compile flags.  Profile summaries record it, so a
+    public headers and each source's compile flags.  Profile summaries record it, so a
     counter reading can be matched to the code it was taken on."""
     import hashlib
     h = hashlib.sha256()
@@ -55,7 +65,8 @@ def source_digest() -> str:
     for name in ("svgemm.h", "svgemm_layer.h"):
         with open(os.path.join(ROOT, "include", name), "rb") as f:
             h.update(f.read())
-    h.update(" ".join(CFLAGS[:-4]).encode())  # flags, without the include paths
+    for src in SOURCES:
+        h.update(" ".join([src, *flags_of(src)[:-4]]).encode())  # flags, without the include paths
     return h.hexdigest()[:16]
 
 
@@ -68,12 +79,7 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-    flags = list(CFLAGS)
-    less = LESS_FLAGS.get(src)
-    if less:
-        at = next(i for i in range(len(flags)) if tuple(flags[i:i + len(less)]) == less)
-        del flags[at:at + len(less)]
-    cmd = [hipcc(), *flags, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *flags_of(src), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

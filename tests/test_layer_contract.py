@@ -370,3 +370,17 @@ def test_no_slots_are_empty_calls(gpu, T):
     svg.kv_reserve(cache, none(), none(), svg.kv_workspace(cache))
     torch.cuda.synchronize()
     assert not C.host(cache.refs).any()
+
+
+# ------------------------------------------------------------------- the build
+def test_the_digest_covers_the_flags_of_each_source(monkeypatch):
+    from speculative_verify_gemm_amd import build as B
+    less = B.LESS_FLAGS["tree_attention.hip"]
+    assert all(f not in B.flags_of("tree_attention.hip") for f in less[1:]) and all(f in B.flags_of("layout.hip") for f in less)
+    now = B.source_digest()
+    monkeypatch.setattr(B, "LESS_FLAGS", {})
+    assert B.source_digest() != now
+    monkeypatch.setattr(B, "LESS_FLAGS", {"tree_attention.hip": less, "layout.hip": less})
+    assert B.source_digest() != now
+    monkeypatch.setattr(B, "LESS_FLAGS", {"tree_attention.hip": less})
+    assert B.source_digest() == now
