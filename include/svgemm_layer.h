@@ -70,7 +70,8 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
  *  pages     int32 [n_slots]: entries of each row that are in use.
  *  len       int32 [n_slots]: committed tokens of each slot.
  *  refs      int32 [n_pages]: the number of slots that hold each page; a page is
- *            free where it is 0.  A page that several slots hold (a count above 1) is never written.
+ *            free where it is 0.  A page that several slots hold (a count above 1) is never written but by
+ *            kv_copy_pages, which goes by the page numbers that it is given.
  *  (table, pages, len, refs: 4-byte aligned.  Each call names the ones it needs.)
  *
  * A page holds head after head, page * dim values each, in the lane order of
@@ -190,7 +191,7 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *            idle); NULL: all T.  Behind a slot's nodes rows of q do not matter and rows of out are left as they were.
  *  shared    int32 [1] or NULL: a number of leading tokens that are the same pages in the
  *            table rows of all slots that are not idle (as after kv_fork).  They are read once for
- *            all rows.  What is used is the largest multiple of 32 that neither this number nor any
+ *            every 128 rows of a head (slots * T * query heads of it).  What is used is the largest multiple of 32 that neither this number nor any
  *            of those slots' len is below; it does not change what is computed.
  *  scale     finite; the scores are scale * q . k.
  *  out       fp32 [n_slots * T][q_heads * dim], 16-byte aligned.

@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(svg_kv_cache c, const int3
       }
     }
   }
-  // free pages, four counts a load where the array allows it
+  // free pages, a count a thread and turn
   int found = 0;
   for (int i = s; i < c.n_pages; i += kPlan) found += c.refs[i] == 0;
   int n_free;
