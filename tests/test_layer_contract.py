@@ -384,3 +384,80 @@ def test_the_digest_covers_the_flags_of_each_source(monkeypatch):
     assert B.source_digest() != now
     monkeypatch.setattr(B, "LESS_FLAGS", {"tree_attention.hip": less})
     assert B.source_digest() == now
+
+
+@pytest.mark.gpu
+def test_without_counts_no_page_is_passed_over(gpu):
+    """refs NULL (the C calls): append, attention and commit go by the tables alone."""
+    T = 8
+    c, cache = refused_forks()
+    cache._c.refs = None
+    c["refs"][:] = 0
+    k, v, kp, vp = rows(4, 3, T)
+    n = [T, T, 0]                        # one of the two slots over the same page
+    svg.kv_append(cache, 1, k, v, T, n_rows=A.i32(n))
+    CO.append(c, 1, kp, vp, T, n)
+    K.same(cache, c, ("k", "v"))
+    q, qd = A.queries(np.random.default_rng(8), 3, T, 4, 64)
+    ref, spread = AO.attention(c, A.wide("fp16"), 1, q, None, T, n, 64 ** -0.5)
+    got = A.run(cache, qd, None, T, layer=1, n_nodes=n)
+    assert np.isfinite(ref[:2]).all()
+    A.close(got[:2], ref[:2], A.bound(c, "fp16", spread, 80)[:2])
+    path = np.full((3, T), -1, np.int32)
+    path[:, 0] = 4
+    svg.kv_commit(cache, A.i32(path), A.i32([2, 2, 0]))
+    c["len"] = CO.commit(c, path, [2, 2, 0])
+    assert list(c["len"]) == [12, 42, 40]
+    K.same(cache, c, ("k", "v", "len"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("seed,kind,careful", [(1, "fp16", False), (2, "bf16", False), (3, "fp16", True), (4, "bf16", True)])
+def test_serving_from_a_pool_that_is_too_small(gpu, seed, kind, careful):
+    """Turns of fork, reserve, append, attention and commit with refusals in most of them; every call against the oracle.
+    careful: refused slots are given no rows, nodes and tokens; otherwise the program goes on with them."""
+    S, T, H, G, dim, page = 6, 12, 2, 2, 64, 32
+    rng = np.random.default_rng(seed)
+    c = K.make(seed, [int(x) for x in rng.integers(1, 70, S)], 0, H=H, dim=dim, page=page, spare=0, width=12)
+    A.fill(c, rng, kind)
+    cache = K.to_library(svg, c, kind)
+    ws, kv_ws, status = svg.tree_attention_workspace(cache, H * G, T), svg.kv_workspace(cache), A.i32([0] * S)
+    refused = nan_slots = 0
+    for turn in range(14):
+        src = np.where(rng.random(S) < 0.12, rng.integers(0 if turn % 5 else -1, S, S), np.arange(S))
+        other = cache.other_tables()
+        svg.kv_fork(cache, A.i32(src), other)
+        c, cache = CO.fork(c, src), other
+        K.same(cache, c)
+        assert np.array_equal(CO.holders(c), c["refs"])
+        n = rng.integers(0, T + 1, S)
+        svg.kv_reserve(cache, A.i32(n), status, kv_ws)
+        state = CO.reserve(c, n)
+        assert np.array_equal(C.host(status), state)
+        K.same(cache, c)
+        refused += int((state != 0).sum())
+        if careful:
+            n = np.where(state == 0, n, 0)
+        k, v, kp, vp = rows(100 * seed + turn, S, T, kind)
+        svg.kv_append(cache, 0, k, v, T, n_rows=A.i32(n))
+        CO.append(c, 0, kp, vp, T, n)
+        K.same(cache, c)
+        parent = A.trees(rng, S, T)
+        q, qd = A.queries(rng, S, T, H * G, dim)
+        covered = c["len"] + n <= c["pages"] * page
+        ref, spread = AO.attention(c, A.wide(kind), 0, q, parent, T, np.where(covered, n, 0), dim ** -0.5)
+        tol = A.bound(c, kind, spread, int(c["len"].max()) + T)
+        got = A.run(cache, qd, parent, T, n_nodes=n, workspace=ws)
+        for s in range(S):
+            A.close(got[s, :n[s]], ref[s, :n[s]], tol[s, :n[s]])
+            assert (got[s, n[s]:] == 7.0).all()
+            nan_slots += bool(np.isnan(got[s, :n[s]]).any())
+        count = np.minimum(rng.integers(1, T + 1, S), n)
+        path = np.full((S, T), -1, np.int32)
+        for s in range(S):
+            if count[s] > 1:
+                path[s, :count[s] - 1] = np.sort(rng.choice(np.arange(1, n[s]), size=count[s] - 1, replace=False))
+        svg.kv_commit(cache, A.i32(path), A.i32(count))
+        c["len"] = CO.commit(c, path, count)
+        K.same(cache, c)
+    assert refused > 3 and (nan_slots > 0) != careful
