@@ -110,8 +110,9 @@ SVG_DEV Moves moves_of(const svg_kv_cache& c, int s, int T, const int32_t* path,
 
 // One workgroup per (head, layer, slot): all rows are read before any is written (a row's place may be another's source).
 // The two pages and the places in them are looked up once, by one wave, while nothing else waits.
-// Bound by latency: a chain of the path, the table and the rows (8 slots of 16 nodes, 32 layers of 8 heads of 128,
-// 16.8 MB read and written: 12 us; every thread looking its places up by itself: 18.4 us).
+// Bound by latency, a chain of the path, the table and the rows, and by the lines that the values touch: a token's lie in
+// 2-byte pieces 16 bytes apart (8 slots of 16 nodes, 32 layers of 8 heads of 128: 8.4 MB moved, 23.4 MB read and 16.3 MB written
+// by the counters, 12 to 13 us; every thread looking its places up by itself: 18.4 us).
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void k_kv_commit(svg_kv_cache c, int T, const int32_t* __restrict__ path,
                                                        const int32_t* __restrict__ n_emit, int32_t* len_out) {
