@@ -151,8 +151,6 @@ class KVCache:
 
     def _set(self, name, t):
         now = self._t[name]
-        if t is now:  # (also after cache.len += n)
-            return
         if now is None:
             raise ValueError(f"the cache has no {name}")
         if t is None or t.shape != now.shape:
