@@ -191,8 +191,9 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *            idle); NULL: all T.  Behind a slot's nodes rows of q do not matter and rows of out are left as they were.
  *  shared    int32 [1] or NULL: a number of leading tokens that are the same pages in the
  *            table rows of all slots that are not idle (as after kv_fork).  They are read once for
- *            every 128 rows of a head (slots * T * query heads of it).  What is used is the largest multiple of 32 that neither this number nor any
- *            of those slots' len is below; it does not change what is computed.
+ *            every 128 rows of a head (slots * T * query heads of it).  What is used is the largest
+ *            multiple of 32 that neither this number nor any of those slots' len is below; it does not
+ *            change what is computed.
  *  scale     finite; the scores are scale * q . k.
  *  out       fp32 [n_slots * T][q_heads * dim], 16-byte aligned.
  *  workspace tree_attention_workspace() bytes, 256-byte aligned; its contents need not be set or kept.

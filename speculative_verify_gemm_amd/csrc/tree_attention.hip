@@ -32,16 +32,16 @@
 //    directly and run STEPS - 1 steps ahead, one barrier a step.  Bound by the matrix unit.
 // A shared prefix that is walked the thick way and slots that are walked the thin way are one launch.
 //
-// Measured (kernel + join, medians of a kernel trace, us; bytes and the matrix units' busy share by counters):
-//   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16             9.5 + 3.9   a chain of dependent loads
-//   16 nodes, 8206 seen, 32 heads of 128, fp16                           25.8 + 4.5   bytes: 137 MB, 5.3 TB/s
-//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16                    191 + 8.4   products: 172 GFLOP in five parts, 0.9
-//                                   (156 to 200 as the clock goes)                    PFLOP/s, units busy 47 % (a library
-//                                                                                     product of 8192^3: 68 %); 542 MB
-//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16     69.9 + 5.8   bytes and products side by side: 277 MB,
-//                                                                                     39 GFLOP in four parts, units busy 21 %
-//   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16    25.6 + 6.3   a few tiles a workgroup: its start, and
-//                                                                                     27 MB of partials for 22 MB read
+// Measured (kernel + join in a kernel trace, us; bytes and the matrix units' busy share by counters):
+//   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16        9 to 10 + 4     a chain of dependent loads
+//   16 nodes, 8206 seen, 32 heads of 128, fp16                               26 + 4.5   bytes: 139 MB, 5.3 TB/s
+//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16     190 to 195 on average + 8.5 products: 172 GFLOP in five parts, 0.9
+//                           (155 to 215 as the clock goes)                              PFLOP/s, units busy 46 % (a library
+//                                                                                       product of 8192^3: 67 %); 562 MB
+//   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16         70 + 6     bytes and products side by side: 289 MB,
+//                                                                                       39 GFLOP in four parts, units busy 21 %
+//   6 trees of 7 nodes, 301 tokens behind 4992, 2 heads of 256 for 16      25.5 + 6.4   a few tiles a workgroup: its start, and
+//                                                                                       27 MB of partials for 22 MB read
 //
 // Precision.  q is fp32 and the keys 16-bit: q is normalised per row by a power of
 // two and split into 16-bit parts (two of fp16: 22 bits; three of bf16: 24 bits), one
