@@ -103,7 +103,7 @@ SVG_DEV Moves moves_of(const svg_kv_cache& c, int s, int T, const int32_t* path,
   if (ok) {
     const int last = n > 1 ? __shfl(p, n - 2) : 0;
     int page;
-    ok = own_page_of(c, s, (long)len / c.page, page) && own_page_of(c, s, ((long)len + last) / c.page, page);
+    ok = !__any(!own_page_of(c, s, ((long)len + (lane & 1 ? last : 0)) / c.page, page));  // (both pages at once)
   }
   return {ok ? n : 0, len, p};
 }
