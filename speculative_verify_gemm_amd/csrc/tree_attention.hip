@@ -35,7 +35,7 @@
 // Measured (kernel + join in a kernel trace, us; bytes and the matrix units' busy share by counters):
 //   1 token, 1001 seen, 8 heads of 128 for 32 query heads, fp16        9 to 10 + 4     a chain of dependent loads
 //   16 nodes, 8206 seen, 32 heads of 128, fp16                               26 + 4.5   bytes: 139 MB, 5.3 TB/s
-//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16     190 to 195 on average + 8.5 products: 172 GFLOP in five parts, 0.9
+//   32 nodes, 131033 seen, 8 heads of 128 for 32, bf16     180 to 200 on average + 8.5 products: 172 GFLOP in five parts, 0.9
 //                           (155 to 215 as the clock goes)                              PFLOP/s, units busy 46 % (a library
 //                                                                                       product of 8192^3: 67 %); 562 MB
 //   32 slots of up to 2000 tokens behind 32768, 8 heads for 32, fp16         70 + 6     bytes and products side by side: 289 MB,
