@@ -22,7 +22,7 @@ import os
 
 import torch
 
-from . import layer
+from . import layer, prompt
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsvgemm.so")
@@ -70,6 +70,7 @@ def _load():
     lib.svg_last_error.argtypes = []
     lib.svg_last_error.restype = ctypes.c_char_p
     layer._bind(lib)
+    prompt._bind(lib)
     return lib
 
 
@@ -538,3 +539,6 @@ class LinearPass:
 # --------------------------------------- the steps around the linears (layer.py)
 from .layer import (KVCache, add_rmsnorm_quant_i8, kv_append, kv_commit, kv_copy_pages,  # noqa: E402,F401
                     kv_fork, kv_reserve, kv_workspace, tree_attention, tree_attention_workspace)
+# ------------------------------------------ a prompt's pass (prompt.py)
+from .prompt import (Rope, RowMap, gated_quant_i8, kv_row_map, prompt_attention,  # noqa: E402,F401
+                     prompt_attention_workspace, rope_append, w4a8_prompt_linear, w8a8_prompt_linear)

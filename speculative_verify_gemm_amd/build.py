@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libsvgemm.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["rht_quant.hip", "linear_w4.hip", "linear_w8.hip", "tree_accept.hip", "tree_deltanet.hip",
            "pass.hip", "layout.hip", "svgemm.hip", "norm_quant.hip", "kv_pages.hip",
-           "tree_attention.hip", "layer.hip"]
+           "tree_attention.hip", "layer.hip", "prompt_rows.hip", "prompt_attention.hip", "prompt_linear.hip",
+           "gated_quant.hip", "prompt.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [
@@ -36,9 +37,9 @@ CFLAGS = [
 ]
 
 
-# Sources compiled without one of the flags: the attention's accumulators take
-# turns with its operands, and the compiler is left to place them.
-LESS_FLAGS = {"tree_attention.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
+# Sources compiled without one of the flags: the attentions' accumulators take
+# turns with their operands, and the compiler is left to place them.
+LESS_FLAGS = {name: ("-mllvm", "-amdgpu-mfma-vgpr-form") for name in ("tree_attention.hip", "prompt_attention.hip")}
 
 
 def flags_of(src: str) -> list:
@@ -62,7 +63,7 @@ def source_digest() -> str:
         h.update(name.encode())
         with open(os.path.join(CSRC, name), "rb") as f:
             h.update(f.read())
-    for name in ("svgemm.h", "svgemm_layer.h"):
+    for name in ("svgemm.h", "svgemm_layer.h", "svgemm_prompt.h"):
         with open(os.path.join(ROOT, "include", name), "rb") as f:
             h.update(f.read())
     for src in SOURCES:

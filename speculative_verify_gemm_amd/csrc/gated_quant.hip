@@ -1,0 +1,85 @@
+// The gated activation x * silu(gate), block Hadamard rotation and int8 quantization of activation rows in one
+// launch, gfx950.
+//
+// u = x * gate / (1 + exp(-gate)) decides codes, so it is defined as one rounding of a 64-bit value and computed in
+// fp64 here (its error there, below 2^-50, moves that rounding once in 2^25 values); the rotation and the codes are
+// those of svg_act.h.  One workgroup owns a row and holds it in registers.
+#include "../../include/svgemm_prompt.h"
+#include "svg_act.h"
+#include "svg_internal.h"
+
+#pragma clang fp contract(off)
+
+namespace {
+
+struct GateArgs {
+  const void *x, *gate;
+  const int8_t* signs;
+  int8_t* xq;
+  float* x_scale;
+  long ld_x, ld_gate;  // bytes
+  int M, K, type;
+};
+
+SVG_DEV float gated(float x, float g) {
+  const double d = (double)g;
+  return (float)((double)x * (d / (1.0 + exp(-d))));
+}
+
+// A launch has fewer than 2^32 work-items a dimension: rows go on in y.
+constexpr int kRowsX = 1 << 20;
+
+template <int NT, int CPT, int B>
+__global__ __launch_bounds__(NT) void k_gated_quant(GateArgs a) {
+  __shared__ float red[16];
+  const int m = (int)(blockIdx.y * kRowsX + blockIdx.x), K = a.K;
+  if (m >= a.M) return;
+  const u32 tid = threadIdx.x, size = a.type == SVG_F32 ? 4u : 2u;
+  const rsrc_t xr = make_rsrc(static_cast<const char*>(a.x) + m * a.ld_x, (u32)K * size);
+  const rsrc_t gr = make_rsrc(static_cast<const char*>(a.gate) + (a.gate ? m * a.ld_gate : 0), a.gate ? (u32)K * size : 0u);
+  const rsrc_t sr = make_rsrc(a.signs, (u32)K);
+  RowRegs<CPT> r;
+  float g[CPT][4];
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const u32 c = tid + NT * i;
+    load_chunk(xr, a.type, c, r.e[i]);
+    load_chunk(gr, a.type, c, g[i]);
+    r.sg[i] = (int)bload4(sr, c * 4u);
+  }
+  if (a.gate) {
+#pragma unroll
+    for (int i = 0; i < CPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.e[i][j] = gated(r.e[i][j], g[i][j]);
+  }
+  // the row's 32-row slab buffer
+  const int first = m & ~31, rows = a.M - first < 32 ? a.M - first : 32;
+  const StoreGlobal st(a.xq + (size_t)first * K, m - first, rows, a.x_scale + m, K);
+  act_quant_loaded<CPT, StoreGlobal, B, true>(r, K, st, red);
+}
+
+template <int B>
+void launch(const GateArgs& a, hipStream_t stream) {
+  const int nchunk = a.K / 4;
+  const dim3 grid(a.M < kRowsX ? a.M : kRowsX, (a.M + kRowsX - 1) / kRowsX);
+#define SVG_GATE(NT, CPT) hipLaunchKernelGGL((k_gated_quant<NT, CPT, B>), grid, dim3(NT), 0, stream, a)
+  if (nchunk <= 256) SVG_GATE(256, 1);
+  else if (nchunk <= 512) SVG_GATE(512, 1);
+  else if (nchunk <= 1024) SVG_GATE(1024, 1);
+  else if (nchunk <= 2048) SVG_GATE(1024, 2);
+  else if (nchunk <= 4096) SVG_GATE(1024, 4);
+  else SVG_GATE(1024, 8);
+#undef SVG_GATE
+}
+
+}  // namespace
+
+hipError_t svg_launch_gated_quant(const void* x, int64_t ld_x, const void* gate, int64_t ld_gate, int x_type, int M, int K,
+                                  const int8_t* signs, int block, int8_t* xq, float* x_scale, hipStream_t stream) {
+  const int size = x_type == SVG_F32 ? 4 : 2;
+  const GateArgs a{x, gate, signs, xq, x_scale, ld_x * size, ld_gate * size, M, K, x_type};
+  if (block == 64) launch<64>(a, stream);
+  else launch<32>(a, stream);
+  return hipGetLastError();
+}

@@ -13,20 +13,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Whether slot s's table row names a page of the cache for page number i.
-SVG_DEV bool page_of(const svg_kv_cache& c, int s, long i, int& page) {
-  const int held = c.pages[s];
-  if (i < 0 || i >= held || held > c.width) return false;
-  page = c.table[(size_t)s * c.width + i];
-  return (u32)page < (u32)c.n_pages;
-}
-
-// Whether that page may be written: no other slot holds it.  (A slot that kv_reserve refused still has the page that it
-// shares.)
-SVG_DEV bool own_page_of(const svg_kv_cache& c, int s, long i, int& page) {
-  return page_of(c, s, i, page) && (c.refs == nullptr || c.refs[page] <= 1);
-}
-
 // ------------------------------------------------------------------- append
 // One wave per (four consecutive positions, head, slot): four tokens share the
 // eight-byte halves of the values' 16-byte pieces, so they are written whole.

@@ -11,9 +11,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool type_ok(int t) { return t == SVG_F32 || t == SVG_F16 || t == SVG_BF16; }
 hipStream_t to_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
-enum { kTable = 1, kPages = 2, kLen = 4, kRefs = 8 };  // what a call needs of a cache
+}  // namespace
 
-svg_status check_cache(const char* fn, const svg_kv_cache* c, int needs) {
+int svg_check_cache(const char* fn, const svg_kv_cache* c, int needs) {
   if (!c) return svg_fail(SVG_EINVAL, fn, "null cache");
   if (!c->k || !c->v) return svg_fail(SVG_EINVAL, fn, "null cache pages");
   if (c->type != SVG_F16 && c->type != SVG_BF16) return svg_fail(SVG_EUNSUPPORTED, fn, "cache type must be fp16 or bf16");
@@ -42,8 +42,6 @@ svg_status check_cache(const char* fn, const svg_kv_cache* c, int needs) {
   return SVG_OK;
 }
 
-}  // namespace
-
 extern "C" {
 
 svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, const void* weight, int w_type,
@@ -71,7 +69,7 @@ svg_status add_rmsnorm_quant_i8(const void* x, int x_type, float* residual, cons
 svg_status kv_append(const svg_kv_cache* cache, int layer, const float* k, int64_t ld_k, const float* v, int64_t ld_v, int T,
                      const int32_t* n_rows, void* stream) {
   static const char* fn = "kv_append";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen)) return st;
   if (T < 1) return svg_fail(SVG_EINVAL, fn, "T < 1");
   if (layer < 0 || layer >= cache->n_layers) return svg_fail(SVG_EINVAL, fn, "layer outside the cache");
   const int64_t row = (int64_t)cache->heads * cache->dim;
@@ -88,7 +86,7 @@ svg_status kv_append(const svg_kv_cache* cache, int layer, const float* k, int64
 svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, const int32_t* n_emit, int32_t* len_out,
                      void* stream) {
   static const char* fn = "kv_commit";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen)) return st;
   if (T < 1) return svg_fail(SVG_EINVAL, fn, "T < 1");
   if (T > SVG_TREE_MAX_NODES) return svg_fail(SVG_EUNSUPPORTED, fn, "T > SVG_TREE_MAX_NODES");
   if (cache->n_slots == 0) return svg_ok();
@@ -101,7 +99,7 @@ svg_status kv_commit(const svg_kv_cache* cache, int T, const int32_t* path, cons
 svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table_out, int32_t* pages_out,
                    int32_t* len_out, void* stream) {
   static const char* fn = "kv_fork";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
   if (cache->n_slots == 0) return svg_ok();
   if (!src || !table_out || !pages_out || !len_out) return svg_fail(SVG_EINVAL, fn, "null required pointer");
   if (table_out == cache->table || pages_out == cache->pages || len_out == cache->len)
@@ -113,7 +111,7 @@ svg_status kv_fork(const svg_kv_cache* cache, const int32_t* src, int32_t* table
 
 svg_status kv_reserve(const svg_kv_cache* cache, const int32_t* need, int32_t* status, void* workspace, void* stream) {
   static const char* fn = "kv_reserve";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen | kRefs)) return st;
   if (cache->n_slots == 0) return svg_ok();
   if (!need || !status || !workspace) return svg_fail(SVG_EINVAL, fn, "null required pointer");
   if (!aligned(need, 4) || !aligned(status, 4)) return svg_fail(SVG_EALIGN, fn, "need and status need 4-byte alignment");
@@ -123,7 +121,7 @@ svg_status kv_reserve(const svg_kv_cache* cache, const int32_t* need, int32_t* s
 
 svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream) {
   static const char* fn = "kv_copy_pages";
-  if (const svg_status st = check_cache(fn, cache, 0)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, 0)) return st;
   if (n < 0) return svg_fail(SVG_EINVAL, fn, "n < 0");
   if (n == 0) return svg_ok();
   if (!src || !dst) return svg_fail(SVG_EINVAL, fn, "null required pointer");
@@ -143,7 +141,7 @@ static svg_status check_heads(const char* fn, const svg_kv_cache* c, int q_heads
 
 svg_status tree_attention_workspace(const svg_kv_cache* cache, int q_heads, int T, uint64_t* bytes) {
   static const char* fn = "tree_attention_workspace";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen)) return st;
   if (const svg_status st = check_heads(fn, cache, q_heads, T)) return st;
   if (!bytes) return svg_fail(SVG_EINVAL, fn, "null bytes");
   *bytes = cache->n_slots ? svg_tree_attention_bytes(*cache, T, q_heads / cache->heads) : 0;
@@ -154,7 +152,7 @@ svg_status tree_attention(const svg_kv_cache* cache, int layer, const float* q, 
                           int T, const int32_t* n_nodes, const int32_t* shared, float scale, float* out, void* workspace,
                           void* stream) {
   static const char* fn = "tree_attention";
-  if (const svg_status st = check_cache(fn, cache, kTable | kPages | kLen)) return st;
+  if (const svg_status st = svg_check_cache(fn, cache, kTable | kPages | kLen)) return st;
   if (const svg_status st = check_heads(fn, cache, q_heads, T)) return st;
   if (layer < 0 || layer >= cache->n_layers) return svg_fail(SVG_EINVAL, fn, "layer outside the cache");
   if (!std::isfinite(scale)) return svg_fail(SVG_EINVAL, fn, "scale must be finite");

@@ -13,7 +13,6 @@
 // written once.  Few rows are bound by the chain of one load, two reductions
 // and one store (one row of 4096 3.8 us, 16 rows with y 4.8 us, of which the launch is 2 to 3);
 // many rows by memory (4099 rows of 4096, fp16 in: 39 to 44 us, 4.7 TB/s).
-#include "../../include/svgemm_layer.h"
 #include "svg_act.h"
 #include "svg_device.h"
 #include "svg_internal.h"
@@ -33,26 +32,6 @@ struct NormArgs {
   double eps;
   int M, K, x_type, w_type;
 };
-
-// Four consecutive values of an array of `type` (chunk c), as fp32; zeros past
-// the array.  The type is the same for the whole launch.
-SVG_DEV void load_chunk(rsrc_t r, int type, u32 c, float v[4]) {
-  if (type == SVG_F32) {
-    const u32x4 t = bload16(r, c * 16u);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(t[i]);
-    return;
-  }
-  Bytes<8> t;
-  bload_bytes<8>(t, r, c * 8u);
-  if (type == SVG_F16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = half_at(t.w, i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((i & 1) ? (t.w[i >> 1] & 0xFFFF0000u) : (t.w[i >> 1] << 16));
-  }
-}
 
 template <int CTRL>
 SVG_DEV double dpp_f64(double v) {

@@ -1,0 +1,536 @@
+// Causal attention of prompt rows over a paged cache, gfx950.
+//
+// Row i of slot s attends to the positions 0 .. len[s] + i:
+//   o = sum_t p_t v_t / sum_t p_t,   p_t = 2^(f (q . k_t) - m),  f = scale log2(e),
+// in one pass over the tokens with a running maximum m per row.
+//
+// Work.  The rows of a slot and a key/value head (tokens x query heads of the group) are cut into tiles of kTile; a tile and
+// the tokens that it sees form an item.  Items are counted by the tokens that they see and all of them, in order, are
+// dealt out evenly over the workgroups, so that one long row fills the device as well as many prompts do.  A workgroup that does
+// not have all of an item writes a partial (O, m, sum); a second launch joins those.  Lengths are read on the device.
+//
+// Layout.  A page is laid out in the lane order of v_mfma_f32_16x16x32: S^T = K Q^T leaves a row's scores in one
+// lane column, four consecutive tokens in each lane, which is the order the values are stored in, so the probabilities
+// go from the first product's result registers into the second's operand registers: O^T += V^T P^T.
+// The sum of the probabilities is a product as well, with ones: it adds up what the second product sees.
+#include <math.h>
+
+#include "../../include/svgemm_prompt.h"
+#include "svg_cache.h"
+#include "svg_internal.h"
+#include "svg_lds.h"
+
+namespace {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 128;                   // rows of an item
+constexpr int kMaxSlots = 1024;
+constexpr int kItem = 4;                     // token tiles that starting and ending an item counts as
+constexpr int kLeast = 4;                    // token tiles of a workgroup at least
+
+template <bool BF>
+SVG_DEV f32x4 mfma(u32x4 x, u32x4 y, f32x4 c) {
+  if constexpr (BF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+}
+// Two values rounded to nearest, packed.
+template <bool BF>
+SVG_DEV u32 pack2(float x, float y) {
+  if constexpr (BF) return __builtin_bit_cast(u32, __builtin_convertvector(f32x2{x, y}, bf16x2));
+  else return __builtin_bit_cast(u32, __builtin_convertvector(f32x2{x, y}, f16x2));
+}
+template <bool BF>
+constexpr u32 kOnes = BF ? 0x3F803F80u : 0x3C003C00u;
+// Bits 15 and 31: the halves that are not finite (their exponent, all ones, plus one).
+template <bool BF>
+SVG_DEV u32 odd_halves(u32 w) {
+  return BF ? ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u : ((w & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+}
+
+// A probability is at most 2^kTop: the running maximum is raised when a score passes it by kSlack, and everything is lifted by
+// kTop - kSlack, so that small ones stay above the smallest number of fp16.
+constexpr float kTop = 15.f, kSlack = 7.f, kLift = kTop - kSlack;
+
+struct Args {
+  svg_kv_cache c;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t *start, *count;
+  float* stats;   // [groups][2][kTile] (bias, sum); the bias is infinite where no token was seen
+  float* parts;   // [groups][2][kTile][dim]
+  long ld_q;
+  int layer, G, n_rows, groups;
+  float scale;
+};
+
+// ---------------------------------------------------------------------- plan
+// Cost of the items of a slot, in 1 / G of a token tile of 32: item j of a head counts G * (tiles of the committed tokens +
+// kItem) + per * (j + 1), where per = kTile / 32 covers the rows' own tokens; the cost of the first j is a polynomial.  It
+// decides only how the work is shared out.
+struct Slot {
+  int first, n, len;    // its rows in q and out, committed tokens
+  bool valid;
+  u32 items;            // of a head
+  unsigned long long base;
+  SVG_DEV unsigned long long before(unsigned long long j) const { return base * j + (kTile / 64) * j * (j + 1); }
+  SVG_DEV unsigned long long cost(u32 j) const { return base + (kTile / 32) * (unsigned long long)(j + 1); }
+};
+SVG_DEV Slot slot_of(const Args& a, int s) {
+  Slot x;
+  const int first = a.start[s], held = a.c.pages[s];
+  int n = a.count[s];
+  x.len = a.c.len[s];
+  if (first < 0 || first >= a.n_rows || n < 0) n = 0;
+  else if (n > a.n_rows - first) n = a.n_rows - first;
+  x.first = first;
+  x.n = n;
+  x.valid = x.len >= 0 && held >= 0 && held <= a.c.width && (long)x.len + n <= (long)held * a.c.page;
+  x.items = (u32)(((long)n * a.G + kTile - 1) / kTile);
+  x.base = (unsigned long long)a.G * ((x.valid ? (u32)x.len >> 5 : 0u) + kItem);
+  return x;
+}
+
+struct Plan {
+  unsigned long long cum[kMaxSlots + 1];  // cost of the slots before s
+  unsigned long long red[8];
+};
+
+SVG_DEV unsigned long long shfl_up64(unsigned long long v, int off) {
+  const u32 lo = (u32)__shfl_up((int)(u32)v, off), hi = (u32)__shfl_up((int)(u32)(v >> 32), off);
+  return (unsigned long long)hi << 32 | lo;
+}
+
+template <int WAVES>
+SVG_DEV void make_plan(const Args& a, Plan& p) {
+  const int S = a.c.n_slots, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int EACH = kMaxSlots / (64 * WAVES);
+  unsigned long long c[EACH], sum = 0;
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int s = tid * EACH + i;
+    c[i] = 0;
+    if (s < S) {
+      const Slot x = slot_of(a, s);
+      c[i] = x.before(x.items) * (unsigned long long)a.c.heads;
+    }
+    sum += c[i];
+  }
+  unsigned long long upto = sum;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const unsigned long long y = shfl_up64(upto, off);
+    if (lane >= off) upto += y;
+  }
+  if (lane == 63) p.red[wave] = upto;
+  __syncthreads();
+  unsigned long long at = upto - sum;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w)
+    if (w < wave) at += p.red[w];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int s = tid * EACH + i;
+    if (s < S) p.cum[s] = at;
+    at += c[i];
+  }
+  if (tid == 64 * WAVES - 1) p.cum[S] = at;
+  __syncthreads();
+}
+
+struct Deal {
+  unsigned long long total;
+  unsigned long long quot, rest;
+  u32 groups;  // workgroups that take part: w has the costs from start(w) on
+  SVG_DEV unsigned long long start(u32 w) const { return w * quot + (w < rest ? w : rest); }
+};
+SVG_DEV Deal deal_of(const Args& a, const Plan& p) {
+  Deal d;
+  d.total = p.cum[a.c.n_slots];
+  const unsigned long long want = d.total / ((unsigned long long)a.G * (kItem + kLeast)) + 1;
+  d.groups = (u32)(want < (unsigned long long)a.groups ? want : (unsigned long long)a.groups);
+  d.quot = d.total / d.groups;
+  d.rest = d.total - d.quot * d.groups;
+  return d;
+}
+
+// The item at cost `at`.
+struct Item {
+  int s;
+  u32 h, j;
+  unsigned long long from, cost;  // of the whole launch; its own
+};
+SVG_DEV Item item_at(const Args& a, const Plan& p, unsigned long long at, Slot& x) {
+  int s = 0;
+  for (int step = kMaxSlots / 2; step > 0; step >>= 1)
+    if (s + step <= a.c.n_slots - 1 && p.cum[s + step] <= at) s += step;  // the last slot that begins at or before
+  x = slot_of(a, s);
+  const unsigned long long head = x.before(x.items), in = at - p.cum[s];
+  Item it;
+  it.s = s;
+  it.h = (u32)(in / head);
+  const unsigned long long rest = in - it.h * head;
+  u32 lo = 0, hi = x.items;  // the last j with before(j) <= rest
+  while (hi - lo > 1) {
+    const u32 mid = (lo + hi) >> 1;
+    if (x.before(mid) <= rest) lo = mid;
+    else hi = mid;
+  }
+  it.j = lo;
+  it.from = p.cum[s] + it.h * head + x.before(lo);
+  it.cost = x.cost(lo);
+  return it;
+}
+SVG_DEV int uniform_i(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Tokens of an item: what its last row sees; tiles of 32.
+SVG_DEV int tokens_of(const Args& a, const Slot& x, u32 j) {
+  const int rows = x.n * a.G, end = (int)(j + 1) * kTile < rows ? (int)(j + 1) * kTile : rows;
+  return x.len + (end - 1) / a.G + 1;
+}
+// The token tile where a share that begins at cost c of the item begins.
+SVG_DEV int tile_at(unsigned long long c, const Item& it, int tiles) { return (int)(c * (u32)tiles / it.cost); }
+
+// ---------------------------------------------------------------------- kernel
+template <int D, bool BF, int STAGES, int RT>
+struct Kernel {
+  static constexpr int WAVES = kTile / 16 / RT;         // RT row tiles of 16 each
+  static constexpr int NC = D / 32, ND = D / 16;     // fragments of a token tile's half, of its values
+  static constexpr int HALF = D * 64;                // bytes of a tile's keys, of its values
+  static constexpr int STAGE = 2 * HALF, LOADS = STAGE / 1024 / WAVES;
+
+  struct Row {
+    f32x4 o[ND];
+    f32x4 l;
+    float m, bias;   // the maximum that the row's exponents go by (-infinity: no token yet), and what is added to them
+  };
+
+  // Value that is not finite in a tile that not all rows see whole: taken out of the product, and put into the sums of the
+  // rows that see it as NaN.
+  SVG_DEV static void odd_values(const char* v, int lane, const u32x4 (&p)[RT], const u32x4 (&sees)[RT], Row (&row)[RT]) {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      u32x4 x = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16), is;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const u32 mask = (odd_halves<BF>(x[w]) >> 15) * 0xFFFFu;  // (bits 0 and 16 times all ones: no carry)
+        is[w] = mask & kOnes<BF>;
+        x[w] &= ~mask;
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const f32x4 hits = mfma<BF>(is, sees[rt], f32x4{});
+        row[rt].o[d] = mfma<BF>(x, p[rt], row[rt].o[d]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) row[rt].o[d][e] = hits[e] > 0.f ? __builtin_nanf("") : row[rt].o[d][e];
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one at a time: this path must not set the kernel's registers
+    }
+  }
+
+  SVG_DEV static void run(const Args& a, char* lds, Plan& plan) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), col = lane & 15, quad = lane >> 4;
+    make_plan<WAVES>(a, plan);
+    const Deal deal = deal_of(a, plan);
+    // XCDs take stretches of neighbouring workgroups, which read the same keys
+    const u32 per = (u32)a.groups >> 3;
+    const u32 wg = (blockIdx.x & 7u) * per + (blockIdx.x >> 3);
+    if (wg >= deal.groups) return;
+    unsigned long long at = deal.start(wg);
+    const unsigned long long end = deal.start(wg + 1);
+    const u32 base = lds_at(lds);
+    const float f = a.scale * 1.4426950408889634f;
+    const int shift = __builtin_ctz(a.c.page);
+    const size_t page_bytes = (size_t)a.c.heads * a.c.page * D * 2;
+    const int G = a.G;
+    while (at < end) {
+      Slot x;
+      const Item it = item_at(a, plan, at, x);
+      const unsigned long long stop = it.from + it.cost < end ? it.from + it.cost : end;
+      const bool whole = at == it.from && stop == it.from + it.cost;
+      const int which = at == it.from ? 1 : 0;  // the partial's place: an item's first share, or a later one
+      const int row0 = (int)it.j * kTile, rows = x.n * G - row0 < kTile ? x.n * G - row0 : kTile;
+      const int tokens = x.valid ? tokens_of(a, x, it.j) : 0, tiles = (tokens + 31) >> 5;
+      const int t0 = uniform_i(at == it.from ? 0 : tile_at(at - it.from, it, tiles));
+      const int t1 = uniform_i(stop == it.from + it.cost ? tiles : tile_at(stop - it.from, it, tiles));
+      at = stop;
+      // this lane's rows (those past the item's: its last one, not stored), and the last position that each sees
+      const int mine = wave * 16 * RT;
+      const bool live = mine < rows;
+      int seen[RT];
+      size_t q_at[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        int r = mine + 16 * rt + col;
+        r = row0 + (r < rows ? r : rows - 1);
+        const int tok = r / G, head = (int)it.h * G + (r - tok * G);
+        seen[rt] = x.len + tok;
+        q_at[rt] = (size_t)(x.first + tok) * (size_t)a.ld_q + (size_t)head * D;
+      }
+      const int low = x.len + (row0 + (mine < rows ? mine : rows - 1)) / G;                                      // of the wave's rows
+      const int high = x.len + (row0 + (mine + 16 * RT < rows ? mine + 16 * RT : rows) - 1) / G;
+      u32x4 q[RT][NC];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) q[rt][c] = *reinterpret_cast<const u32x4*>(a.q + q_at[rt] + 32 * c + 8 * quad);
+      Row row[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) row[rt].o[d] = f32x4{};
+        row[rt].l = f32x4{};
+        row[rt].m = -INFINITY;
+        row[rt].bias = 0.f;
+      }
+      // pages: position p lies in entry p >> shift of the slot's table row
+      const int32_t* table = a.c.table + (size_t)it.s * a.c.width;
+      const char* kl = static_cast<const char*>(a.c.k) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)it.h * a.c.page * D * 2;
+      const char* vl = static_cast<const char*>(a.c.v) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)it.h * a.c.page * D * 2;
+      // Requests a tile; the first of its positions that makes the rows which see it NaN (no page of the cache: all; the
+      // step's own positions in a page that other slots hold: those).
+      auto fetch = [&](int t, int slot) {
+        const int p = t * 32, entry = p >> shift;
+        int page = uniform_i(table[entry]);
+        int from = 0x7FFFFFFF;
+        if ((u32)page >= (u32)a.c.n_pages) {
+          page = 0;
+          from = 0;
+        } else if (a.c.refs != nullptr && p + 31 >= x.len && a.c.refs[page] > 1) {
+          from = x.len;
+        }
+        const size_t off = (size_t)page * page_bytes + (size_t)(p & (a.c.page - 1)) * D * 2;
+        const u32 to = base + (u32)slot * STAGE;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const int piece = wave + i * WAVES;
+          const bool key = piece * 1024 < HALF;
+          load_to_lds((key ? kl : vl) + off + (key ? piece * 1024 : piece * 1024 - HALF), lane * 16u, to + piece * 1024u);
+        }
+        return uniform_i(from);
+      };
+      wait_loads<0>();
+      barrier();  // (the places of the item before are free)
+      int odd_from[STAGES];
+#pragma unroll
+      for (int i = 0; i < STAGES - 1; ++i) odd_from[i] = t0 + i < t1 ? fetch(t0 + i, i) : 0;
+      int slot = 0;
+      for (int t = t0; t < t1; ++t) {
+        if (t + STAGES - 2 < t1) wait_loads<LOADS * (STAGES - 2)>();
+        else wait_loads<0>();
+        barrier();
+        const int nan_from = odd_from[0];
+#pragma unroll
+        for (int i = 0; i + 1 < STAGES - 1; ++i) odd_from[i] = odd_from[i + 1];
+        if (t + STAGES - 1 < t1) odd_from[STAGES - 2] = fetch(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+        const char* k = lds + slot * STAGE;
+        const char* v = k + HALF;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        const int p0 = t * 32;
+        if (!live || p0 > high) continue;
+        f32x4 s[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const u32x4 k0 = *reinterpret_cast<const u32x4*>(k + c * 1024 + lane * 16);
+          const u32x4 k1 = *reinterpret_cast<const u32x4*>(k + (NC + c) * 1024 + lane * 16);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            s[rt][0] = mfma<BF>(k0, q[rt][c], s[rt][0]);
+            s[rt][1] = mfma<BF>(k1, q[rt][c], s[rt][1]);
+          }
+        }
+        float ff = f;
+        if (p0 + 31 > low || nan_from != 0x7FFFFFFF || !(f > 0.f)) {
+          ff = 1.f;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = p0 + 16 * i + 4 * quad + e;
+                s[rt][i][e] *= f;
+                if (tok >= nan_from) s[rt][i][e] = __builtin_nanf("");
+                if (tok > seen[rt]) s[rt][i][e] = -INFINITY;
+              }
+        }
+        u32x4 p[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          Row& r = row[rt];
+          float top = s[rt][0][0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) top = fmaxf(top, s[rt][e >> 2][e & 3]);
+          top *= ff;
+          if (__any(top > r.m + kSlack)) {
+            // raised for the whole row: its four lanes agree
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (top > r.m + kSlack) {
+              const float bias = kLift - top, by = r.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(bias - r.bias);
+              r.m = top;
+              r.bias = bias;
+#pragma unroll
+              for (int d = 0; d < ND; ++d) r.o[d] *= by;
+              r.l *= by;
+            }
+          }
+          float w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float y = s[rt][e >> 2][e & 3];
+            w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(y, ff, r.bias));
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[rt][e] = pack2<BF>(w[2 * e], w[2 * e + 1]);
+        }
+        const u32x4 ones{kOnes<BF>, kOnes<BF>, kOnes<BF>, kOnes<BF>};
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
+        if (p0 + 31 > low) {
+          u32 odd = 0;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
+            odd |= odd_halves<BF>(y[0]) | odd_halves<BF>(y[1]) | odd_halves<BF>(y[2]) | odd_halves<BF>(y[3]);
+          }
+          if (__any(odd != 0)) {
+            u32x4 sees[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = p0 + 16 * (e >> 1) + 4 * quad + 2 * (e & 1);
+                sees[rt][e] = (tok <= seen[rt] ? kOnes<BF> & 0xFFFFu : 0u) | (tok + 1 <= seen[rt] ? kOnes<BF> & 0xFFFF0000u : 0u);
+              }
+            odd_values(v, lane, p, sees, row);
+            continue;
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) row[rt].o[d] = mfma<BF>(y, p[rt], row[rt].o[d]);
+        }
+      }
+      if (!live) continue;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int r = mine + 16 * rt + col;
+        if (r >= rows) continue;
+        Row& w = row[rt];
+        if (whole) {
+          const float inv = x.valid ? 1.f / w.l[0] : __builtin_nanf("");
+          const int tok = (row0 + r) / G, head = (int)it.h * G + (row0 + r - tok * G);
+          uint16_t* to = a.out + ((size_t)(x.first + tok) * a.c.heads * G + head) * D + 4 * quad;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+            *reinterpret_cast<uint2*>(to + 16 * d) = make_uint2(pack2<BF>(w.o[d][0] * inv, w.o[d][1] * inv),
+                                                                pack2<BF>(w.o[d][2] * inv, w.o[d][3] * inv));
+        } else {
+          const size_t at_part = ((size_t)wg * 2 + which) * kTile + r;
+          float* to = a.parts + at_part * D + 4 * quad;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+            *reinterpret_cast<float4*>(to + 16 * d) = make_float4(w.o[d][0], w.o[d][1], w.o[d][2], w.o[d][3]);
+          if (quad == 0) {
+            a.stats[at_part * 2] = w.m == -INFINITY ? INFINITY : w.bias;
+            a.stats[at_part * 2 + 1] = x.valid ? w.l[0] : __builtin_nanf("");
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int D, bool BF, int STAGES, int RT>
+__global__ __launch_bounds__(kTile / 16 / RT * 64, 2) void k_prompt_attention(Args a) {
+  __shared__ __attribute__((aligned(1024))) char lds[STAGES * Kernel<D, BF, STAGES, RT>::STAGE];
+  __shared__ Plan plan;
+  Kernel<D, BF, STAGES, RT>::run(a, lds, plan);
+}
+
+// Joins the partials of the item that begins in workgroup blockIdx.x's share and goes on behind it: its first share's partial
+// lies at place 1 of that workgroup, the others' at place 0 of the next ones.
+constexpr int kJoinRows = 16, kJoinWaves = 4;
+template <int D, bool BF>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args a) {
+  __shared__ Plan plan;
+  make_plan<kJoinWaves>(a, plan);
+  const Deal deal = deal_of(a, plan);
+  const u32 wg = blockIdx.x;
+  if (wg >= deal.groups) return;
+  const unsigned long long begin = deal.start(wg), end = deal.start(wg + 1);
+  if (end <= begin || end >= deal.total) return;
+  Slot x;
+  const Item it = item_at(a, plan, end, x);   // the item that the next workgroup begins with
+  if (it.from >= end || it.from < begin) return;
+  u32 last = wg;                              // the last workgroup that has some of it
+  while (deal.start(last + 1) < it.from + it.cost) ++last;
+  const int row0 = (int)it.j * kTile, rows = x.n * a.G - row0 < kTile ? x.n * a.G - row0 : kTile;
+  for (int u = threadIdx.x; u < kJoinRows * (D / 4); u += 64 * kJoinWaves) {
+    const int r = blockIdx.y * kJoinRows + u / (D / 4), d = 4 * (u % (D / 4));
+    if (r >= rows) continue;
+    float low = INFINITY;
+    for (u32 w = wg; w <= last; ++w) low = fminf(low, a.stats[(((size_t)w * 2 + (w == wg)) * kTile + r) * 2]);
+    float sum = 0.f;
+    f32x4 o{};
+    for (u32 w = wg; w <= last; ++w) {
+      const size_t at = ((size_t)w * 2 + (w == wg)) * kTile + r;
+      const float bias = a.stats[at * 2], by = bias == INFINITY ? 0.f : __builtin_amdgcn_exp2f(low - bias);
+      const float4 y = *reinterpret_cast<const float4*>(a.parts + at * D + d);
+      sum = __builtin_fmaf(a.stats[at * 2 + 1], by, sum);
+      o[0] = __builtin_fmaf(y.x, by, o[0]);
+      o[1] = __builtin_fmaf(y.y, by, o[1]);
+      o[2] = __builtin_fmaf(y.z, by, o[2]);
+      o[3] = __builtin_fmaf(y.w, by, o[3]);
+    }
+    const float inv = 1.f / sum;
+    const int tok = (row0 + r) / a.G, head = (int)it.h * a.G + (row0 + r - tok * a.G);
+    *reinterpret_cast<uint2*>(a.out + ((size_t)(x.first + tok) * a.c.heads * a.G + head) * D + d) =
+        make_uint2(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv));
+  }
+}
+
+template <int D, bool BF, int STAGES, int RT>
+void launch(const Args& a, hipStream_t stream) {
+  hipLaunchKernelGGL((k_prompt_attention<D, BF, STAGES, RT>), dim3(a.groups), dim3(kTile / 16 / RT * 64), 0, stream, a);
+  hipLaunchKernelGGL((k_prompt_attention_join<D, BF>), dim3(a.groups, kTile / kJoinRows), dim3(64 * kJoinWaves), 0, stream, a);
+}
+
+constexpr int kMaxGroups = 512;
+// Two workgroups a compute unit, the same number on each XCD.
+int groups_of() {
+  const int n = svg_cu_count() * 2 / 8 * 8;
+  return n < 8 ? 8 : (n < kMaxGroups ? n : kMaxGroups);
+}
+size_t stats_bytes(int groups) { return ((size_t)groups * 2 * kTile * 8 + 255) / 256 * 256; }
+
+}  // namespace
+
+uint64_t svg_prompt_attention_bytes(const svg_kv_cache& c) {
+  return stats_bytes(kMaxGroups) + (size_t)kMaxGroups * 2 * kTile * c.dim * 4;
+}
+
+hipError_t svg_launch_prompt_attention(const svg_kv_cache& c, int layer, const void* q, int64_t ld_q, int G, int n_rows,
+                                       const int32_t* start, const int32_t* count, float scale, void* out, void* workspace,
+                                       hipStream_t stream) {
+  const int groups = groups_of();
+  const Args a{c, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), start, count, static_cast<float*>(workspace),
+               reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(groups)), ld_q, layer, G, n_rows, groups, scale};
+  const bool bf = c.type == SVG_BF16;
+  if (c.dim == 64) bf ? launch<64, true, 4, 2>(a, stream) : launch<64, false, 4, 2>(a, stream);
+  else if (c.dim == 128) bf ? launch<128, true, 3, 2>(a, stream) : launch<128, false, 3, 2>(a, stream);
+  else bf ? launch<256, true, 2, 1>(a, stream) : launch<256, false, 2, 1>(a, stream);
+  return hipGetLastError();
+}

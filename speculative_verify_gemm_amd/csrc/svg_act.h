@@ -24,11 +24,32 @@
 // same integer as t, so rint(t) is the code; near a half-integer (about one
 // value in 4000) the exact division decides.
 #pragma once
+#include "../../include/svgemm_layer.h"
 #include "svg_device.h"
 
 #pragma clang fp contract(off)
 
 SVG_DEV int clamp_i(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// Four consecutive values of an array of `type` (chunk c), as fp32; zeros past
+// the array.  The type is the same for the whole launch.
+SVG_DEV void load_chunk(rsrc_t r, int type, u32 c, float v[4]) {
+  if (type == SVG_F32) {
+    const u32x4 t = bload16(r, c * 16u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(t[i]);
+    return;
+  }
+  Bytes<8> t;
+  bload_bytes<8>(t, r, c * 8u);
+  if (type == SVG_F16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = half_at(t.w, i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float((i & 1) ? (t.w[i >> 1] & 0xFFFF0000u) : (t.w[i >> 1] << 16));
+  }
+}
 
 // int8 codes of four values u for the scale sigma (> 0); rinv = 1 / sigma;
 // `fast` is false when 1 / sigma is not a normal float (then every code

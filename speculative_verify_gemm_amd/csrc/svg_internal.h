@@ -66,8 +66,12 @@ hipError_t svg_launch_norm_quant(const void* x, int x_type, float* residual, con
                                  double eps, int M, int K, const int8_t* signs, int block, float* y, int8_t* xq,
                                  float* x_scale, hipStream_t stream);
 
-// The paged cache (kv_pages.hip); every argument checked by the caller.
+// What a call needs of a cache, and its check (layer.hip): SVG_OK, or the status of the error that it has set.
 struct svg_kv_cache;
+enum { kTable = 1, kPages = 2, kLen = 4, kRefs = 8 };
+int svg_check_cache(const char* fn, const svg_kv_cache* c, int needs);
+
+// The paged cache (kv_pages.hip); every argument checked by the caller.
 hipError_t svg_launch_kv_append(const svg_kv_cache& c, int layer, const float* k, int64_t ld_k, const float* v,
                                 int64_t ld_v, int T, const int32_t* n_rows, hipStream_t stream);
 hipError_t svg_launch_kv_commit(const svg_kv_cache& c, int T, const int32_t* path, const int32_t* n_emit,
@@ -87,6 +91,24 @@ uint64_t svg_tree_attention_bytes(const svg_kv_cache& c, int T, int G);
 hipError_t svg_launch_tree_attention(const svg_kv_cache& c, int layer, const float* q, int64_t ld_q, int G,
                                      const int32_t* parent, int T, const int32_t* n_nodes, const int32_t* shared,
                                      float scale, float* out, void* workspace, hipStream_t stream);
+
+// A prompt's pass (prompt_rows.hip, prompt_attention.hip, prompt_linear.hip, gated_quant.hip).
+struct svg_rope;
+hipError_t svg_launch_kv_row_map(const svg_kv_cache& c, const int32_t* n_new, const int32_t* parent, int T, int n_rows,
+                                 int32_t* start, int32_t* count, int32_t* slot, int32_t* pos, int32_t* place, hipStream_t stream);
+hipError_t svg_launch_rope_append(const svg_kv_cache& c, int layer, const svg_rope& rope, const void* q, int64_t ld_q, int q_heads,
+                                  const void* k, int64_t ld_k, const void* v, int64_t ld_v, int x_type, int n_rows,
+                                  const int32_t* pos, const int32_t* place, void* q_out, int q_type, hipStream_t stream);
+uint64_t svg_prompt_attention_bytes(const svg_kv_cache& c);
+hipError_t svg_launch_prompt_attention(const svg_kv_cache& c, int layer, const void* q, int64_t ld_q, int G, int n_rows,
+                                       const int32_t* start, const int32_t* count, float scale, void* out, void* workspace,
+                                       hipStream_t stream);
+hipError_t svg_launch_prompt_w8(const int8_t* xq, const float* x_scale, int M, int K, const int8_t* wq, const uint16_t* w_scale, int N,
+                                void* y, int y_type, hipStream_t stream);
+hipError_t svg_launch_prompt_w4(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
+                                const void* w_zero, bool z4, int group, int N, void* y, int y_type, hipStream_t stream);
+hipError_t svg_launch_gated_quant(const void* x, int64_t ld_x, const void* gate, int64_t ld_gate, int x_type, int M, int K,
+                                  const int8_t* signs, int block, int8_t* xq, float* x_scale, hipStream_t stream);
 
 // Layout conversions (layout.hip): canonical row-major arrays <-> storage.
 hipError_t svg_launch_import_weights(int fmt_w8, int z4, int group, int N, int K, const void* codes,
