@@ -37,9 +37,9 @@ CFLAGS = [
 ]
 
 
-# Sources compiled without one of the flags: the attentions' accumulators take
-# turns with their operands, and the compiler is left to place them.
-LESS_FLAGS = {name: ("-mllvm", "-amdgpu-mfma-vgpr-form") for name in ("tree_attention.hip", "prompt_attention.hip")}
+# Sources compiled without one of the flags: the attention's accumulators take
+# turns with its operands, and the compiler is left to place them.
+LESS_FLAGS = {"tree_attention.hip": ("-mllvm", "-amdgpu-mfma-vgpr-form")}
 
 
 def flags_of(src: str) -> list:
