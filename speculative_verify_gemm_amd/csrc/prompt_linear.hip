@@ -1,4 +1,6 @@
 // y = x . W^T of many int8 activation rows against the tiled int8 or 4-bit weights, gfx950.
+#include <type_traits>
+
 #include "../../include/svgemm_prompt.h"
 #include "svg_cache.h"
 #include "svg_internal.h"
@@ -17,20 +19,73 @@ struct Args {
   void* y;
   int M, N, K, y_type;
   int tiles_m, tiles_n;
+  int whole;  // four values of a row of y can be stored together
 };
 
+SVG_DEV u32 round_to(int type, float v) { return type == SVG_F16 ? kv_round<false>(v) : kv_round<true>(v); }
+SVG_DEV u32 round2(int type, float x, float y) { return round_to(type, x) | (round_to(type, y) << 16); }
+SVG_DEV void put(const Args& a, size_t at, float v) {
+  if (a.y_type == SVG_F32) static_cast<float*>(a.y)[at] = v;
+  else static_cast<uint16_t*>(a.y)[at] = (uint16_t)round_to(a.y_type, v);
+}
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+SVG_DEV v4i mfma(u32x4 a, u32x4 b, v4i c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
+}
 
 // Weight formats: kStep values of K a step; kX fragments of 16 x 64 activation codes in one.
 struct W8 {
   static constexpr int kStep = 64, kX = 1, kParams = 0;
   static constexpr bool k4 = false;
   typedef v4i Acc;
+  template <int TN>
+  struct Operands {
+    u32x4 w[TN];
+    SVG_DEV void take(const u32x4 (&raw)[TN], const u32 (&)[TN][1], int, int) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) w[j] = raw[j];
+    }
+    SVG_DEV void multiply(const u32x4 (&x)[1], int j, v4i& acc) const { acc = mfma(w[j], x[0], acc); }
+  };
+  // lane: row 16 (tm + i) + lane % 16 of the tile, columns 16 (tn + j) + 4 (lane / 16) + 0 .. 3
+  template <int TM, int TN>
+  SVG_DEV static void store(const Args& a, const Acc (&acc)[TM][TN], const char* scales, int columns, int m0, int n0, int tm, int tn,
+                            int lane, bool full) {
+    float sx[TM];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) sx[i] = *reinterpret_cast<const float*>(scales + ((tm + i) * 16 + (lane & 15)) * 4);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const u32x4 h = *reinterpret_cast<const u32x4*>(scales + columns + ((tn + j) * 16 + 4 * (lane >> 4)) * 4);
+      const int n = n0 + (tn + j) * 16 + 4 * (lane >> 4);
+      float sw[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sw[e] = half_bits_to_float((uint16_t)h[e]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int m = m0 + (tm + i) * 16 + (lane & 15);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * (sx[i] * sw[e]);
+        const size_t at = (size_t)m * a.N + n;
+        if (full) {
+          if (a.y_type == SVG_F32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+                make_uint2(round2(a.y_type, v[0], v[1]), round2(a.y_type, v[2], v[3]));
+          }
+        } else if (m < a.M) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) put(a, at + e, v[e]);
+        }
+      }
+    }
+  }
 };
-SVG_DEV v4i mfma(u32x4 a, u32x4 b, v4i c) {
-  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
-}
-
 // Codes 0 .. 15 of the low nibbles less their zero points (the same in every byte of z), as int8: no byte borrows.
 SVG_DEV u32 less(u32 codes, u32 z) { return (((codes & 0x0F0F0F0Fu) | 0x80808080u) - z) ^ 0x80808080u; }
 
@@ -57,29 +112,63 @@ struct W4 {
       return (u32)(int)half_bits_to_float((uint16_t)(hi ? w >> 16 : w & 0xFFFFu)) & 15u;
     }
   }
-  template <int TM, int TN>
-  SVG_DEV static void product(const u32x4 (&x)[TM][2], const u32x4 (&w)[2], const u32* word, int s, int lane, Acc (&acc)[TM][TN], int j) {
-    const v4i none{};
-    if constexpr (G == 128) {
-      const float sc = half_bits_to_float((uint16_t)(s & 1 ? word[0] >> 16 : word[0] & 0xFFFFu));
+  // A step's weights: codes less zero points, and the scales of its groups.
+  template <int TN>
+  struct Operands {
+    static constexpr int GROUPS = 128 / G;
+    u32x4 w[TN][2];
+    float scale[TN][GROUPS];
+    bool high;
+    SVG_DEV void take(const u32x4 (&raw)[TN], const u32 (&word)[TN][kParams + 1], int s, int lane) {
+      high = lane >= 32;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) add(acc[i][j], mfma(x[i][1], w[1], mfma(x[i][0], w[0], none)), sc);
-    } else if constexpr (G == 64) {
+      for (int j = 0; j < TN; ++j) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float sc = half_at(word, h);
+        for (int h = 0; h < 2; ++h) {
+          const u32 z = zero(word[j] + kS, s, h, lane) * 0x01010101u;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) add(acc[i][j], mfma(x[i][h], w[h], none), sc);
+          for (int q = 0; q < 2; ++q) {
+            w[j][h][2 * q] = less(raw[j][2 * h + q], z);
+            w[j][h][2 * q + 1] = less(raw[j][2 * h + q] >> 4, z);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q)
+          scale[j][q] = G == 128 ? half_bits_to_float((uint16_t)(s & 1 ? word[j][0] >> 16 : word[j][0] & 0xFFFFu)) : half_at(word[j], q);
       }
-    } else {
-      // groups of 32: half the lanes' weights at a time
+    }
+    SVG_DEV void multiply(const u32x4 (&x)[2], int j, f32x4& acc) const {
+      const v4i none{};
+      if constexpr (G == 128) {
+        add(acc, mfma(x[1], w[j][1], mfma(x[0], w[j][0], none)), scale[j][0]);
+      } else if constexpr (G == 64) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float sc = half_at(word, q);
-        u32x4 part = w[q >> 1];
-        if ((lane >> 5) != (q & 1)) part = u32x4{};
+        for (int h = 0; h < 2; ++h) add(acc, mfma(x[h], w[j][h], none), scale[j][h]);
+      } else {
+        // groups of 32: half the lanes' weights at a time
 #pragma unroll
-        for (int i = 0; i < TM; ++i) add(acc[i][j], mfma(x[i][q >> 1], part, none), sc);
+        for (int q = 0; q < 4; ++q) {
+          u32x4 part = w[j][q >> 1];
+          if (high != (q & 1)) part = u32x4{};
+          add(acc, mfma(x[q >> 1], part, none), scale[j][q]);
+        }
+      }
+    }
+  };
+  // lane: column 16 (tn + j) + lane % 16 of the tile, rows 16 (tm + i) + 4 (lane / 16) + 0 .. 3
+  template <int TM, int TN>
+  SVG_DEV static void store(const Args& a, const Acc (&acc)[TM][TN], const char* scales, int, int m0, int n0, int tm, int tn, int lane,
+                            bool) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int m = m0 + (tm + i) * 16 + 4 * (lane >> 4);
+      const f32x4 sx = *reinterpret_cast<const f32x4*>(scales + ((tm + i) * 16 + 4 * (lane >> 4)) * 4);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = n0 + (tn + j) * 16 + (lane & 15);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n < a.N && m + e < a.M) put(a, (size_t)(m + e) * a.N + n, acc[i][j][e] * sx[e]);
       }
     }
   }
@@ -94,201 +183,273 @@ SVG_DEV void load4_to_lds(const char* from, u32 lane4, u32 to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane4), "s"(from) : "memory");
 }
-SVG_DEV u32 round_to(int type, float v) {
-  return type == SVG_F16 ? kv_round<false>(v) : kv_round<true>(v);
+// 2 bytes a lane, each to a dword of its own.
+SVG_DEV void load2_to_lds(const char* from, u32 lane2, u32 to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2"
+               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane2), "s"(from) : "memory");
+}
+// A pointer that is the same for the wave, in scalar registers.
+SVG_DEV const char* uniform(const char* p) {
+  const unsigned long long v = reinterpret_cast<unsigned long long>(p);
+  const u32 lo = (u32)__builtin_amdgcn_readfirstlane((int)(u32)v), hi = (u32)__builtin_amdgcn_readfirstlane((int)(u32)(v >> 32));
+  return reinterpret_cast<const char*>((unsigned long long)hi << 32 | lo);
+}
+// All but the last N loads of this wave have arrived.
+template <int N>
+SVG_DEV void wait_vm() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N)
+  asm volatile("" ::: "memory");
 }
 
-template <class F, int WM, int WN, int TM, int TN, int STAGES>
+// One workgroup a compute unit, which goes from tile to tile: the next tile's first stages are requested during a
+// tile's last steps and its results are on their way out while the next one is computed.
+template <class F, int WM, int WN, int TM, int TN>
 __global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
-  constexpr int WAVES = WM * WN, MF = WM * TM, NF = WN * TN;          // fragments of 16 rows, of 16 columns
+  constexpr int WAVES = WM * WN, MF = WM * TM, NF = WN * TN, STAGES = 4;  // fragments of 16 rows, of 16 columns
   constexpr int FRAGS = NF + MF * F::kX;                              // KiB of a stage
   constexpr int PARAMS = F::k4 ? NF / 4 * F::kParams : 0;             // 256-byte loads of parameters
   constexpr int STAGE = FRAGS * 1024 + PARAMS * 256;
-  static_assert(FRAGS % WAVES == 0 && (PARAMS == 0 || PARAMS <= WAVES), "loads of a wave");
-  constexpr int LOADS = FRAGS / WAVES;
-  __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE];
+  constexpr int XI = MF / 4, WI = F::k4 ? 0 : NF / 4;                 // 64 row scales, 64 column scales a load
+  static_assert(FRAGS % WAVES == 0 && PARAMS <= WAVES && MF % 4 == 0 && NF % 4 == 0 && XI + WI <= WAVES, "loads of a wave");
+  static_assert(TM % 4 == 0, "the places of the activations' fragments are the same in every step");
+  constexpr int LOADS = FRAGS / WAVES, STORES = TM * TN;
+  static_assert(STORES + LOADS < 64, "what the counter of loads holds");
+  __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE + (XI + WI) * 256];
+  char* const scales = lds + STAGES * STAGE;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
   const u32 base = lds_at(lds);
   const int steps = (a.K + F::kStep - 1) / F::kStep, slabs = a.K >> 5;
-  // tiles: every XCD takes a stretch of them, by columns inside groups of 8 tile rows
-  const u32 total = (u32)a.tiles_m * (u32)a.tiles_n, per = total >> 3, more = total & 7u;
-  const u32 xcd = blockIdx.x & 7u, t = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
-  const u32 group = t / (8u * a.tiles_n), in = t % (8u * a.tiles_n);
-  const u32 rows_in = (u32)a.tiles_m - group * 8 < 8 ? (u32)a.tiles_m - group * 8 : 8;
-  const int m0 = (int)(group * 8 + in % rows_in) * MF * 16, n0 = (int)(in / rows_in) * NF * 16;
+  const int last_tile = ((a.N + 15) >> 4) - 1;
+  // Tiles: round after round of one for each workgroup; in a round every XCD takes a stretch of them, by columns inside
+  // groups of 8 tile rows.
+  const u32 total = (u32)a.tiles_m * (u32)a.tiles_n, grid = gridDim.x;
+  auto tile_of = [&](u32 round, int& m0, int& n0) {
+    const u32 first = round * grid, left = total - first < grid ? total - first : grid, per = left >> 3, more = left & 7u;
+    const u32 xcd = blockIdx.x & 7u, at = blockIdx.x >> 3;
+    if (first >= total || at >= per + (xcd < more ? 1u : 0u)) return false;
+    const u32 t = first + xcd * per + (xcd < more ? xcd : more) + at;
+    const u32 group = t / (8u * a.tiles_n), in = t % (8u * a.tiles_n);
+    const u32 rows_in = (u32)a.tiles_m - group * 8 < 8 ? (u32)a.tiles_m - group * 8 : 8;
+    m0 = (int)(group * 8 + in % rows_in) * MF * 16;
+    n0 = (int)(in / rows_in) * NF * 16;
+    return true;
+  };
 
-  // this wave's fragments of a stage: number wave + i * WAVES, first the weights', then the activations'
-  const char* wbase = a.wq + (size_t)(n0 >> 4) * steps * 1024;
-  const char* xbase = reinterpret_cast<const char*>(a.xq) + (size_t)m0 * a.K;
-  const int last_tile = ((a.N + 15) >> 4) - 1 - (n0 >> 4);
-  u32 off[LOADS], stride[LOADS];
-#pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int f = wave + i * WAVES;
-    if (f < NF) {
-      off[i] = (u32)(f < last_tile ? f : last_tile) * (u32)steps * 1024u + lane * 16u;
-      stride[i] = 1024u;
-    } else {
-      const int j = (f - NF) / F::kX, h = (f - NF) % F::kX, kb = lane >> 4;
-      int m = m0 + 16 * j + (lane & 15);
-      m = m < a.M ? m : a.M - 1;
-      const int buf = m & ~31, R = a.M - buf < 32 ? a.M - buf : 32;
-      off[i] = (u32)(buf - m0) * (u32)a.K + ((u32)(2 * h + (kb >> 1)) * R + (m & 31)) * 32u + (kb & 1) * 16u;
-      stride[i] = (u32)R * (F::kStep == 64 ? 64u : 128u);
-    }
-  }
+  // This wave's loads of a stage: fragment wave + i * WAVES, first the weights', then the activations'.  The addresses are
+  // the same for the wave but for a lane's place, and rise by the same number each stage.
+  const char* src[LOADS];
+  u32 lane_at[LOADS], stride[LOADS];
   // parameters: load number p brings one dword of 64 rows, of kind p / (NF / 4); waves below PARAMS have one each
   const char* pbase = nullptr;
   u32 poff = 0;
-  if constexpr (F::k4) {
-    const int kind = wave / (NF / 4), tile = wave % (NF / 4) * 4 + (lane >> 4);
-    const u32 blocks = (u32)(a.K + 511) >> 9, row = (u32)(tile < last_tile ? tile : last_tile) * blocks * 16u + (lane & 15);
-    if (kind < F::kS) {
-      pbase = reinterpret_cast<const char*>(a.w_scale) + (size_t)(n0 >> 4) * blocks * F::kRow;
-      poff = row * (F::kRow / 16) + 4u * kind;
-    } else {
-      constexpr u32 zrow = F::kZ4 ? F::kRow / 64 : F::kRow / 16;
-      pbase = a.w_zero + (size_t)(n0 >> 4) * blocks * (zrow * 16u);
-      poff = (row * zrow & ~3u) + 4u * (kind - F::kS);
-    }
-  }
-  auto fetch = [&](int s) {
-    const u32 to = base + (u32)(s % STAGES) * STAGE;
+  auto aim = [&](int m0, int n0) {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int f = wave + i * WAVES;
-      u32 o = off[i] + (u32)s * stride[i];
-      if (f >= NF) {
-        // K's last slabs may be missing: any codes do, the weights there are zero
-        const int slab = s * (F::kStep / 32) + (F::kX == 2 ? 2 * ((f - NF) & 1) : 0) + (lane >> 5);
-        if (slab >= slabs) o -= (u32)(slab - slabs + 1) * (stride[i] / (F::kStep / 32));
+      if (f < NF) {
+        const int tile = (n0 >> 4) + f;
+        src[i] = a.wq + (size_t)(tile < last_tile ? tile : last_tile) * steps * 1024;
+        lane_at[i] = lane * 16u;
+        stride[i] = 1024u;
+      } else {
+        // rows past the last one: that one's codes, whose products are not stored
+        const int j = (f - NF) / F::kX, h = (f - NF) % F::kX, kb = lane >> 4, m = m0 + 16 * j;
+        const int buf = (m < a.M ? m : a.M - 1) & ~31, R = a.M - buf < 32 ? a.M - buf : 32;
+        const int row = 16 * (j & 1) + (lane & 15);
+        src[i] = reinterpret_cast<const char*>(a.xq) + (size_t)buf * a.K;
+        lane_at[i] = ((u32)((2 * h + (kb >> 1)) * R) + (u32)(row < R ? row : R - 1)) * 32u + (kb & 1) * 16u;
+        stride[i] = (u32)R * F::kStep;
       }
-      load_to_lds(f < NF ? wbase : xbase, o, to + (u32)f * 1024u);
     }
     if constexpr (F::k4) {
-      if (wave < PARAMS) {
-        const u32 o = poff + (u32)(s >> 2) * (wave / (NF / 4) < F::kS || !F::kZ4 ? F::kRow : F::kRow / 4);
-        const u32 in_block = wave / (NF / 4) < F::kS || !F::kZ4 ? F::scale_at(s & 3) : F::zero_at(s & 3);
-        load4_to_lds(pbase, o + in_block, to + FRAGS * 1024 + wave * 256);
+      const int kind = wave / (NF / 4), tile = (n0 >> 4) + wave % (NF / 4) * 4 + (lane >> 4);
+      const u32 blocks = (u32)(a.K + 511) >> 9, row = (u32)((tile < last_tile ? tile : last_tile) - (n0 >> 4)) * blocks * 16u + (lane & 15);
+      if (kind < F::kS) {
+        pbase = reinterpret_cast<const char*>(a.w_scale) + (size_t)(n0 >> 4) * blocks * F::kRow;
+        poff = row * (F::kRow / 16) + 4u * kind;
+      } else {
+        constexpr u32 zrow = F::kZ4 ? F::kRow / 64 : F::kRow / 16;
+        pbase = a.w_zero + (size_t)(n0 >> 4) * blocks * (zrow * 16u);
+        poff = (row * zrow & ~3u) + 4u * (kind - F::kS);
       }
     }
   };
-  typename F::Acc acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = typename F::Acc{};
-#pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s)
-    if (s < steps) fetch(s);
-  for (int s = 0; s < steps; ++s) {
-    if (s + STAGES - 2 >= steps) wait_loads<0>();
-    else if (PARAMS > 0 && wave < PARAMS) wait_loads<(LOADS + 1) * (STAGES - 2)>();
-    else wait_loads<LOADS * (STAGES - 2)>();
-    barrier();
-    if (s + STAGES - 1 < steps) fetch(s + STAGES - 1);
-    const char* at = lds + (s % STAGES) * STAGE + lane * 16;
-    if constexpr (!F::k4) {
-      u32x4 x[TM];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) x[i] = *reinterpret_cast<const u32x4*>(at + (NF + wm * TM + i) * 1024);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(at + (wn * TN + j) * 1024);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) acc[i][j] = mfma(w, x[i], acc[i][j]);
+  auto fetch_piece = [&](int s, int slot, int i, bool last) {
+    const int f = wave + i * WAVES;
+    u32 o = lane_at[i];
+    if (last && f >= NF) {
+      // K's last slabs may be missing: the last one's codes, the weights there are zero
+      const int slab = s * (F::kStep / 32) + (F::kX == 2 ? 2 * ((f - NF) & 1) : 0) + (lane >> 5);
+      if (slab >= slabs) o -= (u32)(slab - slabs + 1) * (stride[i] / (F::kStep / 32));
+    }
+    load_to_lds(uniform(src[i]), o, base + (u32)slot * STAGE + (u32)f * 1024u);
+    src[i] += stride[i];
+  };
+  auto fetch_params = [&](int s, int slot) {
+    if constexpr (F::k4) {
+      if (wave < PARAMS) {
+        const bool scale = wave / (NF / 4) < F::kS || !F::kZ4;
+        const u32 o = poff + (u32)(s >> 2) * (scale ? F::kRow : F::kRow / 4) + (scale ? F::scale_at(s & 3) : F::zero_at(s & 3));
+        load4_to_lds(uniform(pbase), o, base + (u32)slot * STAGE + FRAGS * 1024 + wave * 256);
       }
+    }
+  };
+  // Waits until this wave's loads of a stage have arrived, behind which those of N more stages were requested (and EXTRA others).
+  auto arrived = [&](auto n, auto extra) {
+    constexpr int N = decltype(n)::value, X = decltype(extra)::value;
+    if constexpr (PARAMS == 0) {
+      wait_vm<LOADS * N + X>();
     } else {
-      const char* par = lds + (s % STAGES) * STAGE + FRAGS * 1024;
-      u32x4 x[TM][2];
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) x[i][h] = *reinterpret_cast<const u32x4*>(at + (NF + (wm * TM + i) * 2 + h) * 1024);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const u32x4 raw = *reinterpret_cast<const u32x4*>(at + (wn * TN + j) * 1024);
-        u32 word[F::kParams];
-#pragma unroll
-        for (int p = 0; p < F::kParams; ++p)
-          word[p] = *reinterpret_cast<const u32*>(par + p * (NF / 4 * 256) + (wn * TN + j) * 64 + (lane & 15) * 4);
-        u32x4 w[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32 z = F::zero(word + F::kS, s & 3, h, lane) * 0x01010101u;
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            w[h][2 * q] = less(raw[2 * h + q], z);
-            w[h][2 * q + 1] = less(raw[2 * h + q] >> 4, z);
-          }
-        }
-        F::product(x, w, word, s & 3, lane, acc, j);
-      }
+      if (wave < PARAMS) wait_vm<(LOADS + 1) * N + X>();
+      else wait_vm<LOADS * N + X>();
     }
+  };
+  using std::integral_constant;
+  using Zero = integral_constant<int, 0>;
+  using One = integral_constant<int, 1>;
+
+  int m0 = 0, n0 = 0;
+  if (!tile_of(0, m0, n0)) return;
+  u32 tiles = 1, round = 0;          // of this workgroup; the round whose tile is being requested
+  for (int x, y; tile_of(tiles, x, y);) ++tiles;
+  const u32 all = tiles * (u32)steps;
+  int fs = 0;                        // the stage of that tile that is requested next
+  bool feeding = true;
+  auto fed = [&] {                   // a stage has been requested
+    if (++fs < steps) return;
+    fs = 0;
+    int x = 0, y = 0;
+    feeding = tile_of(++round, x, y);
+    if (feeding) aim(x, y);
+  };
+
+  typename F::Acc acc[TM][TN];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = typename F::Acc{};
+  };
+  clear();
+  aim(m0, n0);
+#pragma unroll 1
+  for (int s = 0; s < STAGES - 1; ++s) {
+    if (!feeding) break;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fetch_piece(fs, s, i, fs == steps - 1);
+    fetch_params(fs, s);
+    fed();
   }
-  if constexpr (F::k4) {
-    // lane: column n0 + .. + lane % 16, rows m0 + .. + 4 (lane / 16) + 0 .. 3
+  if (all > 2) arrived(integral_constant<int, 2>{}, Zero{});
+  else wait_vm<0>();
+  barrier();
+
+  // The weights' fragments of a step are read while the step before is computed, from the next stage, which has arrived
+  // before the step begins; the activations' a few groups of products ahead.
+  constexpr int AHEAD = 3, RING = 4;
+  u32x4 x[RING][F::kX], w[2][TN];
+  u32 word[2][TN][F::kParams + 1];
+  const char* mine = lds + lane * 16;
+  const char* params = lds + FRAGS * 1024 + wn * TN * 64 + (lane & 15) * 4;
+  auto read_w = [&](int slot, int j, int to) {
+    w[to][j] = *reinterpret_cast<const u32x4*>(mine + slot * STAGE + (wn * TN + j) * 1024);
+#pragma unroll
+    for (int p = 0; p < F::kParams; ++p) word[to][j][p] = *reinterpret_cast<const u32*>(params + slot * STAGE + p * (NF / 4 * 256) + j * 64);
+  };
+  auto read_x = [&](int slot, int i) {
+#pragma unroll
+    for (int h = 0; h < F::kX; ++h)
+      x[i % RING][h] = *reinterpret_cast<const u32x4*>(mine + slot * STAGE + (NF + (wm * TM + i) * F::kX + h) * 1024);
+  };
+#pragma unroll
+  for (int j = 0; j < TN; ++j) read_w(0, j, 0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) read_x(0, i);
+
+  int s = 0, slot = 0;               // step of the tile, its place
+  u32 g = 0;                         // steps done
+  u32 round_done = 0;
+  bool stored = false;               // whether stores are on their way (STORES of every wave)
+  // One step (parity: of its fragments).  FAST: in the middle of a tile.
+  auto step = [&](auto parity, auto fast) {
+    constexpr int P = decltype(parity)::value;
+    constexpr bool FAST = decltype(fast)::value;
+    const int next = (slot + 1) & 3, into = (slot + 3) & 3;
+    __builtin_amdgcn_sched_barrier(0);
+    if (FAST) arrived(One{}, Zero{});
+    else if (g + 2 >= all) wait_vm<0>();
+    else if (stored && s < 2) arrived(One{}, integral_constant<int, STORES>{});
+    else arrived(One{}, Zero{});
+    barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (!FAST && s == 0 && wave < XI + WI) {
+      // the tile's scales, read behind its last step
+      const bool rows = wave < XI;
+      const int at = rows ? m0 + wave * 64 + lane : n0 + (wave - XI) * 64 + lane, most = rows ? a.M : a.N;
+      const u32 clamped = (u32)(at < most ? at : most - 1);
+      const u32 to = base + STAGES * STAGE + wave * 256;
+      if (rows) load4_to_lds(reinterpret_cast<const char*>(a.x_scale), clamped * 4u, to);
+      else load2_to_lds(reinterpret_cast<const char*>(a.w_scale), clamped * 2u, to);
+    }
+    typename F::template Operands<TN> op;
+    op.take(w[P], word[P], s & 3, lane);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int m = m0 + (wm * TM + i) * 16 + 4 * (lane >> 4);
-      float sx[4];
+      if (i + AHEAD < TM) read_x(slot, i + AHEAD);
+      else read_x(next, i + AHEAD - TM);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sx[e] = m + e < a.M ? a.x_scale[m + e] : 0.f;
+      for (int j = i * TN / TM; j < (i + 1) * TN / TM; ++j) read_w(next, j, P ^ 1);
+      if (FAST || feeding) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int n = n0 + (wn * TN + j) * 16 + (lane & 15);
-        if (n >= a.N) continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (m + e >= a.M) continue;
-          const float v = acc[i][j][e] * sx[e];
-          const size_t to = (size_t)(m + e) * a.N + n;
-          if (a.y_type == SVG_F32) static_cast<float*>(a.y)[to] = v;
-          else static_cast<uint16_t*>(a.y)[to] = (uint16_t)round_to(a.y_type, v);
-        }
+        for (int l = i * LOADS / TM; l < (i + 1) * LOADS / TM; ++l) fetch_piece(fs, into, l, !FAST && fs == steps - 1);
+        if (i == TM - 1) fetch_params(fs, into);
       }
+#pragma unroll
+      for (int j = 0; j < TN; ++j) op.multiply(x[i % RING], j, acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    return;
-  } else {
-  // lane: row m0 + .. + lane % 16, columns n0 + .. + 4 (lane / 16) + 0 .. 3
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int n = n0 + (wn * TN + j) * 16 + 4 * (lane >> 4);
-    float sw[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sw[e] = n + e < a.N ? half_bits_to_float(a.w_scale[n + e]) : 0.f;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int m = m0 + (wm * TM + i) * 16 + (lane & 15);
-      if (m >= a.M || n >= a.N) continue;
-      const float sx = a.x_scale[m];
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * (sx * sw[e]);
-      const size_t at = (size_t)m * a.N + n;
-      if (a.y_type == SVG_F32) {
-        float* p = static_cast<float*>(a.y) + at;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) p[e] = v[e];
-      } else {
-        uint16_t* p = static_cast<uint16_t*>(a.y) + at;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) p[e] = (uint16_t)round_to(a.y_type, v[e]);
-      }
+    if (FAST) ++fs;
+    else if (feeding) fed();
+    ++s;
+    ++g;
+    slot = next;
+  };
+  auto finish = [&] {
+    if (steps < STAGES) {            // (the scales have had no step to arrive in)
+      wait_vm<0>();
+      barrier();
     }
-  }
+    stored = a.whole && m0 + MF * 16 <= a.M && n0 + NF * 16 <= a.N;
+    F::template store<TM, TN>(a, acc, scales, XI * 256, m0, n0, wm * TM, wn * TN, lane, stored);
+    if (!stored) wait_vm<0>();
+    clear();
+    s = 0;
+    ++round_done;
+    tile_of(round_done, m0, n0);
+  };
+  while (g < all) {
+    while (s >= 2 && s + 6 <= steps) {
+      step(Zero{}, std::true_type{});
+      step(One{}, std::true_type{});
+    }
+    step(Zero{}, std::false_type{});
+    if (s == steps) finish();
+    if (g >= all) break;
+    step(One{}, std::false_type{});
+    if (s == steps) finish();
   }
 }
 
-template <class F, int WM, int WN, int TM, int TN, int STAGES>
+template <class F, int WM, int WN, int TM, int TN>
 hipError_t launch(Args a, hipStream_t stream) {
   constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
-  const auto fn = k_prompt_linear<F, WM, WN, TM, TN, STAGES>;
-  hipLaunchKernelGGL(fn, dim3((u32)a.tiles_m * (u32)a.tiles_n), dim3(64 * WM * WN), 0, stream, a);
+  a.whole = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  const auto fn = k_prompt_linear<F, WM, WN, TM, TN>;
+  const u32 tiles = (u32)a.tiles_m * (u32)a.tiles_n, cus = (u32)svg_cu_count() & ~7u;
+  hipLaunchKernelGGL(fn, dim3(tiles < cus ? (tiles + 7) / 8 * 8 : cus), dim3(64 * WM * WN), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -296,19 +457,19 @@ hipError_t launch(Args a, hipStream_t stream) {
 
 hipError_t svg_launch_prompt_w8(const int8_t* xq, const float* x_scale, int M, int K, const int8_t* wq, const uint16_t* w_scale, int N,
                                 void* y, int y_type, hipStream_t stream) {
-  const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, nullptr, y, M, N, K, y_type, 0, 0};
-  if (M <= 128) return launch<W8, 2, 4, 4, 2, 4>(a, stream);
-  return launch<W8, 2, 4, 8, 4, 4>(a, stream);
+  const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, nullptr, y, M, N, K, y_type, 0, 0, 0};
+  if (M <= 128) return launch<W8, 2, 4, 4, 2>(a, stream);
+  return launch<W8, 2, 4, 8, 4>(a, stream);
 }
 
 template <int G, bool Z4>
 static hipError_t launch_w4(const Args& a, hipStream_t stream) {
-  return launch<W4<G, Z4>, 2, 4, 4, 2, 4>(a, stream);
+  return launch<W4<G, Z4>, 2, 4, 4, 2>(a, stream);
 }
 
 hipError_t svg_launch_prompt_w4(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
                                 const void* w_zero, bool z4, int group, int N, void* y, int y_type, hipStream_t stream) {
-  const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, static_cast<const char*>(w_zero), y, M, N, K, y_type, 0, 0};
+  const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, static_cast<const char*>(w_zero), y, M, N, K, y_type, 0, 0, 0};
   if (z4) return group == 32 ? launch_w4<32, true>(a, stream) : (group == 64 ? launch_w4<64, true>(a, stream) : launch_w4<128, true>(a, stream));
   return group == 32 ? launch_w4<32, false>(a, stream) : (group == 64 ? launch_w4<64, false>(a, stream) : launch_w4<128, false>(a, stream));
 }
