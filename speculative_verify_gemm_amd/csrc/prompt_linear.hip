@@ -29,7 +29,16 @@ SVG_DEV void put(const Args& a, size_t at, float v) {
   else static_cast<uint16_t*>(a.y)[at] = (uint16_t)round_to(a.y_type, v);
 }
 
+// Four values of a row together (Args::whole).
+SVG_DEV void put4(const Args& a, size_t at, const float (&v)[4]) {
+  if (a.y_type == SVG_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = make_uint2(round2(a.y_type, v[0], v[1]), round2(a.y_type, v[2], v[3]));
+}
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 SVG_DEV v4i mfma(u32x4 a, u32x4 b, v4i c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
@@ -37,7 +46,7 @@ SVG_DEV v4i mfma(u32x4 a, u32x4 b, v4i c) {
 
 // Weight formats: kStep values of K a step; kX fragments of 16 x 64 activation codes in one.
 struct W8 {
-  static constexpr int kStep = 64, kX = 1, kParams = 0;
+  static constexpr int kStep = 64, kX = 1, kParams = 0, kStages = 4, kAhead = 3, kRing = 4;
   static constexpr bool k4 = false;
   typedef v4i Acc;
   template <int TN>
@@ -47,8 +56,29 @@ struct W8 {
 #pragma unroll
       for (int j = 0; j < TN; ++j) w[j] = raw[j];
     }
-    SVG_DEV void multiply(const u32x4 (&x)[1], int j, v4i& acc) const { acc = mfma(w[j], x[0], acc); }
+    template <int TM>
+    SVG_DEV void multiply(const u32x4 (&x)[1], int i, v4i (&acc)[TM][TN]) const {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mfma(w[j], x[0], acc[i][j]);
+    }
   };
+  // 16 rows and columns, scales from memory
+  SVG_DEV static void store_one(const Args& a, v4i sum, int m0, int n0, int lane) {
+    const int m = m0 + (lane & 15), n = n0 + 4 * (lane >> 4);
+    if (m >= a.M) return;
+    const float sx = a.x_scale[m];
+    const size_t at = (size_t)m * a.N + n;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = n + e < a.N ? (float)sum[e] * (sx * half_bits_to_float(a.w_scale[n + e])) : 0.f;
+    if (a.whole && n < a.N) {
+      put4(a, at, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) put(a, at + e, v[e]);
+    }
+  }
   // lane: row 16 (tm + i) + lane % 16 of the tile, columns 16 (tn + j) + 4 (lane / 16) + 0 .. 3
   template <int TM, int TN>
   SVG_DEV static void store(const Args& a, const Acc (&acc)[TM][TN], const char* scales, int columns, int m0, int n0, int tm, int tn,
@@ -71,12 +101,7 @@ struct W8 {
         for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * (sx[i] * sw[e]);
         const size_t at = (size_t)m * a.N + n;
         if (full) {
-          if (a.y_type == SVG_F32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
-          } else {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
-                make_uint2(round2(a.y_type, v[0], v[1]), round2(a.y_type, v[2], v[3]));
-          }
+          put4(a, at, v);
         } else if (m < a.M) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -91,7 +116,7 @@ SVG_DEV u32 less(u32 codes, u32 z) { return (((codes & 0x0F0F0F0Fu) | 0x80808080
 
 template <int G, bool Z4_>
 struct W4 {
-  static constexpr int kStep = 128, kX = 2, kGroup = G;
+  static constexpr int kStep = 128, kX = 2, kGroup = G, kStages = 3, kAhead = 1, kRing = 2;
   static constexpr bool k4 = true, kZ4 = Z4_;
   // dwords of scales and of zeros that a row has in a step
   static constexpr int kS = G == 32 ? 2 : 1, kZ = G == 32 && !Z4_ ? 2 : 1, kParams = kS + kZ;
@@ -100,16 +125,17 @@ struct W4 {
   SVG_DEV static u32 scale_at(int s) { return G == 32 ? s * 8u : (G == 64 ? s * 4u : (s >> 1) * 4u); }
   SVG_DEV static u32 zero_at(int s) { return G == 32 ? (s >> 1) * 4u : 0u; }
   typedef f32x4 Acc;
-  // the zero point of the 16 values that a lane holds of half h of step s (of four in 512 values)
+  // the zero point of the 16 values that a lane holds of half h of step s (of four in 512 values), in every byte; fp16
+  // zeros: added to 1024 they are the low bits of the sum
   SVG_DEV static u32 zero(const u32* word, int s, int h, int lane) {
     const int b = lane >> 5;  // which half of 64 values
     if constexpr (Z4_) {
       const int at = G == 64 ? 2 * s + h : (G == 128 ? 4 * (lane & 1) + s : 4 * (s & 1) + 2 * h + b);
-      return (word[0] >> (4 * at)) & 15u;
+      return __builtin_amdgcn_perm(0u, (word[0] >> (4 * at)) & 15u, 0u);
     } else {
-      const u32 w = G == 32 ? word[h] : word[0];
+      const u32 w = __builtin_bit_cast(u32, __builtin_bit_cast(f16x2, G == 32 ? word[h] : word[0]) + f16x2{1024, 1024});
       const int hi = G == 64 ? h : (G == 128 ? s & 1 : b);
-      return (u32)(int)half_bits_to_float((uint16_t)(hi ? w >> 16 : w & 0xFFFFu)) & 15u;
+      return __builtin_amdgcn_perm(0u, w & 0x00FF00FFu, hi ? 0x02020202u : 0u);
     }
   }
   // A step's weights: codes less zero points, and the scales of its groups.
@@ -125,7 +151,7 @@ struct W4 {
       for (int j = 0; j < TN; ++j) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const u32 z = zero(word[j] + kS, s, h, lane) * 0x01010101u;
+          const u32 z = zero(word[j] + kS, s, h, lane);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             w[j][h][2 * q] = less(raw[j][2 * h + q], z);
@@ -137,24 +163,50 @@ struct W4 {
           scale[j][q] = G == 128 ? half_bits_to_float((uint16_t)(s & 1 ? word[j][0] >> 16 : word[j][0] & 0xFFFFu)) : half_at(word[j], q);
       }
     }
-    SVG_DEV void multiply(const u32x4 (&x)[2], int j, f32x4& acc) const {
+    // the products of row tile i, and what those of the one before add to its sums
+    v4i sum[2][TN][GROUPS];
+    template <int TM>
+    SVG_DEV void multiply(const u32x4 (&x)[2], int i, f32x4 (&acc)[TM][TN]) {
       const v4i none{};
-      if constexpr (G == 128) {
-        add(acc, mfma(x[1], w[j][1], mfma(x[0], w[j][0], none)), scale[j][0]);
-      } else if constexpr (G == 64) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) add(acc, mfma(x[h], w[j][h], none), scale[j][h]);
-      } else {
-        // groups of 32: half the lanes' weights at a time
+      for (int j = 0; j < TN; ++j) {
+        v4i (&to)[GROUPS] = sum[i & 1][j];
+        if constexpr (G == 128) {
+          to[0] = mfma(x[1], w[j][1], mfma(x[0], w[j][0], none));
+        } else if constexpr (G == 64) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          u32x4 part = w[j][q >> 1];
-          if (high != (q & 1)) part = u32x4{};
-          add(acc, mfma(x[q >> 1], part, none), scale[j][q]);
+          for (int h = 0; h < 2; ++h) to[h] = mfma(x[h], w[j][h], none);
+        } else {
+          // groups of 32: half the lanes' weights at a time
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            u32x4 part = w[j][q >> 1];
+            if (high != (q & 1)) part = u32x4{};
+            to[q] = mfma(x[q >> 1], part, none);
+          }
         }
+      }
+      if (i > 0) add(i - 1, acc);
+      if (i == TM - 1) add(i, acc);
+    }
+    template <int TM>
+    SVG_DEV void add(int i, f32x4 (&acc)[TM][TN]) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+#pragma unroll
+        for (int q = 0; q < GROUPS; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf((float)sum[i & 1][j][q][e], scale[j][q], acc[i][j][e]);
+        asm volatile("" : "+v"(acc[i][j]));  // here, not at the step's end: the products' registers are needed again
       }
     }
   };
+  SVG_DEV static void store_one(const Args& a, f32x4 sum, int m0, int n0, int lane) {
+    const int m = m0 + 4 * (lane >> 4), n = n0 + (lane & 15);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n < a.N && m + e < a.M) put(a, (size_t)(m + e) * a.N + n, sum[e] * a.x_scale[m + e]);
+  }
   // lane: column 16 (tn + j) + lane % 16 of the tile, rows 16 (tm + i) + 4 (lane / 16) + 0 .. 3
   template <int TM, int TN>
   SVG_DEV static void store(const Args& a, const Acc (&acc)[TM][TN], const char* scales, int, int m0, int n0, int tm, int tn, int lane,
@@ -171,10 +223,6 @@ struct W4 {
           if (n < a.N && m + e < a.M) put(a, (size_t)(m + e) * a.N + n, acc[i][j][e] * sx[e]);
       }
     }
-  }
-  SVG_DEV static void add(Acc& to, v4i sum, float scale) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) to[e] = __builtin_fmaf((float)sum[e], scale, to[e]);
   }
 };
 
@@ -204,15 +252,15 @@ SVG_DEV void wait_vm() {
 
 // One workgroup a compute unit, which goes from tile to tile: the next tile's first stages are requested during a
 // tile's last steps and its results are on their way out while the next one is computed.
-template <class F, int WM, int WN, int TM, int TN>
-__global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
-  constexpr int WAVES = WM * WN, MF = WM * TM, NF = WN * TN, STAGES = 4;  // fragments of 16 rows, of 16 columns
+template <class F, int WM, int WN, int TM, int TN, int WGS>
+__global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_prompt_linear(Args a) {
+  constexpr int WAVES = WM * WN, MF = WM * TM, NF = WN * TN, STAGES = F::kStages;  // fragments of 16 rows, of 16 columns
   constexpr int FRAGS = NF + MF * F::kX;                              // KiB of a stage
   constexpr int PARAMS = F::k4 ? NF / 4 * F::kParams : 0;             // 256-byte loads of parameters
   constexpr int STAGE = FRAGS * 1024 + PARAMS * 256;
   constexpr int XI = MF / 4, WI = F::k4 ? 0 : NF / 4;                 // 64 row scales, 64 column scales a load
   static_assert(FRAGS % WAVES == 0 && PARAMS <= WAVES && MF % 4 == 0 && NF % 4 == 0 && XI + WI <= WAVES, "loads of a wave");
-  static_assert(TM % 4 == 0, "the places of the activations' fragments are the same in every step");
+  static_assert(TM % F::kRing == 0, "the places of the activations' fragments are the same in every step");
   constexpr int LOADS = FRAGS / WAVES, STORES = TM * TN;
   static_assert(STORES + LOADS < 64, "what the counter of loads holds");
   __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE + (XI + WI) * 256];
@@ -341,13 +389,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
     fetch_params(fs, s);
     fed();
   }
-  if (all > 2) arrived(integral_constant<int, 2>{}, Zero{});
+  if (all > STAGES - 2) arrived(integral_constant<int, STAGES - 2>{}, Zero{});
   else wait_vm<0>();
   barrier();
 
   // The weights' fragments of a step are read while the step before is computed, from the next stage, which has arrived
   // before the step begins; the activations' a few groups of products ahead.
-  constexpr int AHEAD = 3, RING = 4;
+  constexpr int AHEAD = F::kAhead, RING = F::kRing;
   u32x4 x[RING][F::kX], w[2][TN];
   u32 word[2][TN][F::kParams + 1];
   const char* mine = lds + lane * 16;
@@ -375,12 +423,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
   auto step = [&](auto parity, auto fast) {
     constexpr int P = decltype(parity)::value;
     constexpr bool FAST = decltype(fast)::value;
-    const int next = (slot + 1) & 3, into = (slot + 3) & 3;
+    constexpr int NEWER = STAGES - 3;  // stages that were requested behind the one that is needed
+    const int next = slot + 1 == STAGES ? 0 : slot + 1, into = slot == 0 ? STAGES - 1 : slot - 1;
     __builtin_amdgcn_sched_barrier(0);
-    if (FAST) arrived(One{}, Zero{});
-    else if (g + 2 >= all) wait_vm<0>();
-    else if (stored && s < 2) arrived(One{}, integral_constant<int, STORES>{});
-    else arrived(One{}, Zero{});
+    if (FAST) arrived(integral_constant<int, NEWER>{}, Zero{});
+    else if (g + 1 + NEWER >= all) wait_vm<0>();
+    else if (stored && s < STAGES - 2) arrived(integral_constant<int, NEWER>{}, integral_constant<int, STORES>{});
+    else arrived(integral_constant<int, NEWER>{}, Zero{});
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     if (!FAST && s == 0 && wave < XI + WI) {
@@ -405,8 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
         for (int l = i * LOADS / TM; l < (i + 1) * LOADS / TM; ++l) fetch_piece(fs, into, l, !FAST && fs == steps - 1);
         if (i == TM - 1) fetch_params(fs, into);
       }
-#pragma unroll
-      for (int j = 0; j < TN; ++j) op.multiply(x[i % RING], j, acc[i][j]);
+      op.multiply(x[i % RING], i, acc);
       __builtin_amdgcn_sched_barrier(0);
     }
     if (FAST) ++fs;
@@ -441,35 +489,182 @@ __global__ __launch_bounds__(64 * WM * WN) void k_prompt_linear(Args a) {
   }
 }
 
-template <class F, int WM, int WN, int TM, int TN>
+// Few rows: bound by the weights' bytes, and by the way to them.  A workgroup takes 16 columns and up to 16 TM rows; its waves
+// take the steps of K in turn, weights and codes straight into registers, and their sums are added up in LDS.
+constexpr int kShortWaves = 8;
+template <class F, int TM>
+__global__ __launch_bounds__(64 * kShortWaves) void k_prompt_linear_short(Args a) {
+  typedef typename F::Acc Acc;
+  __shared__ __attribute__((aligned(1024))) char lds[kShortWaves * TM * 1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * TM * 16;
+  const int steps = (a.K + F::kStep - 1) / F::kStep, slabs = a.K >> 5;
+  const char* wp = a.wq + (size_t)blockIdx.x * steps * 1024 + lane * 16;
+  const char* xp[TM];
+  u32 stride[TM];
+  int slab_bytes[TM];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + 16 * i + (lane & 15), row = m < a.M ? m : a.M - 1, buf = row & ~31, R = a.M - buf < 32 ? a.M - buf : 32;
+    xp[i] = reinterpret_cast<const char*>(a.xq) + (size_t)buf * a.K + (u32)((lane >> 5) * R + (row & 31)) * 32u + ((lane >> 4) & 1) * 16u;
+    slab_bytes[i] = R * 32;
+    stride[i] = (u32)R * F::kStep;
+  }
+  struct Regs {
+    u32x4 w[1], x[TM][F::kX];
+    u32 word[1][F::kParams + 1];
+  };
+  auto load = [&](int s, Regs& r) {
+    r.w[0] = *reinterpret_cast<const u32x4*>(wp + (size_t)s * 1024);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int h = 0; h < F::kX; ++h) {
+        // K's last slabs may be missing: the last one's codes, the weights there are zero
+        const int slab = s * (F::kStep / 32) + 2 * h + (lane >> 5), over = slab < slabs ? 0 : slab - slabs + 1;
+        r.x[i][h] = *reinterpret_cast<const u32x4*>(xp[i] + (size_t)((u32)s * stride[i]) + (2 * h - over) * slab_bytes[i]);
+      }
+    if constexpr (F::k4) {
+      const u32 blocks = (u32)(a.K + 511) >> 9, row = ((u32)blockIdx.x * blocks + (u32)(s >> 2)) * 16u + (lane & 15);
+      const char* sp = reinterpret_cast<const char*>(a.w_scale) + (size_t)row * (F::kRow / 16) + F::scale_at(s & 3);
+#pragma unroll
+      for (int p = 0; p < F::kS; ++p) r.word[0][p] = *reinterpret_cast<const u32*>(sp + 4 * p);
+      constexpr u32 zrow = F::kZ4 ? F::kRow / 64 : F::kRow / 16;
+      const char* zp = a.w_zero + ((size_t)row * zrow & ~(size_t)3) + (F::kZ4 ? F::zero_at(s & 3) : F::scale_at(s & 3));
+#pragma unroll
+      for (int p = 0; p < F::kZ; ++p) r.word[0][F::kS + p] = *reinterpret_cast<const u32*>(zp + 4 * p);
+    }
+  };
+  Acc acc[TM][1];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) acc[i][0] = Acc{};
+  auto compute = [&](int s, const Regs& r) {
+    typename F::template Operands<1> op;
+    op.take(r.w, r.word, s & 3, lane);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) op.multiply(r.x[i], i, acc);
+  };
+  Regs r[2];
+  if (wave < steps) load(wave, r[0]);
+  int s = wave;
+#pragma unroll 1
+  for (; s + kShortWaves < steps; s += 2 * kShortWaves) {
+    load(s + kShortWaves, r[1]);
+    compute(s, r[0]);
+    if (s + 2 * kShortWaves < steps) load(s + 2 * kShortWaves, r[0]);
+    compute(s + kShortWaves, r[1]);
+  }
+  if (s < steps) compute(s, r[0]);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) *reinterpret_cast<Acc*>(lds + (wave * TM + i) * 1024 + lane * 16) = acc[i][0];
+  __syncthreads();
+  if (wave >= TM) return;
+  Acc sum{};
+#pragma unroll
+  for (int w = 0; w < kShortWaves; ++w) sum += *reinterpret_cast<const Acc*>(lds + (w * TM + wave) * 1024 + lane * 16);
+  F::store_one(a, sum, m0 + wave * 16, n0, lane);
+}
+
+template <class F, int WM, int WN, int TM, int TN, int WGS>
 hipError_t launch(Args a, hipStream_t stream) {
   constexpr int BM = WM * TM * 16, BN = WN * TN * 16;
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
   a.whole = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-  const auto fn = k_prompt_linear<F, WM, WN, TM, TN>;
-  const u32 tiles = (u32)a.tiles_m * (u32)a.tiles_n, cus = (u32)svg_cu_count() & ~7u;
+  const auto fn = k_prompt_linear<F, WM, WN, TM, TN, WGS>;
+  const u32 tiles = (u32)a.tiles_m * (u32)a.tiles_n, cus = WGS * (u32)svg_cu_count() & ~7u;
   hipLaunchKernelGGL(fn, dim3(tiles < cus ? (tiles + 7) / 8 * 8 : cus), dim3(64 * WM * WN), 0, stream, a);
   return hipGetLastError();
+}
+
+template <class F, int TM>
+hipError_t launch_short(Args a, hipStream_t stream) {
+  a.whole = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+  hipLaunchKernelGGL((k_prompt_linear_short<F, TM>), dim3((a.N + 15) / 16, (a.M + 16 * TM - 1) / (16 * TM)), dim3(64 * kShortWaves), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+template <class F>
+hipError_t launch_few(const Args& a, hipStream_t stream) {
+  switch ((a.M + 15) / 16) {
+    case 1: return launch_short<F, 1>(a, stream);
+    case 2: return launch_short<F, 2>(a, stream);
+    case 3: return launch_short<F, 3>(a, stream);
+    case 4: return launch_short<F, 4>(a, stream);
+    case 5: case 6: return launch_short<F, 6>(a, stream);
+    default: return launch_short<F, 8>(a, stream);
+  }
+}
+
+// Which of them: the one that is expected to take the least time, in 1/100 us, from the rounds of workgroups that its tiles
+// take and what a round takes for a step of K.  Measured (W8, us): ...
+enum { kFew, kMid, kBig };
+template <class F>
+long cost_of(int way, int M, int N, int K) {
+  const long cus = svg_cu_count(), steps = (K + F::kStep - 1) / F::kStep;
+  const auto up = [](long x, long y) { return (x + y - 1) / y; };
+  if (M == 0) return 0;
+  if (way == kFew) {
+    const long tm = up(M < 128 ? M : 128, 16);
+    return up(up(N, 16) * up(M, 128), cus) * steps * (F::k4 ? 500 + 300 * tm : 250 + 120 * tm) / 100;
+  }
+  if (way == kMid) {
+    const long t = up(M, 128) * up(N, 128), rest = t % (2 * cus);
+    const long one = F::k4 ? 114 : 33, two = F::k4 ? 190 : 58;
+    return steps * (two * (t / (2 * cus)) + (rest > cus ? two : (rest > 0 ? one : 0)));
+  }
+  return steps * 86 * up(up(M, 256) * up(N, 256), cus);
+}
+template <class F>
+hipError_t launch_way(int way, const Args& a, hipStream_t stream) {
+  if (way == kFew) return launch_few<F>(a, stream);
+  if constexpr (F::k4) {
+    return launch<F, 1, 8, 8, 1, F::kGroup == 32 ? 1 : 2>(a, stream);
+  } else {
+    if (way == kMid) return launch<F, 2, 4, 4, 2, 2>(a, stream);
+    return launch<F, 2, 4, 8, 4, 1>(a, stream);
+  }
+}
+template <class F>
+hipError_t launch_best(const Args& a, hipStream_t stream) {
+  int way = kFew;
+  long least = cost_of<F>(kFew, a.M, a.N, a.K);
+  const auto look = [&](int w, int M) {
+    const long c = cost_of<F>(w, M, a.N, a.K);
+    if (c < least) least = c, way = w;
+  };
+  look(kMid, a.M);
+  if constexpr (!F::k4) {
+    look(kBig, a.M);
+    // the rows of whole large tiles, and the rest another way, in a launch of its own (3 us)
+    const int main = a.M & ~255, rest = a.M - main;
+    if (main > 0 && rest > 0) {
+      const int then = cost_of<F>(kFew, rest, a.N, a.K) <= cost_of<F>(kMid, rest, a.N, a.K) ? kFew : kMid;
+      if (cost_of<F>(kBig, main, a.N, a.K) + cost_of<F>(then, rest, a.N, a.K) + 300 < least) {
+        Args first = a, second = a;
+        first.M = main;
+        second.M = rest;
+        second.xq += (size_t)main * a.K;
+        second.x_scale += main;
+        second.y = static_cast<char*>(a.y) + (size_t)main * a.N * (a.y_type == SVG_F32 ? 4 : 2);
+        if (const hipError_t e = launch_way<F>(kBig, first, stream)) return e;
+        return launch_way<F>(then, second, stream);
+      }
+    }
+  }
+  return launch_way<F>(way, a, stream);
 }
 
 }  // namespace
 
 hipError_t svg_launch_prompt_w8(const int8_t* xq, const float* x_scale, int M, int K, const int8_t* wq, const uint16_t* w_scale, int N,
                                 void* y, int y_type, hipStream_t stream) {
-  const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, nullptr, y, M, N, K, y_type, 0, 0, 0};
-  if (M <= 128) return launch<W8, 2, 4, 4, 2>(a, stream);
-  return launch<W8, 2, 4, 8, 4>(a, stream);
-}
-
-template <int G, bool Z4>
-static hipError_t launch_w4(const Args& a, hipStream_t stream) {
-  return launch<W4<G, Z4>, 2, 4, 4, 2>(a, stream);
+  return launch_best<W8>({xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, nullptr, y, M, N, K, y_type, 0, 0, 0}, stream);
 }
 
 hipError_t svg_launch_prompt_w4(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
                                 const void* w_zero, bool z4, int group, int N, void* y, int y_type, hipStream_t stream) {
   const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, static_cast<const char*>(w_zero), y, M, N, K, y_type, 0, 0, 0};
-  if (z4) return group == 32 ? launch_w4<32, true>(a, stream) : (group == 64 ? launch_w4<64, true>(a, stream) : launch_w4<128, true>(a, stream));
-  return group == 32 ? launch_w4<32, false>(a, stream) : (group == 64 ? launch_w4<64, false>(a, stream) : launch_w4<128, false>(a, stream));
+  if (z4) return group == 32 ? launch_best<W4<32, true>>(a, stream) : (group == 64 ? launch_best<W4<64, true>>(a, stream) : launch_best<W4<128, true>>(a, stream));
+  return group == 32 ? launch_best<W4<32, false>>(a, stream) : (group == 64 ? launch_best<W4<64, false>>(a, stream) : launch_best<W4<128, false>>(a, stream));
 }
