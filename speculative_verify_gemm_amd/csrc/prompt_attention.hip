@@ -15,6 +15,8 @@
 // The sum of the probabilities is a product as well, with ones: it adds up what the second product sees.
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/svgemm_prompt.h"
 #include "svg_cache.h"
 #include "svg_internal.h"
@@ -59,6 +61,12 @@ SVG_DEV u32 odd_halves(u32 w) {
 // kTop - kSlack, so that small ones stay above the smallest number of fp16.
 constexpr float kTop = 15.f, kSlack = 7.f, kLift = kTop - kSlack;
 
+// What the second launch has to know of an item that begins in a workgroup's share and does not end there.
+struct Join {
+  u32 last;               // the last workgroup that has some of it (the workgroup itself: there is no such item)
+  int first, rows, row0, head;
+};
+
 struct Args {
   svg_kv_cache c;
   const uint16_t* q;
@@ -66,6 +74,7 @@ struct Args {
   const int32_t *start, *count;
   float* stats;   // [groups][2][kTile] (bias, sum); the bias is infinite where no token was seen
   float* parts;   // [groups][2][kTile][dim]
+  Join* joins;    // [groups + 1]: the last one's `last` is the number of workgroups that took part
   long ld_q;
   int layer, G, n_rows, groups;
   float scale;
@@ -212,6 +221,32 @@ struct Kernel {
     float m, bias;   // the maximum that the row's exponents go by (-infinity: no token yet), and what is added to them
   };
 
+  // The pages of a slot's table row, 64 entries at a time: entry base + l in lane l (reading them one by one would wait for
+  // the tiles that are on their way).  Numbers outside the cache and pages that other slots hold too are marked.
+  static constexpr u32 kOutside = 1u << 31, kShared = 1u << 30;
+  static constexpr int kNone = 0x7FFFFFFF;
+  struct Pages {
+    const int32_t *table, *refs;
+    int first_own, n_pages, last, base;   // the entry of the first of the step's own positions; the last entry
+    u32 v;
+    SVG_DEV void look(int entry) {
+      base = entry;
+      const int e = entry + (int)(threadIdx.x & 63u);
+      v = kOutside;
+      if (e <= last) {
+        const u32 page = (u32)table[e];
+        if (page < (u32)n_pages) {
+          v = page;
+          if (refs != nullptr && e >= first_own && refs[page] > 1) v |= kShared;
+        }
+      }
+    }
+    SVG_DEV u32 at(int entry) {
+      if (entry - base >= 64) look(entry);
+      return (u32)__builtin_amdgcn_readlane((int)v, entry - base);
+    }
+  };
+
   // Value that is not finite in a tile that not all rows see whole: taken out of the product, and put into the sums of the
   // rows that see it as NaN.
   SVG_DEV static void odd_values(const char* v, int lane, const u32x4 (&p)[RT], const u32x4 (&sees)[RT], Row (&row)[RT]) {
@@ -240,9 +275,13 @@ struct Kernel {
     make_plan<WAVES>(a, plan);
     const Deal deal = deal_of(a, plan);
     // XCDs take stretches of neighbouring workgroups, which read the same keys
-    const u32 per = (u32)a.groups >> 3;
-    const u32 wg = (blockIdx.x & 7u) * per + (blockIdx.x >> 3);
-    if (wg >= deal.groups) return;
+    const u32 per = deal.groups >> 3, more = deal.groups & 7u, xcd = blockIdx.x & 7u;
+    if ((blockIdx.x >> 3) >= per + (xcd < more ? 1u : 0u)) return;
+    const u32 wg = xcd * per + (xcd < more ? xcd : more) + (blockIdx.x >> 3);
+    if (tid == 0) {
+      a.joins[wg].last = wg;
+      if (wg == 0) a.joins[a.groups].last = deal.groups;
+    }
     unsigned long long at = deal.start(wg);
     const unsigned long long end = deal.start(wg + 1);
     const u32 base = lds_at(lds);
@@ -256,8 +295,10 @@ struct Kernel {
       const unsigned long long stop = it.from + it.cost < end ? it.from + it.cost : end;
       const bool whole = at == it.from && stop == it.from + it.cost;
       const int which = at == it.from ? 1 : 0;  // the partial's place: an item's first share, or a later one
-      const int row0 = (int)it.j * kTile, rows = x.n * G - row0 < kTile ? x.n * G - row0 : kTile;
-      const int tokens = x.valid ? tokens_of(a, x, it.j) : 0, tiles = (tokens + 31) >> 5;
+      const int slot_no = uniform_i(it.s), head = uniform_i((int)it.h), len = uniform_i(x.len), first = uniform_i(x.first);
+      const int row0 = uniform_i((int)it.j) * kTile, all_rows = uniform_i(x.n) * G, rows = all_rows - row0 < kTile ? all_rows - row0 : kTile;
+      const bool valid = uniform_i(x.valid) != 0;
+      const int tokens = uniform_i(valid ? tokens_of(a, x, it.j) : 0), tiles = (tokens + 31) >> 5;
       const int t0 = uniform_i(at == it.from ? 0 : tile_at(at - it.from, it, tiles));
       const int t1 = uniform_i(stop == it.from + it.cost ? tiles : tile_at(stop - it.from, it, tiles));
       at = stop;
@@ -270,12 +311,12 @@ struct Kernel {
       for (int rt = 0; rt < RT; ++rt) {
         int r = mine + 16 * rt + col;
         r = row0 + (r < rows ? r : rows - 1);
-        const int tok = r / G, head = (int)it.h * G + (r - tok * G);
-        seen[rt] = x.len + tok;
-        q_at[rt] = (size_t)(x.first + tok) * (size_t)a.ld_q + (size_t)head * D;
+        const int tok = r / G;
+        seen[rt] = len + tok;
+        q_at[rt] = (size_t)(first + tok) * (size_t)a.ld_q + (size_t)(head * G + (r - tok * G)) * D;
       }
-      const int low = x.len + (row0 + (mine < rows ? mine : rows - 1)) / G;                                      // of the wave's rows
-      const int high = x.len + (row0 + (mine + 16 * RT < rows ? mine + 16 * RT : rows) - 1) / G;
+      const int low = len + (row0 + (mine < rows ? mine : rows - 1)) / G;                                      // of the wave's rows
+      const int high = len + (row0 + (mine + 16 * RT < rows ? mine + 16 * RT : rows) - 1) / G;
       u32x4 q[RT][NC];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
@@ -291,21 +332,16 @@ struct Kernel {
         row[rt].bias = 0.f;
       }
       // pages: position p lies in entry p >> shift of the slot's table row
-      const int32_t* table = a.c.table + (size_t)it.s * a.c.width;
-      const char* kl = static_cast<const char*>(a.c.k) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)it.h * a.c.page * D * 2;
-      const char* vl = static_cast<const char*>(a.c.v) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)it.h * a.c.page * D * 2;
+      Pages pages{a.c.table + (size_t)slot_no * a.c.width, a.c.refs, len >> shift, a.c.n_pages, (tokens - 1) >> shift, 0, 0};
+      if (t0 < t1) pages.look((t0 * 32) >> shift);
+      const char* kl = static_cast<const char*>(a.c.k) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)head * a.c.page * D * 2;
+      const char* vl = static_cast<const char*>(a.c.v) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)head * a.c.page * D * 2;
       // Requests a tile; the first of its positions that makes the rows which see it NaN (no page of the cache: all; the
       // step's own positions in a page that other slots hold: those).
       auto fetch = [&](int t, int slot) {
-        const int p = t * 32, entry = p >> shift;
-        int page = uniform_i(table[entry]);
-        int from = 0x7FFFFFFF;
-        if ((u32)page >= (u32)a.c.n_pages) {
-          page = 0;
-          from = 0;
-        } else if (a.c.refs != nullptr && p + 31 >= x.len && a.c.refs[page] > 1) {
-          from = x.len;
-        }
+        const int p = t * 32;
+        const u32 mark = pages.at(p >> shift), page = mark & kOutside ? 0u : mark & ~kShared;
+        const int from = mark & kOutside ? 0 : (mark & kShared ? len : kNone);
         const size_t off = (size_t)page * page_bytes + (size_t)(p & (a.c.page - 1)) * D * 2;
         const u32 to = base + (u32)slot * STAGE;
 #pragma unroll
@@ -314,28 +350,28 @@ struct Kernel {
           const bool key = piece * 1024 < HALF;
           load_to_lds((key ? kl : vl) + off + (key ? piece * 1024 : piece * 1024 - HALF), lane * 16u, to + piece * 1024u);
         }
-        return uniform_i(from);
+        return from;
       };
       wait_loads<0>();
       barrier();  // (the places of the item before are free)
       int odd_from[STAGES];
 #pragma unroll
-      for (int i = 0; i < STAGES - 1; ++i) odd_from[i] = t0 + i < t1 ? fetch(t0 + i, i) : 0;
-      int slot = 0;
-      for (int t = t0; t < t1; ++t) {
-        if (t + STAGES - 2 < t1) wait_loads<LOADS * (STAGES - 2)>();
+      for (int i = 0; i < STAGES - 1; ++i) odd_from[i] = t0 + i < t1 ? fetch(t0 + i, i) : kNone;
+      int slot = 0, t = t0;
+      // What the loops' tops share: tile t + AHEAD has arrived for the whole workgroup, and tile t + STAGES - 1 is requested into the
+      // place of tile t - 1, which nobody reads any more.
+      int nan_from = kNone;
+      auto advance = [&](auto ahead) {
+        constexpr int LEFT = STAGES - 2 - decltype(ahead)::value;
+        if (t + STAGES - 2 < t1) wait_loads<LOADS * LEFT>();
         else wait_loads<0>();
         barrier();
-        const int nan_from = odd_from[0];
+        nan_from = odd_from[0];
 #pragma unroll
         for (int i = 0; i + 1 < STAGES - 1; ++i) odd_from[i] = odd_from[i + 1];
         if (t + STAGES - 1 < t1) odd_from[STAGES - 2] = fetch(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
-        const char* k = lds + slot * STAGE;
-        const char* v = k + HALF;
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
-        const int p0 = t * 32;
-        if (!live || p0 > high) continue;
-        f32x4 s[RT][2];
+      };
+      auto scores = [&](const char* k, f32x4 (&s)[RT][2]) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{};
 #pragma unroll
@@ -348,80 +384,141 @@ struct Kernel {
             s[rt][1] = mfma<BF>(k1, q[rt][c], s[rt][1]);
           }
         }
-        float ff = f;
-        if (p0 + 31 > low || nan_from != 0x7FFFFFFF || !(f > 0.f)) {
-          ff = 1.f;
+      };
+      auto highest = [&](const f32x4 (&s)[2]) {
+        float top = fmaxf(s[0][0], s[0][1]);
+        top = fmaxf(fmaxf(top, s[0][2]), s[0][3]);
+        top = fmaxf(fmaxf(top, s[1][0]), s[1][1]);
+        return fmaxf(fmaxf(top, s[1][2]), s[1][3]);
+      };
+      // Raises a row's maximum to `top` (for the whole row: its four lanes agree).
+      auto raise = [&](Row& r, float top) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (top > r.m + kSlack) {
+          const float bias = kLift - top, by = r.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(bias - r.bias);
+          r.m = top;
+          r.bias = bias;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int tok = p0 + 16 * i + 4 * quad + e;
-                s[rt][i][e] *= f;
-                if (tok >= nan_from) s[rt][i][e] = __builtin_nanf("");
-                if (tok > seen[rt]) s[rt][i][e] = -INFINITY;
-              }
+          for (int d = 0; d < ND; ++d) r.o[d] *= by;
+          r.l *= by;
         }
-        u32x4 p[RT];
+      };
+      auto weights = [&](const f32x4 (&s)[2], float scale, float bias) {
+        float w[8];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          Row& r = row[rt];
-          float top = s[rt][0][0];
-#pragma unroll
-          for (int e = 1; e < 8; ++e) top = fmaxf(top, s[rt][e >> 2][e & 3]);
-          top *= ff;
-          if (__any(top > r.m + kSlack)) {
-            // raised for the whole row: its four lanes agree
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (top > r.m + kSlack) {
-              const float bias = kLift - top, by = r.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(bias - r.bias);
-              r.m = top;
-              r.bias = bias;
-#pragma unroll
-              for (int d = 0; d < ND; ++d) r.o[d] *= by;
-              r.l *= by;
-            }
-          }
-          float w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float y = s[rt][e >> 2][e & 3];
-            w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(y, ff, r.bias));
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[rt][e] = pack2<BF>(w[2 * e], w[2 * e + 1]);
-        }
-        const u32x4 ones{kOnes<BF>, kOnes<BF>, kOnes<BF>, kOnes<BF>};
+        for (int e = 0; e < 8; ++e) w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e >> 2][e & 3], scale, bias));
+        return u32x4{pack2<BF>(w[0], w[1]), pack2<BF>(w[2], w[3]), pack2<BF>(w[4], w[5]), pack2<BF>(w[6], w[7])};
+      };
+      const u32x4 ones{kOnes<BF>, kOnes<BF>, kOnes<BF>, kOnes<BF>};
+      auto values = [&](const char* v, const u32x4 (&p)[RT]) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
-        if (p0 + 31 > low) {
-          u32 odd = 0;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
-            odd |= odd_halves<BF>(y[0]) | odd_halves<BF>(y[1]) | odd_halves<BF>(y[2]) | odd_halves<BF>(y[3]);
-          }
-          if (__any(odd != 0)) {
-            u32x4 sees[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int tok = p0 + 16 * (e >> 1) + 4 * quad + 2 * (e & 1);
-                sees[rt][e] = (tok <= seen[rt] ? kOnes<BF> & 0xFFFFu : 0u) | (tok + 1 <= seen[rt] ? kOnes<BF> & 0xFFFF0000u : 0u);
-              }
-            odd_values(v, lane, p, sees, row);
-            continue;
-          }
-        }
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
           const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) row[rt].o[d] = mfma<BF>(y, p[rt], row[rt].o[d]);
         }
+      };
+      // Tiles that every row of the item sees whole: the next tile's scores are computed beside this one's probabilities.
+      int whole_tiles = (len + row0 / G + 1) >> 5;
+      whole_tiles = f > 0.f && whole_tiles < t1 ? whole_tiles : (f > 0.f ? t1 : t0);
+      if (t < whole_tiles) {
+        f32x4 s[RT][2], ahead[RT][2];
+        bool poisoned = false;
+        if (t + STAGES - 2 < t1) wait_loads<LOADS * (STAGES - 2)>();
+        else wait_loads<0>();
+        barrier();
+        scores(lds, s);
+        for (; t < whole_tiles; ++t) {
+          advance(std::integral_constant<int, 1>{});
+          poisoned = poisoned || nan_from != kNone;
+          const char* v = lds + slot * STAGE + HALF;
+          slot = slot + 1 == STAGES ? 0 : slot + 1;
+          if (!live) continue;
+          float top[RT];
+          bool raised = false;
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = highest(s[rt]) * f;
+            raised = raised || top[rt] > row[rt].m + kSlack;
+          }
+          if (__any(raised)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) raise(row[rt], top[rt]);
+          }
+          scores(lds + slot * STAGE, ahead);
+          u32x4 p[RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) p[rt] = weights(s[rt], f, row[rt].bias);
+          values(v, p);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            s[rt][0] = ahead[rt][0];
+            s[rt][1] = ahead[rt][1];
+          }
+        }
+        if (poisoned) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) row[rt].l = f32x4{} + __builtin_nanf("");
+        }
+      }
+      for (; t < t1; ++t) {
+        advance(std::integral_constant<int, 0>{});
+        const char* k = lds + slot * STAGE;
+        const char* v = k + HALF;
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        const int p0 = t * 32;
+        if (!live || p0 > high) continue;
+        f32x4 s[RT][2];
+        scores(k, s);
+        // scaled here, so that what a row does not see can be left out whatever the scale
+        u32x4 p[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = p0 + 16 * i + 4 * quad + e;
+              s[rt][i][e] *= f;
+              if (tok >= nan_from) s[rt][i][e] = __builtin_nanf("");
+              if (tok > seen[rt]) s[rt][i][e] = -INFINITY;
+            }
+          const float top = highest(s[rt]);
+          if (__any(top > row[rt].m + kSlack)) raise(row[rt], top);
+          p[rt] = weights(s[rt], 1.f, row[rt].bias);
+        }
+        u32 odd = 0;
+        if (p0 + 31 > low) {
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
+            odd |= odd_halves<BF>(y[0]) | odd_halves<BF>(y[1]) | odd_halves<BF>(y[2]) | odd_halves<BF>(y[3]);
+          }
+        }
+        if (__any(odd != 0)) {
+          u32x4 sees[RT];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = p0 + 16 * (e >> 1) + 4 * quad + 2 * (e & 1);
+              sees[rt][e] = (tok <= seen[rt] ? kOnes<BF> & 0xFFFFu : 0u) | (tok + 1 <= seen[rt] ? kOnes<BF> & 0xFFFF0000u : 0u);
+            }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
+          odd_values(v, lane, p, sees, row);
+        } else {
+          values(v, p);
+        }
+      }
+      if (stop < it.from + it.cost && which == 1 && tid == 0) {
+        // the item goes on in the next workgroups' shares
+        u32 last = wg + 1;
+        while (deal.start(last + 1) < it.from + it.cost) ++last;
+        a.joins[wg] = Join{last, first, rows, row0, head};
       }
       if (!live) continue;
 #pragma unroll
@@ -430,9 +527,9 @@ struct Kernel {
         if (r >= rows) continue;
         Row& w = row[rt];
         if (whole) {
-          const float inv = x.valid ? 1.f / w.l[0] : __builtin_nanf("");
-          const int tok = (row0 + r) / G, head = (int)it.h * G + (row0 + r - tok * G);
-          uint16_t* to = a.out + ((size_t)(x.first + tok) * a.c.heads * G + head) * D + 4 * quad;
+          const float inv = valid ? 1.f / w.l[0] : __builtin_nanf("");
+          const int tok = (row0 + r) / G, qh = head * G + (row0 + r - tok * G);
+          uint16_t* to = a.out + ((size_t)(first + tok) * a.c.heads * G + qh) * D + 4 * quad;
 #pragma unroll
           for (int d = 0; d < ND; ++d)
             *reinterpret_cast<uint2*>(to + 16 * d) = make_uint2(pack2<BF>(w.o[d][0] * inv, w.o[d][1] * inv),
@@ -445,7 +542,7 @@ struct Kernel {
             *reinterpret_cast<float4*>(to + 16 * d) = make_float4(w.o[d][0], w.o[d][1], w.o[d][2], w.o[d][3]);
           if (quad == 0) {
             a.stats[at_part * 2] = w.m == -INFINITY ? INFINITY : w.bias;
-            a.stats[at_part * 2 + 1] = x.valid ? w.l[0] : __builtin_nanf("");
+            a.stats[at_part * 2 + 1] = valid ? w.l[0] : __builtin_nanf("");
           }
         }
       }
@@ -454,7 +551,7 @@ struct Kernel {
 };
 
 template <int D, bool BF, int STAGES, int RT>
-__global__ __launch_bounds__(kTile / 16 / RT * 64, 2) void k_prompt_attention(Args a) {
+__global__ __launch_bounds__(kTile / 16 / RT * 64, D == 64 ? 3 : 2) void k_prompt_attention(Args a) {
   __shared__ __attribute__((aligned(1024))) char lds[STAGES * Kernel<D, BF, STAGES, RT>::STAGE];
   __shared__ Plan plan;
   Kernel<D, BF, STAGES, RT>::run(a, lds, plan);
@@ -465,27 +562,18 @@ __global__ __launch_bounds__(kTile / 16 / RT * 64, 2) void k_prompt_attention(Ar
 constexpr int kJoinRows = 16, kJoinWaves = 4;
 template <int D, bool BF>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args a) {
-  __shared__ Plan plan;
-  make_plan<kJoinWaves>(a, plan);
-  const Deal deal = deal_of(a, plan);
-  const u32 wg = blockIdx.x;
-  if (wg >= deal.groups) return;
-  const unsigned long long begin = deal.start(wg), end = deal.start(wg + 1);
-  if (end <= begin || end >= deal.total) return;
-  Slot x;
-  const Item it = item_at(a, plan, end, x);   // the item that the next workgroup begins with
-  if (it.from >= end || it.from < begin) return;
-  u32 last = wg;                              // the last workgroup that has some of it
-  while (deal.start(last + 1) < it.from + it.cost) ++last;
-  const int row0 = (int)it.j * kTile, rows = x.n * a.G - row0 < kTile ? x.n * a.G - row0 : kTile;
+  const u32 wg = blockIdx.x, took_part = a.joins[a.groups].last;
+  const Join j = a.joins[wg];
+  if (wg >= took_part || j.last <= wg) return;
+  const int H = a.c.heads;
   for (int u = threadIdx.x; u < kJoinRows * (D / 4); u += 64 * kJoinWaves) {
     const int r = blockIdx.y * kJoinRows + u / (D / 4), d = 4 * (u % (D / 4));
-    if (r >= rows) continue;
+    if (r >= j.rows) continue;
     float low = INFINITY;
-    for (u32 w = wg; w <= last; ++w) low = fminf(low, a.stats[(((size_t)w * 2 + (w == wg)) * kTile + r) * 2]);
+    for (u32 w = wg; w <= j.last; ++w) low = fminf(low, a.stats[(((size_t)w * 2 + (w == wg)) * kTile + r) * 2]);
     float sum = 0.f;
     f32x4 o{};
-    for (u32 w = wg; w <= last; ++w) {
+    for (u32 w = wg; w <= j.last; ++w) {
       const size_t at = ((size_t)w * 2 + (w == wg)) * kTile + r;
       const float bias = a.stats[at * 2], by = bias == INFINITY ? 0.f : __builtin_amdgcn_exp2f(low - bias);
       const float4 y = *reinterpret_cast<const float4*>(a.parts + at * D + d);
@@ -496,8 +584,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args 
       o[3] = __builtin_fmaf(y.w, by, o[3]);
     }
     const float inv = 1.f / sum;
-    const int tok = (row0 + r) / a.G, head = (int)it.h * a.G + (row0 + r - tok * a.G);
-    *reinterpret_cast<uint2*>(a.out + ((size_t)(x.first + tok) * a.c.heads * a.G + head) * D + d) =
+    const int tok = (j.row0 + r) / a.G, head = j.head * a.G + (j.row0 + r - tok * a.G);
+    *reinterpret_cast<uint2*>(a.out + ((size_t)(j.first + tok) * H * a.G + head) * D + d) =
         make_uint2(pack2<BF>(o[0] * inv, o[1] * inv), pack2<BF>(o[2] * inv, o[3] * inv));
   }
 }
@@ -508,29 +596,33 @@ void launch(const Args& a, hipStream_t stream) {
   hipLaunchKernelGGL((k_prompt_attention_join<D, BF>), dim3(a.groups, kTile / kJoinRows), dim3(64 * kJoinWaves), 0, stream, a);
 }
 
-constexpr int kMaxGroups = 512;
-// Two workgroups a compute unit, the same number on each XCD.
-int groups_of() {
-  const int n = svg_cu_count() * 2 / 8 * 8;
-  return n < 8 ? 8 : (n < kMaxGroups ? n : kMaxGroups);
+// Workgroups of a launch: as many as a compute unit holds at once, the same number on each XCD.
+constexpr int kMaxCus = 256;
+constexpr int per_cu(int dim) { return dim == 64 ? 3 : (dim == 128 ? 2 : 1); }
+int groups_of(int dim) {
+  const int cus = svg_cu_count(), n = (cus < kMaxCus ? cus : kMaxCus) * per_cu(dim) / 8 * 8;
+  return n < 8 ? 8 : n;
 }
-size_t stats_bytes(int groups) { return ((size_t)groups * 2 * kTile * 8 + 255) / 256 * 256; }
+size_t stats_at(int groups) { return ((size_t)(groups + 1) * sizeof(Join) + 255) / 256 * 256; }
+size_t parts_at(int groups) { return stats_at(groups) + ((size_t)groups * 2 * kTile * 8 + 255) / 256 * 256; }
 
 }  // namespace
 
 uint64_t svg_prompt_attention_bytes(const svg_kv_cache& c) {
-  return stats_bytes(kMaxGroups) + (size_t)kMaxGroups * 2 * kTile * c.dim * 4;
+  const int groups = kMaxCus * per_cu(c.dim);
+  return parts_at(groups) + (size_t)groups * 2 * kTile * c.dim * 4;
 }
 
 hipError_t svg_launch_prompt_attention(const svg_kv_cache& c, int layer, const void* q, int64_t ld_q, int G, int n_rows,
                                        const int32_t* start, const int32_t* count, float scale, void* out, void* workspace,
                                        hipStream_t stream) {
-  const int groups = groups_of();
-  const Args a{c, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), start, count, static_cast<float*>(workspace),
-               reinterpret_cast<float*>(static_cast<char*>(workspace) + stats_bytes(groups)), ld_q, layer, G, n_rows, groups, scale};
+  const int groups = groups_of(c.dim);
+  char* ws = static_cast<char*>(workspace);
+  const Args a{c, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), start, count, reinterpret_cast<float*>(ws + stats_at(groups)),
+               reinterpret_cast<float*>(ws + parts_at(groups)), reinterpret_cast<Join*>(ws), ld_q, layer, G, n_rows, groups, scale};
   const bool bf = c.type == SVG_BF16;
   if (c.dim == 64) bf ? launch<64, true, 4, 2>(a, stream) : launch<64, false, 4, 2>(a, stream);
-  else if (c.dim == 128) bf ? launch<128, true, 3, 2>(a, stream) : launch<128, false, 3, 2>(a, stream);
-  else bf ? launch<256, true, 2, 1>(a, stream) : launch<256, false, 2, 1>(a, stream);
+  else if (c.dim == 128) bf ? launch<128, true, 4, 2>(a, stream) : launch<128, false, 4, 2>(a, stream);
+  else bf ? launch<256, true, 4, 1>(a, stream) : launch<256, false, 4, 1>(a, stream);
   return hipGetLastError();
 }
