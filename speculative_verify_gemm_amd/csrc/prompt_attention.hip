@@ -289,6 +289,8 @@ struct Kernel {
     const int shift = __builtin_ctz(a.c.page);
     const size_t page_bytes = (size_t)a.c.heads * a.c.page * D * 2;
     const int G = a.G;
+    static_assert(LOADS % 2 == 0 && HALF / 1024 == LOADS / 2 * WAVES, "a wave's pieces of the keys, then of the values");
+    const u32 piece_at = (u32)wave * 1024u + (u32)lane * 16u;
     while (at < end) {
       Slot x;
       const Item it = item_at(a, plan, at, x);
@@ -343,13 +345,10 @@ struct Kernel {
         const u32 mark = pages.at(p >> shift), page = mark & kOutside ? 0u : mark & ~kShared;
         const int from = mark & kOutside ? 0 : (mark & kShared ? len : kNone);
         const size_t off = (size_t)page * page_bytes + (size_t)(p & (a.c.page - 1)) * D * 2;
-        const u32 to = base + (u32)slot * STAGE;
+        const u32 to = base + (u32)slot * STAGE + wave * 1024u;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-          const int piece = wave + i * WAVES;
-          const bool key = piece * 1024 < HALF;
-          load_to_lds((key ? kl : vl) + off + (key ? piece * 1024 : piece * 1024 - HALF), lane * 16u, to + piece * 1024u);
-        }
+        for (int i = 0; i < LOADS; ++i)
+          load_to_lds((i < LOADS / 2 ? kl : vl) + off, piece_at + (u32)(i % (LOADS / 2)) * (WAVES * 1024u), to + (u32)i * (WAVES * 1024u));
         return from;
       };
       wait_loads<0>();
@@ -431,28 +430,62 @@ struct Kernel {
         else wait_loads<0>();
         barrier();
         scores(lds, s);
+        float top[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) top[rt] = highest(s[rt]) * f;
         for (; t < whole_tiles; ++t) {
           advance(std::integral_constant<int, 1>{});
           poisoned = poisoned || nan_from != kNone;
           const char* v = lds + slot * STAGE + HALF;
           slot = slot + 1 == STAGES ? 0 : slot + 1;
           if (!live) continue;
-          float top[RT];
+          // Fragments are read ahead of the products that need them: the values' first ones before all else.
+          constexpr int AHEAD = 3;
+          u32x4 y[AHEAD + 1], kf[2][2];
+          auto read_v = [&](int d) { y[d % (AHEAD + 1)] = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16); };
+          const char* k = lds + slot * STAGE + lane * 16;
+          auto read_k = [&](int c) {
+            kf[c & 1][0] = *reinterpret_cast<const u32x4*>(k + c * 1024);
+            kf[c & 1][1] = *reinterpret_cast<const u32x4*>(k + (NC + c) * 1024);
+          };
+          read_k(0);
+#pragma unroll
+          for (int d = 0; d < AHEAD; ++d) read_v(d);
           bool raised = false;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            top[rt] = highest(s[rt]) * f;
-            raised = raised || top[rt] > row[rt].m + kSlack;
-          }
+          for (int rt = 0; rt < RT; ++rt) raised = raised || top[rt] > row[rt].m + kSlack;
           if (__any(raised)) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) raise(row[rt], top[rt]);
           }
-          scores(lds + slot * STAGE, ahead);
           u32x4 p[RT];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) p[rt] = weights(s[rt], f, row[rt].bias);
-          values(v, p);
+          for (int c = 0; c < NC; ++c) {
+            if (c + 1 < NC) read_k(c + 1);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) ahead[rt][i] = mfma<BF>(kf[c & 1][i], q[rt][c], c == 0 ? f32x4{} : ahead[rt][i]);
+            // this share of the probabilities, pairs of scores
+#pragma unroll
+            for (int n = c * 4 * RT / NC; n < (c + 1) * 4 * RT / NC; ++n) {
+              const int rt = n / 4, e = n % 4;
+              p[rt][e] = pack2<BF>(__builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][e >> 1][2 * (e & 1)], f, row[rt].bias)),
+                                   __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][e >> 1][2 * (e & 1) + 1], f, row[rt].bias)));
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int d = 0; d < ND; ++d) {
+            if (d + AHEAD < ND) read_v(d + AHEAD);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              if (d == 0) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
+              row[rt].o[d] = mfma<BF>(y[d % (AHEAD + 1)], p[rt], row[rt].o[d]);
+            }
+            if (d >= 1 && d <= RT) top[d - 1] = highest(ahead[d - 1]) * f;
+            __builtin_amdgcn_sched_barrier(0);
+          }
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
             s[rt][0] = ahead[rt][0];
