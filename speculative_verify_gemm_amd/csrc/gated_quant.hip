@@ -21,9 +21,32 @@ struct GateArgs {
   int M, K, type;
 };
 
+// exp(y) for -745 <= y <= 709 within 2^-51 of itself: y = n ln 2 + r (ln 2 in two parts), a polynomial in r (Chebyshev
+// interpolation of exp over |r| <= ln 2 / 2, off by 2^-56), the power of two put into the exponent.
+SVG_DEV double exp_f64(double y) {
+  const double n = rint(y * 1.4426950408889634);
+  const double r = __builtin_fma(n, -1.9082149292705877e-10, __builtin_fma(n, -0.69314718036912382, y));
+  double p = 2.51449546413054e-08;
+  p = __builtin_fma(p, r, 2.7633231742717875e-07);
+  p = __builtin_fma(p, r, 2.7557123950259445e-06);
+  p = __builtin_fma(p, r, 2.480148370245139e-05);
+  p = __builtin_fma(p, r, 0.00019841270034100182);
+  p = __builtin_fma(p, r, 0.0013888888954182422);
+  p = __builtin_fma(p, r, 0.008333333333240394);
+  p = __builtin_fma(p, r, 0.041666666666480195);
+  p = __builtin_fma(p, r, 0.16666666666666866);
+  p = __builtin_fma(p, r, 0.500000000000002);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+// x * g / (1 + exp(-g)), rounded once.  The exponential's argument stops where the result no longer changes.
 SVG_DEV float gated(float x, float g) {
-  const double d = (double)g;
-  return (float)((double)x * (d / (1.0 + exp(-d))));
+  const double d = 1.0 + exp_f64(fmax(fmin(-(double)g, 709.0), -745.0));
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return (float)((double)x * ((double)g * y));
 }
 
 // A launch has fewer than 2^32 work-items a dimension: rows go on in y.
@@ -68,6 +91,7 @@ void launch(const GateArgs& a, hipStream_t stream) {
   else if (nchunk <= 512) SVG_GATE(512, 1);
   else if (nchunk <= 1024) SVG_GATE(1024, 1);
   else if (nchunk <= 2048) SVG_GATE(1024, 2);
+  else if (nchunk <= 3072) SVG_GATE(1024, 3);
   else if (nchunk <= 4096) SVG_GATE(1024, 4);
   else SVG_GATE(1024, 8);
 #undef SVG_GATE

@@ -30,6 +30,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 128;                   // rows of an item
 constexpr int kMaxSlots = 1024;
@@ -340,15 +341,24 @@ struct Kernel {
       const char* vl = static_cast<const char*>(a.c.v) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)head * a.c.page * D * 2;
       // Requests a tile; the first of its positions that makes the rows which see it NaN (no page of the cache: all; the
       // step's own positions in a page that other slots hold: those).
+      const char *kp = nullptr, *vp = nullptr;  // the tile that was requested last
+      int from = kNone;
       auto fetch = [&](int t, int slot) {
         const int p = t * 32;
-        const u32 mark = pages.at(p >> shift), page = mark & kOutside ? 0u : mark & ~kShared;
-        const int from = mark & kOutside ? 0 : (mark & kShared ? len : kNone);
-        const size_t off = (size_t)page * page_bytes + (size_t)(p & (a.c.page - 1)) * D * 2;
+        if (t == t0 || (p & (a.c.page - 1)) == 0) {
+          const u32 mark = pages.at(p >> shift), page = mark & kOutside ? 0u : mark & ~kShared;
+          const size_t off = (size_t)page * page_bytes + (size_t)(p & (a.c.page - 1)) * D * 2;
+          kp = kl + off;
+          vp = vl + off;
+          from = mark & kOutside ? 0 : (mark & kShared ? len : kNone);
+        } else {
+          kp += 64 * D;
+          vp += 64 * D;
+        }
         const u32 to = base + (u32)slot * STAGE + wave * 1024u;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
-          load_to_lds((i < LOADS / 2 ? kl : vl) + off, piece_at + (u32)(i % (LOADS / 2)) * (WAVES * 1024u), to + (u32)i * (WAVES * 1024u));
+          load_to_lds(i < LOADS / 2 ? kp : vp, piece_at + (u32)(i % (LOADS / 2)) * (WAVES * 1024u), to + (u32)i * (WAVES * 1024u));
         return from;
       };
       wait_loads<0>();
@@ -360,28 +370,35 @@ struct Kernel {
       // What the loops' tops share: tile t + AHEAD has arrived for the whole workgroup, and tile t + STAGES - 1 is requested into the
       // place of tile t - 1, which nobody reads any more.
       int nan_from = kNone;
-      auto advance = [&](auto ahead) {
+      auto arrive = [&](auto ahead, auto more) {
         constexpr int LEFT = STAGES - 2 - decltype(ahead)::value;
-        if (t + STAGES - 2 < t1) wait_loads<LOADS * LEFT>();
+        if (decltype(more)::value || t + STAGES - 2 < t1) wait_loads<LOADS * LEFT>();
         else wait_loads<0>();
         barrier();
+      };
+      auto request = [&](auto more) {
         nan_from = odd_from[0];
 #pragma unroll
         for (int i = 0; i + 1 < STAGES - 1; ++i) odd_from[i] = odd_from[i + 1];
-        if (t + STAGES - 1 < t1) odd_from[STAGES - 2] = fetch(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
+        if (decltype(more)::value || t + STAGES - 1 < t1) odd_from[STAGES - 2] = fetch(t + STAGES - 1, slot == 0 ? STAGES - 1 : slot - 1);
       };
+      // Fragments are read AHEAD of the products that need them.
+      constexpr int AHEAD = 3;
       auto scores = [&](const char* k, f32x4 (&s)[RT][2]) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt][0] = s[rt][1] = f32x4{};
+        u32x4 kf[2][2];
+        auto read_k = [&](int c) {
+          kf[c & 1][0] = *reinterpret_cast<const u32x4*>(k + c * 1024 + lane * 16);
+          kf[c & 1][1] = *reinterpret_cast<const u32x4*>(k + (NC + c) * 1024 + lane * 16);
+        };
+        read_k(0);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-          const u32x4 k0 = *reinterpret_cast<const u32x4*>(k + c * 1024 + lane * 16);
-          const u32x4 k1 = *reinterpret_cast<const u32x4*>(k + (NC + c) * 1024 + lane * 16);
+          if (c + 1 < NC) read_k(c + 1);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            s[rt][0] = mfma<BF>(k0, q[rt][c], s[rt][0]);
-            s[rt][1] = mfma<BF>(k1, q[rt][c], s[rt][1]);
-          }
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[rt][i] = mfma<BF>(kf[c & 1][i], q[rt][c], c == 0 ? f32x4{} : s[rt][i]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
       auto highest = [&](const f32x4 (&s)[2]) {
@@ -411,13 +428,19 @@ struct Kernel {
       };
       const u32x4 ones{kOnes<BF>, kOnes<BF>, kOnes<BF>, kOnes<BF>};
       auto values = [&](const char* v, const u32x4 (&p)[RT]) {
+        u32x4 y[AHEAD + 1];
+        auto read_v = [&](int d) { y[d % (AHEAD + 1)] = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16); };
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
+        for (int d = 0; d < AHEAD; ++d) read_v(d);
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
-          const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
+          if (d + AHEAD < ND) read_v(d + AHEAD);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) row[rt].o[d] = mfma<BF>(y, p[rt], row[rt].o[d]);
+          for (int rt = 0; rt < RT; ++rt) {
+            if (d == 0) row[rt].l = mfma<BF>(ones, p[rt], row[rt].l);
+            row[rt].o[d] = mfma<BF>(y[d % (AHEAD + 1)], p[rt], row[rt].o[d]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
       // Tiles that every row of the item sees whole: the next tile's scores are computed beside this one's probabilities.
@@ -433,17 +456,14 @@ struct Kernel {
         float top[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) top[rt] = highest(s[rt]) * f;
-        for (; t < whole_tiles; ++t) {
-          advance(std::integral_constant<int, 1>{});
-          poisoned = poisoned || nan_from != kNone;
+        auto tile = [&](auto more) {
+          arrive(std::integral_constant<int, 1>{}, more);
           const char* v = lds + slot * STAGE + HALF;
-          slot = slot + 1 == STAGES ? 0 : slot + 1;
-          if (!live) continue;
-          // Fragments are read ahead of the products that need them: the values' first ones before all else.
-          constexpr int AHEAD = 3;
+          const int next = slot + 1 == STAGES ? 0 : slot + 1;
+          // the values' first fragments before all else
           u32x4 y[AHEAD + 1], kf[2][2];
           auto read_v = [&](int d) { y[d % (AHEAD + 1)] = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16); };
-          const char* k = lds + slot * STAGE + lane * 16;
+          const char* k = lds + next * STAGE + lane * 16;
           auto read_k = [&](int c) {
             kf[c & 1][0] = *reinterpret_cast<const u32x4*>(k + c * 1024);
             kf[c & 1][1] = *reinterpret_cast<const u32x4*>(k + (NC + c) * 1024);
@@ -451,6 +471,12 @@ struct Kernel {
           read_k(0);
 #pragma unroll
           for (int d = 0; d < AHEAD; ++d) read_v(d);
+          __builtin_amdgcn_sched_barrier(0);
+          request(more);
+          poisoned = poisoned || nan_from != kNone;
+          slot = next;
+          ++t;
+          if (!live) return;
           bool raised = false;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) raised = raised || top[rt] > row[rt].m + kSlack;
@@ -459,6 +485,7 @@ struct Kernel {
             for (int rt = 0; rt < RT; ++rt) raise(row[rt], top[rt]);
           }
           u32x4 p[RT];
+          __builtin_amdgcn_s_setprio(1);
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             if (c + 1 < NC) read_k(c + 1);
@@ -491,14 +518,18 @@ struct Kernel {
             s[rt][0] = ahead[rt][0];
             s[rt][1] = ahead[rt][1];
           }
-        }
+          __builtin_amdgcn_s_setprio(0);
+        };
+        while (t < whole_tiles && t + STAGES - 1 < t1) tile(std::true_type{});
+        while (t < whole_tiles) tile(std::false_type{});
         if (poisoned) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) row[rt].l = f32x4{} + __builtin_nanf("");
         }
       }
       for (; t < t1; ++t) {
-        advance(std::integral_constant<int, 0>{});
+        arrive(std::integral_constant<int, 0>{}, std::false_type{});
+        request(std::false_type{});
         const char* k = lds + slot * STAGE;
         const char* v = k + HALF;
         slot = slot + 1 == STAGES ? 0 : slot + 1;
@@ -507,31 +538,41 @@ struct Kernel {
         f32x4 s[RT][2];
         scores(k, s);
         // scaled here, so that what a row does not see can be left out whatever the scale
+        const bool part = p0 + 31 > low;  // (not all of the wave's rows see all of the tile)
         u32x4 p[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) s[rt][i] *= f;
+          if (part || nan_from != kNone) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = p0 + 16 * i + 4 * quad + e;
-              s[rt][i][e] *= f;
-              if (tok >= nan_from) s[rt][i][e] = __builtin_nanf("");
-              if (tok > seen[rt]) s[rt][i][e] = -INFINITY;
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int tok = p0 + 16 * i + 4 * quad + e;
+                if (tok >= nan_from) s[rt][i][e] = __builtin_nanf("");
+                if (tok > seen[rt]) s[rt][i][e] = -INFINITY;
+              }
+          }
           const float top = highest(s[rt]);
           if (__any(top > row[rt].m + kSlack)) raise(row[rt], top);
           p[rt] = weights(s[rt], 1.f, row[rt].bias);
         }
-        u32 odd = 0;
-        if (p0 + 31 > low) {
+        bool odd = false;
+        if (part) {
+          u16x2 largest{0, 0};  // of the values' patterns without their signs
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
             const u32x4 y = *reinterpret_cast<const u32x4*>(v + d * 1024 + lane * 16);
-            odd |= odd_halves<BF>(y[0]) | odd_halves<BF>(y[1]) | odd_halves<BF>(y[2]) | odd_halves<BF>(y[3]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              largest = __builtin_elementwise_max(largest, __builtin_bit_cast(u16x2, y[w] & 0x7FFF7FFFu));
+            if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
           }
+          constexpr unsigned short kInf = BF ? 0x7F80 : 0x7C00;
+          odd = largest[0] >= kInf || largest[1] >= kInf;
         }
-        if (__any(odd != 0)) {
+        if (__any(odd)) {
           u32x4 sees[RT];
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)

@@ -145,40 +145,34 @@ struct RopeArgs {
   float amplitude;
 };
 
-// N consecutive values (4 or 8) from value `at` on, as fp32; 16-byte aligned, or 8-byte for four of 16 bits.
-template <int N>
-SVG_DEV void load_row(const void* base, int type, size_t at, float (&v)[N]) {
-  if (type == SVG_F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+// N consecutive values (4 or 8) of a row as they lie in memory, and as fp32.
+template <int XT, int N>
+struct Raw {
+  static constexpr int WORDS = XT == SVG_F32 ? N : N / 2;
+  u32 w[WORDS];
+  SVG_DEV void load(const void* base, size_t at) {
+    const char* p = static_cast<const char*>(base) + at * (XT == SVG_F32 ? 4 : 2);
+    if constexpr (WORDS == 2) {
+      const uint2 t = *reinterpret_cast<const uint2*>(p);
+      w[0] = t.x;
+      w[1] = t.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 t = p[i];
-      v[4 * i] = t.x;
-      v[4 * i + 1] = t.y;
-      v[4 * i + 2] = t.z;
-      v[4 * i + 3] = t.w;
+      for (int i = 0; i < WORDS / 4; ++i) {
+        const uint4 t = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = t.x;
+        w[4 * i + 1] = t.y;
+        w[4 * i + 2] = t.z;
+        w[4 * i + 3] = t.w;
+      }
     }
-    return;
   }
-  u32 w[N / 2];
-  const uint16_t* p = static_cast<const uint16_t*>(base) + at;
-  if constexpr (N == 8) {
-    const uint4 t = *reinterpret_cast<const uint4*>(p);
-    w[0] = t.x;
-    w[1] = t.y;
-    w[2] = t.z;
-    w[3] = t.w;
-  } else {
-    const uint2 t = *reinterpret_cast<const uint2*>(p);
-    w[0] = t.x;
-    w[1] = t.y;
+  SVG_DEV float at(int i) const {
+    if constexpr (XT == SVG_F32) return __uint_as_float(w[i]);
+    else if constexpr (XT == SVG_F16) return half_at(w, i);
+    else return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (type == SVG_F16) v[i] = half_at(w, i);
-    else v[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-  }
-}
+};
 
 template <bool BF>
 SVG_DEV uint4 pack8(const float (&v)[8]) {
@@ -210,7 +204,7 @@ SVG_DEV float2 cos_sin(double angle, double amplitude) {
 }
 
 // A workgroup takes 32 rows and `heads_each` of the q_heads + 2 heads; the angles of its rows are computed once into LDS.
-template <bool BF>
+template <bool BF, int XT>
 __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
   extern __shared__ float2 turns[];  // [kRows][rot / 2]
   __shared__ int pos[kRows], place[kRows], quads[kRows], n_quads;
@@ -219,6 +213,7 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
   const int last = first + a.heads_each < all ? first + a.heads_each : all;
   const size_t head_size = (size_t)a.c.page * dim;
   const long places = (long)a.c.n_pages * a.c.page;
+  const int page_bits = __builtin_ctz(a.c.page);
   uint16_t* kl = static_cast<uint16_t*>(a.c.k) + (size_t)a.layer * a.c.n_pages * H * head_size;
   uint16_t* vl = static_cast<uint16_t*>(a.c.v) + (size_t)a.layer * a.c.n_pages * H * head_size;
   for (long r0 = (long)blockIdx.x * kRows; r0 < a.n_rows; r0 += (long)gridDim.x * kRows) {
@@ -250,70 +245,91 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
       }
       __syncthreads();
     }
-    // queries and keys: 16 values of a head at a time, with both values of each pair
+    // queries and keys: 16 values of a head at a time, with both values of each pair; several on their way at once
+    constexpr int U = XT == SVG_F32 ? 2 : 4;
     const int rotating = (last < a.q_heads + H ? last : a.q_heads + H) - first, units = kRows * per_row;
-    for (int x = tid; x < rotating * units; x += kThreads) {
-      const int h = first + x / units, u = x % units, row = u / per_row, c = u % per_row;
-      const bool key = h >= a.q_heads;
-      if (key ? place[row] < 0 : pos[row] < 0) continue;
-      const size_t r = (size_t)(r0 + row);
-      const void* base = key ? a.k : a.q;
-      const size_t from = key ? r * (size_t)a.ld_k + (size_t)(h - a.q_heads) * dim : r * (size_t)a.ld_q + (size_t)h * dim;
-      const bool turned = 16 * c < a.rot, halves = turned && !a.interleaved;
-      const int d0 = halves ? 8 * c : 16 * c, d1 = halves ? d0 + pairs : d0 + 8;
-      float lo[8], hi[8];
-      load_row<8>(base, a.x_type, from + d0, lo);
-      load_row<8>(base, a.x_type, from + d1, hi);
-      if (halves) {
-        const float2* t = turns + row * pairs + d0;
+    for (int x0 = tid; x0 < rotating * units; x0 += U * kThreads) {
+      Raw<XT, 8> raw[U][2];
+      int h[U], row[U], d0[U], d1[U];
+      bool live[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x0 = lo[i], x1 = hi[i];
-          lo[i] = __builtin_fmaf(x0, t[i].x, -(x1 * t[i].y));
-          hi[i] = __builtin_fmaf(x1, t[i].x, x0 * t[i].y);
-        }
-      } else if (turned) {
-        const float2* t = turns + row * pairs + 8 * c;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x0 = lo[2 * i], x1 = lo[2 * i + 1], y0 = hi[2 * i], y1 = hi[2 * i + 1];
-          lo[2 * i] = __builtin_fmaf(x0, t[i].x, -(x1 * t[i].y));
-          lo[2 * i + 1] = __builtin_fmaf(x1, t[i].x, x0 * t[i].y);
-          hi[2 * i] = __builtin_fmaf(y0, t[i + 4].x, -(y1 * t[i + 4].y));
-          hi[2 * i + 1] = __builtin_fmaf(y1, t[i + 4].x, y0 * t[i + 4].y);
-        }
+      for (int i = 0; i < U; ++i) {
+        const int x = x0 + i * kThreads, u = x % units, c = u % per_row;
+        h[i] = first + x / units;
+        row[i] = u / per_row;
+        const bool key = h[i] >= a.q_heads;
+        live[i] = x < rotating * units && (key ? place[row[i]] >= 0 : pos[row[i]] >= 0);
+        const bool halves = 16 * c < a.rot && !a.interleaved;
+        d0[i] = halves ? 8 * c : 16 * c;
+        d1[i] = halves ? d0[i] + pairs : d0[i] + 8;
+        if (!live[i]) continue;
+        const size_t r = (size_t)(r0 + row[i]);
+        const void* base = key ? a.k : a.q;
+        const size_t from = key ? r * (size_t)a.ld_k + (size_t)(h[i] - a.q_heads) * dim : r * (size_t)a.ld_q + (size_t)h[i] * dim;
+        raw[i][0].load(base, from + d0[i]);
+        raw[i][1].load(base, from + d1[i]);
       }
-      if (key) {
-        const int at = place[row], page = at / a.c.page, t = at % a.c.page;
-        uint16_t* to = kl + ((size_t)page * H + (h - a.q_heads)) * head_size;
-        *reinterpret_cast<uint4*>(to + kv_key_at(t, d0, dim)) = pack8<BF>(lo);
-        *reinterpret_cast<uint4*>(to + kv_key_at(t, d1, dim)) = pack8<BF>(hi);
-      } else {
-        const size_t to = (r * a.q_heads + h) * dim;
-        if (a.q_f32) {
-          float4* p0 = reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + to + d0);
-          float4* p1 = reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + to + d1);
-          p0[0] = make_float4(lo[0], lo[1], lo[2], lo[3]);
-          p0[1] = make_float4(lo[4], lo[5], lo[6], lo[7]);
-          p1[0] = make_float4(hi[0], hi[1], hi[2], hi[3]);
-          p1[1] = make_float4(hi[4], hi[5], hi[6], hi[7]);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (!live[i]) continue;
+        float lo[8], hi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lo[e] = raw[i][0].at(e);
+          hi[e] = raw[i][1].at(e);
+        }
+        if (!a.interleaved && d0[i] < pairs) {
+          const float2* t = turns + row[i] * pairs + d0[i];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x0 = lo[e], x1 = hi[e];
+            lo[e] = __builtin_fmaf(x0, t[e].x, -(x1 * t[e].y));
+            hi[e] = __builtin_fmaf(x1, t[e].x, x0 * t[e].y);
+          }
+        } else if (d0[i] < a.rot) {
+          const float2* t = turns + row[i] * pairs + d0[i] / 2;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = lo[2 * e], x1 = lo[2 * e + 1], y0 = hi[2 * e], y1 = hi[2 * e + 1];
+            lo[2 * e] = __builtin_fmaf(x0, t[e].x, -(x1 * t[e].y));
+            lo[2 * e + 1] = __builtin_fmaf(x1, t[e].x, x0 * t[e].y);
+            hi[2 * e] = __builtin_fmaf(y0, t[e + 4].x, -(y1 * t[e + 4].y));
+            hi[2 * e + 1] = __builtin_fmaf(y1, t[e + 4].x, y0 * t[e + 4].y);
+          }
+        }
+        if (h[i] >= a.q_heads) {
+          const int at = place[row[i]], page = at >> page_bits, t = at & (a.c.page - 1);
+          uint16_t* to = kl + ((size_t)page * H + (h[i] - a.q_heads)) * head_size;
+          *reinterpret_cast<uint4*>(to + kv_key_at(t, d0[i], dim)) = pack8<BF>(lo);
+          *reinterpret_cast<uint4*>(to + kv_key_at(t, d1[i], dim)) = pack8<BF>(hi);
         } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + to + d0) = pack8<BF>(lo);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + to + d1) = pack8<BF>(hi);
+          const size_t to = ((size_t)(r0 + row[i]) * a.q_heads + h[i]) * dim;
+          if (a.q_f32) {
+            float4* p0 = reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + to + d0[i]);
+            float4* p1 = reinterpret_cast<float4*>(static_cast<float*>(a.q_out) + to + d1[i]);
+            p0[0] = make_float4(lo[0], lo[1], lo[2], lo[3]);
+            p0[1] = make_float4(lo[4], lo[5], lo[6], lo[7]);
+            p1[0] = make_float4(hi[0], hi[1], hi[2], hi[3]);
+            p1[1] = make_float4(hi[4], hi[5], hi[6], hi[7]);
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + to + d0[i]) = pack8<BF>(lo);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + to + d1[i]) = pack8<BF>(hi);
+          }
         }
       }
     }
     // values: up to four rows that share 8-byte pieces, four values of a head at a time
-    const int from_v = first > a.q_heads + H ? first : a.q_heads + H, vheads = last - from_v, vunits = n_quads * (dim >> 2);
+    const int from_v = first > a.q_heads + H ? first : a.q_heads + H, vheads = last - from_v, quarter = dim >> 2;
+    const int vunits = n_quads * quarter;
     for (int x = tid; x < vheads * vunits; x += kThreads) {
-      const int h = from_v - a.q_heads - H + x / vunits, u = x % vunits, row = quads[u / (dim >> 2)], d = 4 * (u % (dim >> 2));
-      const int at = place[row], page = at / a.c.page, t = at % a.c.page;
-      float w[4][4];
+      const int h = from_v - a.q_heads - H + x / vunits, u = x % vunits, row = quads[u / quarter], d = 4 * (u % quarter);
+      const int at = place[row], page = at >> page_bits, t = at & (a.c.page - 1);
+      Raw<XT, 4> w[4];
       int n = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (n == j && (t & 3) + j < 4 && row + j < kRows && place[row + j] == at + j) {
-          load_row<4>(a.v, a.x_type, (size_t)(r0 + row + j) * (size_t)a.ld_v + (size_t)h * dim + d, w[j]);
+          w[j].load(a.v, (size_t)(r0 + row + j) * (size_t)a.ld_v + (size_t)h * dim + d);
           n = j + 1;
         }
       }
@@ -322,12 +338,12 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(RopeArgs a) {
       for (int e = 0; e < 4; ++e) {
         uint16_t* p = to + kv_value_at(t, d + e, dim);
         if (n == 4) {
-          *reinterpret_cast<uint2*>(p) = make_uint2(kv_round<BF>(w[0][e]) | (kv_round<BF>(w[1][e]) << 16),
-                                                    kv_round<BF>(w[2][e]) | (kv_round<BF>(w[3][e]) << 16));
+          *reinterpret_cast<uint2*>(p) = make_uint2(kv_round<BF>(w[0].at(e)) | (kv_round<BF>(w[1].at(e)) << 16),
+                                                    kv_round<BF>(w[2].at(e)) | (kv_round<BF>(w[3].at(e)) << 16));
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (j < n) p[j] = (uint16_t)kv_round<BF>(w[j][e]);
+            if (j < n) p[j] = (uint16_t)kv_round<BF>(w[j].at(e));
         }
       }
     }
@@ -361,7 +377,15 @@ hipError_t svg_launch_rope_append(const svg_kv_cache& c, int layer, const svg_ro
                    rope.rot, rope.interleaved, each, rope.amplitude};
   const dim3 grid(rows, (heads + each - 1) / each);
   const u32 lds = kRows * (u32)(rope.rot / 2) * sizeof(float2);
-  if (c.type == SVG_BF16) hipLaunchKernelGGL(k_rope_append<true>, grid, dim3(kThreads), lds, stream, a);
-  else hipLaunchKernelGGL(k_rope_append<false>, grid, dim3(kThreads), lds, stream, a);
+#define SVG_ROPE(BF)                                                                                             \
+  if (x_type == SVG_F32) hipLaunchKernelGGL((k_rope_append<BF, SVG_F32>), grid, dim3(kThreads), lds, stream, a); \
+  else if (x_type == SVG_F16) hipLaunchKernelGGL((k_rope_append<BF, SVG_F16>), grid, dim3(kThreads), lds, stream, a); \
+  else hipLaunchKernelGGL((k_rope_append<BF, SVG_BF16>), grid, dim3(kThreads), lds, stream, a)
+  if (c.type == SVG_BF16) {
+    SVG_ROPE(true);
+  } else {
+    SVG_ROPE(false);
+  }
+#undef SVG_ROPE
   return hipGetLastError();
 }
