@@ -4,6 +4,11 @@
 // u = x * gate / (1 + exp(-gate)) decides codes, so it is defined as one rounding of a 64-bit value and computed in
 // fp64 here (its error there, below 2^-50, moves that rounding once in 2^25 values); the rotation and the codes are
 // those of svg_act.h.  One workgroup owns a row and holds it in registers.
+//
+// Bound by vector instructions, about 63 a value with a gate, of which the gate is half and the rotation and the codes are the
+// rest (4099 rows of 12288, bf16 halves of one product: 109 us, 2.3 TB/s, units busy 70 to 85 %; a table of 128 powers of two, which
+// saves a third of the fp64 operations: 111 us); without a gate by memory (4099 rows of 4096, fp16: 18.6 us, 2.7 TB/s); few rows
+// by the chain of one load, a reduction and one store (40 rows of 4096: 4.1 us).
 #include "../../include/svgemm_prompt.h"
 #include "svg_act.h"
 #include "svg_internal.h"
@@ -82,12 +87,16 @@ __global__ __launch_bounds__(NT) void k_gated_quant(GateArgs a) {
   act_quant_loaded<CPT, StoreGlobal, B, true>(r, K, st, red);
 }
 
+// As many threads as the row has chunks, up to 1024; many short rows: a row for 256 threads, so that a compute unit has several at
+// different steps.  Measured (256 | 1024 threads): 4099 rows of 4096, fp16, no gate 18.6 | 25.3 us; 40 rows alike; longer rows gain
+// nothing (1000 rows of 12288, fp32 with a gate: 37.6 | 32.2 us).
 template <int B>
 void launch(const GateArgs& a, hipStream_t stream) {
   const int nchunk = a.K / 4;
   const dim3 grid(a.M < kRowsX ? a.M : kRowsX, (a.M + kRowsX - 1) / kRowsX);
 #define SVG_GATE(NT, CPT) hipLaunchKernelGGL((k_gated_quant<NT, CPT, B>), grid, dim3(NT), 0, stream, a)
   if (nchunk <= 256) SVG_GATE(256, 1);
+  else if (nchunk <= 1024 && a.M >= 512) SVG_GATE(256, 4);
   else if (nchunk <= 512) SVG_GATE(512, 1);
   else if (nchunk <= 1024) SVG_GATE(1024, 1);
   else if (nchunk <= 2048) SVG_GATE(1024, 2);

@@ -5,6 +5,7 @@ same name on the current stream of the tensors' device (or the stream given)."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -224,9 +225,10 @@ def prompt_attention(cache, layer, rows, q, out, workspace, scale=None, stream=N
 # ------------------------------------------------------------------ linears
 def _linear_args(xq, x_scale, N, y):
     dev = _device(xq, "xq")
-    if xq.dim() != 2:
+    shape = xq.shape
+    if len(shape) != 2:
         raise ValueError("xq must be [M, K]")
-    M, K = xq.shape
+    M, K = shape
     if x_scale.shape != (M,) or y.shape != (M, N):
         raise ValueError("y must be [M, N] and x_scale [M]")
     kind = _FLOATS.get(y.dtype)
@@ -235,33 +237,42 @@ def _linear_args(xq, x_scale, N, y):
     return dev, M, K, _tensor(xq, "xq", torch.int8, dev), _tensor(x_scale, "x_scale", torch.float32, dev), _tensor(y, "y", y.dtype, dev), kind
 
 
-def _storage(dev, N, K, f, group, wq, w_scale, w_zero):
-    from . import _check_storage
-    for name, t in (("wq", wq), ("w_scale", w_scale), ("w_zero", w_zero)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if N > 0:
-        _check_storage(N, K, f, group, wq, w_scale, w_zero)
+@functools.lru_cache(maxsize=4096)
+def _sizes(N, K, f, group):
+    """Values that the weight storage has at least: codes (bytes), scales, zeros (bytes of 4-bit ones, fp16 values)."""
+    from . import W4_Z4, weight_sizes
+    codes, scales, zeros = weight_sizes(N, K, f, group) if N > 0 else (0, 0, 0)
+    return codes, scales // 2, zeros if f == W4_Z4 else zeros // 2
+
+
+def _large(t, name, dtype, dev, least):
+    at = _tensor(t, name, dtype, dev)
+    if t.numel() < least:
+        raise ValueError(f"{name} is too small: need {least} values")
+    return at
 
 
 def w4a8_prompt_linear(xq, x_scale, wq, w_scale, w_zero, fmt, group, N, y, stream=None):
     """y[M, N] = dequantized (xq . W^T) for any number of rows: xq [M, K] in 32-row
     slab buffers, tiled W4 weights of N rows, y fp32, fp16 or bf16."""
-    from . import _fmt
-    f = _fmt(fmt)
+    from . import FORMATS, W4_Z4
+    f = FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
     dev, M, K, px, ps, py, kind = _linear_args(xq, x_scale, N, y)
-    _storage(dev, N, K, f, group, wq, w_scale, w_zero)
-    _call(_lib.w4a8_prompt_linear, dev, stream, px, ps, M, K, wq.data_ptr(), w_scale.data_ptr(),
-          None if w_zero is None else w_zero.data_ptr(), f, group, N, py, kind)
+    codes, scales, zeros = _sizes(N, K, f, group)
+    if w_zero is None:
+        raise ValueError("W4 formats need w_zero")
+    _call(_lib.w4a8_prompt_linear, dev, stream, px, ps, M, K, _large(wq, "wq", torch.uint8, dev, codes),
+          _large(w_scale, "w_scale", torch.float16, dev, scales),
+          _large(w_zero, "w_zero", torch.uint8 if f == W4_Z4 else torch.float16, dev, zeros), f, group, N, py, kind)
 
 
 def w8a8_prompt_linear(xq, x_scale, wq, w_scale, N, y, stream=None):
     """y[M, N] = dequantized (xq . W^T) for any number of rows: xq [M, K] in 32-row
     slab buffers, tiled W8 weights of N rows, y fp32, fp16 or bf16."""
-    from . import W8
     dev, M, K, px, ps, py, kind = _linear_args(xq, x_scale, N, y)
-    _storage(dev, N, K, W8, 0, wq, w_scale, None)
-    _call(_lib.w8a8_prompt_linear, dev, stream, px, ps, M, K, wq.data_ptr(), w_scale.data_ptr(), N, py, kind)
+    codes, scales, _ = _sizes(N, K, 2, 0)  # (SVG_W8_SYM)
+    _call(_lib.w8a8_prompt_linear, dev, stream, px, ps, M, K, _large(wq, "wq", torch.int8, dev, codes),
+          _large(w_scale, "w_scale", torch.float16, dev, scales), N, py, kind)
 
 
 def gated_quant_i8(x, gate, signs, xq, x_scale, block=32, stream=None):
