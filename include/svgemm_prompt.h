@@ -95,7 +95,8 @@ svg_status rope_append(const svg_kv_cache* cache, int layer, const svg_rope* rop
  *  q_heads    a multiple of heads: query head a reads key/value head a / (q_heads / heads); at most 4096.
  *  n_rows     rows of q and out.
  *  start, count  int32 [n_slots] as from kv_row_map: rows start[s] .. start[s] + count[s] - 1 are slot s's (a start
- *             outside 0 .. n_rows - 1 is no row, and rows past n_rows are not computed).  Rows of out that belong to no slot are left as they were.  No row belongs to two.
+ *             outside 0 .. n_rows - 1 is no row, and rows past n_rows are not computed).  Rows of out that belong to no slot
+ *             are left as they were.  No row belongs to two.
  *  scale      finite; the scores are scale * q . k.
  *  out        [n_rows][q_heads * dim] of the cache's type, 16-byte aligned.
  *  workspace  prompt_attention_workspace() bytes, 256-byte aligned; its contents need not be set or kept.  Calls that may
@@ -103,8 +104,8 @@ svg_status rope_append(const svg_kv_cache* cache, int layer, const svg_rope* rop
  *
  *  Row i of slot s: o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale * q . k_t), over the positions 0 .. len[s] + i.
  *  Scores, sums and accumulators are fp32; p enters the second product rounded to the cache's type (as v is held in it), so an
- *  output is off by its own rounding and by about as much again.  A probability below the type's smallest
- *  number, 2^-24 (fp16) of the row's largest so far or less, may be lost.
+ *  output is off by its own rounding and by about as much again.  Of an fp16 cache a p below 2^-33 of the
+ *  row's largest so far may be lost.
  *  Keys and values of tokens that a row does not see never reach it, whatever they are.  Of those it sees: a key that gives a
  *  NaN or +infinite score makes the row NaN (-infinity leaves the token out, and a row all of whose tokens are left out is NaN);
  *  a value that is not finite makes its own element of the row NaN or infinite, and no other.

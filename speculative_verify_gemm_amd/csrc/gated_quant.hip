@@ -100,7 +100,7 @@ void launch(const GateArgs& a, hipStream_t stream) {
   else if (nchunk <= 512) SVG_GATE(512, 1);
   else if (nchunk <= 1024) SVG_GATE(1024, 1);
   else if (nchunk <= 2048) SVG_GATE(1024, 2);
-  else if (nchunk <= 3072) SVG_GATE(1024, 3);
+  else if (nchunk <= 3 * 1024) SVG_GATE(1024, 3);
   else if (nchunk <= 4096) SVG_GATE(1024, 4);
   else SVG_GATE(1024, 8);
 #undef SVG_GATE

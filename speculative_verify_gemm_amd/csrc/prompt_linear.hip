@@ -1,4 +1,6 @@
 // y = x . W^T of many int8 activation rows against the tiled int8 or 4-bit weights, gfx950.
+#include <limits.h>
+
 #include <type_traits>
 
 #include "../../include/svgemm_prompt.h"
@@ -599,12 +601,14 @@ hipError_t launch_few(const Args& a, hipStream_t stream) {
 // Which of them: the one that is expected to take the least time, in 1/100 us, from the rounds of workgroups that its tiles
 // take and what a round takes for a step of K.  Measured (W8, us): ...
 enum { kFew, kMid, kBig };
+constexpr long kMaxGridY = 65535;  // a launch has no more workgroups in y
 template <class F>
 long cost_of(int way, int M, int N, int K) {
   const long cus = svg_cu_count(), steps = (K + F::kStep - 1) / F::kStep;
   const auto up = [](long x, long y) { return (x + y - 1) / y; };
   if (M == 0) return 0;
   if (way == kFew) {
+    if (up(M, 128) > kMaxGridY) return LONG_MAX;
     const long tm = up(M < 128 ? M : 128, 16);
     return up(up(N, 16) * up(M, 128), cus) * steps * (F::k4 ? 500 + 300 * tm : 250 + 120 * tm) / 100;
   }

@@ -210,7 +210,7 @@ def prompt_attention(cache, layer, rows, q, out, workspace, scale=None, stream=N
         raise ValueError("q must have n_rows rows")
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    key = ("prompt", heads, n)
+    key = ("prompt", heads, n > 0)
     need = cache._attn_bytes.get(key)
     if need is None:
         b = ctypes.c_uint64()

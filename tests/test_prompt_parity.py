@@ -550,6 +550,24 @@ def test_w8_rows_do_not_depend_on_the_number_of_rows():
         assert torch.equal(y, first[:M]), M
 
 
+def test_w8_rows_past_a_launch_of_few_columns():
+    """2^23 and more rows of few columns: more tiles of rows than a launch has workgroups in its second dimension."""
+    M, N, Kd = (1 << 23) + 131, 5, 32
+    C.say(f"w8a8_prompt_linear M={M} N={N} K={Kd}")
+    rng = np.random.default_rng(11)
+    wq, ws, _, s, w = weights(rng, N, Kd, "w8", 0)
+    g = torch.Generator(device=C.DEV).manual_seed(5)
+    x = torch.randint(-127, 128, (M, Kd), dtype=torch.int8, device=C.DEV, generator=g)  # (with 32 codes a row, slabs are rows)
+    xs = torch.rand(M, device=C.DEV, generator=g) * 1e-2 + 1e-4
+    y = torch.full((M, N), 7.0, device=C.DEV)
+    svg.w8a8_prompt_linear(x, xs, wq, ws, N, y)
+    for at in range(0, M, 1 << 21):
+        part = slice(at, min(at + (1 << 21), M))
+        ref = (x[part].double() @ torch.from_numpy(w.T.copy()).to(C.DEV).double()) * torch.from_numpy(s[:, 0]).to(C.DEV) * xs[part, None].double()
+        assert bool(((y[part].double() - ref).abs() <= 3 * E * ref.abs() * (1 + 1e-6)).all()), at
+
+
+
 # --------------------------------------------------------------- gated rows
 @pytest.mark.parametrize("M,Kd,block", [(1, 32, 32), (1, 4096, 64), (5, 96, 32), (31, 1024, 32), (33, 1088, 64), (64, 12288, 32), (70, 640, 64),
                                         (3, 32768, 64), (600, 2048, 32), (1030, 544, 32), (520, 5120, 32), (513, 12288, 64), (515, 9216, 32)])
