@@ -34,7 +34,10 @@ typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTile = 128;                   // rows of an item
 constexpr int kMaxSlots = 1024;
-constexpr int kItem = 4;                     // token tiles that starting and ending an item counts as
+// Token tiles that starting and ending an item counts as: finding it, the wait for its first tile, the tiles of the rows' own
+// tokens, which take half as long again, and the results' way out were 7 to 8 tiles of 1900 cycles (counted as 4 | 8: a prompt of
+// 4099 tokens, 32 heads of 128, 214 | 203 us, 24 slots of a step 140 | 137 us).
+constexpr int kItem = 8;
 constexpr int kLeast = 4;                    // token tiles of a workgroup at least
 
 template <bool BF>
@@ -93,6 +96,13 @@ struct Slot {
   SVG_DEV unsigned long long before(unsigned long long j) const { return base * j + (kTile / 64) * j * (j + 1); }
   SVG_DEV unsigned long long cost(u32 j) const { return base + (kTile / 32) * (unsigned long long)(j + 1); }
 };
+// Values that are the same for the wave, in scalar registers.
+SVG_DEV int uniform_i(int v) { return __builtin_amdgcn_readfirstlane(v); }
+SVG_DEV unsigned long long uniform_l(unsigned long long v) {
+  return (unsigned long long)(u32)uniform_i((int)(u32)(v >> 32)) << 32 | (u32)uniform_i((int)(u32)v);
+}
+
+template <bool UNIFORM>
 SVG_DEV Slot slot_of(const Args& a, int s) {
   Slot x;
   const int first = a.start[s], held = a.c.pages[s];
@@ -103,7 +113,13 @@ SVG_DEV Slot slot_of(const Args& a, int s) {
   x.first = first;
   x.n = n;
   x.valid = x.len >= 0 && held >= 0 && held <= a.c.width && (long)x.len + n <= (long)held * a.c.page;
-  x.items = (u32)(((long)n * a.G + kTile - 1) / kTile);
+  if (UNIFORM) {
+    x.first = uniform_i(x.first);
+    x.n = uniform_i(x.n);
+    x.len = uniform_i(x.len);
+    x.valid = uniform_i(x.valid) != 0;
+  }
+  x.items = (u32)(((long)x.n * a.G + kTile - 1) / kTile);
   x.base = (unsigned long long)a.G * ((x.valid ? (u32)x.len >> 5 : 0u) + kItem);
   return x;
 }
@@ -128,7 +144,7 @@ SVG_DEV void make_plan(const Args& a, Plan& p) {
     const int s = tid * EACH + i;
     c[i] = 0;
     if (s < S) {
-      const Slot x = slot_of(a, s);
+      const Slot x = slot_of<false>(a, s);
       c[i] = x.before(x.items) * (unsigned long long)a.c.heads;
     }
     sum += c[i];
@@ -163,10 +179,10 @@ struct Deal {
 };
 SVG_DEV Deal deal_of(const Args& a, const Plan& p) {
   Deal d;
-  d.total = p.cum[a.c.n_slots];
+  d.total = uniform_l(p.cum[a.c.n_slots]);
   const unsigned long long want = d.total / ((unsigned long long)a.G * (kItem + kLeast)) + 1;
   d.groups = (u32)(want < (unsigned long long)a.groups ? want : (unsigned long long)a.groups);
-  d.quot = d.total / d.groups;
+  d.quot = uniform_l(d.total / d.groups);
   d.rest = d.total - d.quot * d.groups;
   return d;
 }
@@ -181,11 +197,12 @@ SVG_DEV Item item_at(const Args& a, const Plan& p, unsigned long long at, Slot& 
   int s = 0;
   for (int step = kMaxSlots / 2; step > 0; step >>= 1)
     if (s + step <= a.c.n_slots - 1 && p.cum[s + step] <= at) s += step;  // the last slot that begins at or before
-  x = slot_of(a, s);
-  const unsigned long long head = x.before(x.items), in = at - p.cum[s];
+  s = uniform_i(s);
+  x = slot_of<true>(a, s);
+  const unsigned long long first = uniform_l(p.cum[s]), head = x.before(x.items), in = at - first;
   Item it;
   it.s = s;
-  it.h = (u32)(in / head);
+  it.h = (u32)uniform_i((int)(u32)(in / head));
   const unsigned long long rest = in - it.h * head;
   u32 lo = 0, hi = x.items;  // the last j with before(j) <= rest
   while (hi - lo > 1) {
@@ -193,13 +210,26 @@ SVG_DEV Item item_at(const Args& a, const Plan& p, unsigned long long at, Slot& 
     if (x.before(mid) <= rest) lo = mid;
     else hi = mid;
   }
+  lo = (u32)uniform_i((int)lo);
   it.j = lo;
-  it.from = p.cum[s] + it.h * head + x.before(lo);
+  it.from = first + it.h * head + x.before(lo);
   it.cost = x.cost(lo);
   return it;
 }
-SVG_DEV int uniform_i(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
+// The item behind it, which begins at cost `at`.
+SVG_DEV void next_item(const Args& a, const Plan& p, unsigned long long at, Item& it, Slot& x) {
+  if (it.j + 1 < x.items) {
+    ++it.j;
+  } else if (it.h + 1 < (u32)a.c.heads) {
+    ++it.h;
+    it.j = 0;
+  } else {
+    it = item_at(a, p, at, x);
+    return;
+  }
+  it.from = at;
+  it.cost = x.cost(it.j);
+}
 // Tokens of an item: what its last row sees; tiles of 32.
 SVG_DEV int tokens_of(const Args& a, const Slot& x, u32 j) {
   const int rows = x.n * a.G, end = (int)(j + 1) * kTile < rows ? (int)(j + 1) * kTile : rows;
@@ -229,7 +259,7 @@ struct Kernel {
   struct Pages {
     const int32_t *table, *refs;
     int first_own, n_pages, last, base;   // the entry of the first of the step's own positions; the last entry
-    u32 v;
+    u32 v, first;                         // first: entries 0 .. 63, kept for the slot's next item
     SVG_DEV void look(int entry) {
       base = entry;
       const int e = entry + (int)(threadIdx.x & 63u);
@@ -241,6 +271,10 @@ struct Kernel {
           if (refs != nullptr && e >= first_own && refs[page] > 1) v |= kShared;
         }
       }
+    }
+    SVG_DEV void rewind() {
+      base = 0;
+      v = first;
     }
     SVG_DEV u32 at(int entry) {
       if (entry - base >= 64) look(entry);
@@ -292,15 +326,21 @@ struct Kernel {
     const int G = a.G;
     static_assert(LOADS % 2 == 0 && HALF / 1024 == LOADS / 2 * WAVES, "a wave's pieces of the keys, then of the values");
     const u32 piece_at = (u32)wave * 1024u + (u32)lane * 16u;
-    while (at < end) {
-      Slot x;
-      const Item it = item_at(a, plan, at, x);
+    Slot x;
+    Item it;
+    Pages pages;
+    pages.refs = a.c.refs;
+    pages.n_pages = a.c.n_pages;
+    int pages_of = -1;  // the slot that `pages` is of
+    for (bool more = false; at < end; more = true) {
+      if (more) next_item(a, plan, at, it, x);
+      else it = item_at(a, plan, at, x);
       const unsigned long long stop = it.from + it.cost < end ? it.from + it.cost : end;
       const bool whole = at == it.from && stop == it.from + it.cost;
       const int which = at == it.from ? 1 : 0;  // the partial's place: an item's first share, or a later one
-      const int slot_no = uniform_i(it.s), head = uniform_i((int)it.h), len = uniform_i(x.len), first = uniform_i(x.first);
-      const int row0 = uniform_i((int)it.j) * kTile, all_rows = uniform_i(x.n) * G, rows = all_rows - row0 < kTile ? all_rows - row0 : kTile;
-      const bool valid = uniform_i(x.valid) != 0;
+      const int slot_no = it.s, head = (int)it.h, len = x.len, first = x.first;
+      const int row0 = (int)it.j * kTile, all_rows = x.n * G, rows = all_rows - row0 < kTile ? all_rows - row0 : kTile;
+      const bool valid = x.valid;
       const int tokens = uniform_i(valid ? tokens_of(a, x, it.j) : 0), tiles = (tokens + 31) >> 5;
       const int t0 = uniform_i(at == it.from ? 0 : tile_at(at - it.from, it, tiles));
       const int t1 = uniform_i(stop == it.from + it.cost ? tiles : tile_at(stop - it.from, it, tiles));
@@ -335,8 +375,16 @@ struct Kernel {
         row[rt].bias = 0.f;
       }
       // pages: position p lies in entry p >> shift of the slot's table row
-      Pages pages{a.c.table + (size_t)slot_no * a.c.width, a.c.refs, len >> shift, a.c.n_pages, (tokens - 1) >> shift, 0, 0};
-      if (t0 < t1) pages.look((t0 * 32) >> shift);
+      if (slot_no != pages_of) {
+        pages_of = slot_no;
+        pages.table = a.c.table + (size_t)slot_no * a.c.width;
+        pages.first_own = len >> shift;
+        pages.last = valid ? (len + x.n - 1) >> shift : -1;
+        pages.look(0);
+        pages.first = pages.v;
+      } else {
+        pages.rewind();
+      }
       const char* kl = static_cast<const char*>(a.c.k) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)head * a.c.page * D * 2;
       const char* vl = static_cast<const char*>(a.c.v) + (size_t)a.layer * a.c.n_pages * page_bytes + (size_t)head * a.c.page * D * 2;
       // Requests a tile; the first of its positions that makes the rows which see it NaN (no page of the cache: all; the
@@ -361,8 +409,7 @@ struct Kernel {
           load_to_lds(i < LOADS / 2 ? kp : vp, piece_at + (u32)(i % (LOADS / 2)) * (WAVES * 1024u), to + (u32)i * (WAVES * 1024u));
         return from;
       };
-      wait_loads<0>();
-      barrier();  // (the places of the item before are free)
+      barrier();  // (the places of the item before are free: its loads have arrived, and nobody reads them any more)
       int odd_from[STAGES];
 #pragma unroll
       for (int i = 0; i < STAGES - 1; ++i) odd_from[i] = t0 + i < t1 ? fetch(t0 + i, i) : kNone;
