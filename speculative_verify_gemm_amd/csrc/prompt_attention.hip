@@ -680,7 +680,9 @@ __global__ __launch_bounds__(kTile / 16 / RT * 64, D == 64 ? 3 : 2) void k_promp
 
 // Joins the partials of the item that begins in workgroup blockIdx.x's share and goes on behind it: its first share's partial
 // lies at place 1 of that workgroup, the others' at place 0 of the next ones.
-constexpr int kJoinRows = 16, kJoinWaves = 4;
+// Bound by the partials' bytes: 512 items of 128 rows of 128 values, 84 MB, 15 us; 256 of 256 values, 12 us (one partial after the
+// other, 16 rows a workgroup: 16 us each).
+constexpr int kJoinRows = 8, kJoinWaves = 4;
 template <int D, bool BF>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args a) {
   const u32 wg = blockIdx.x, took_part = a.joins[a.groups].last;
@@ -690,19 +692,30 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args 
   for (int u = threadIdx.x; u < kJoinRows * (D / 4); u += 64 * kJoinWaves) {
     const int r = blockIdx.y * kJoinRows + u / (D / 4), d = 4 * (u % (D / 4));
     if (r >= j.rows) continue;
-    float low = INFINITY;
-    for (u32 w = wg; w <= j.last; ++w) low = fminf(low, a.stats[(((size_t)w * 2 + (w == wg)) * kTile + r) * 2]);
-    float sum = 0.f;
+    // the weights go by the smallest bias so far; two partials on their way at once
+    float low = INFINITY, sum = 0.f;
     f32x4 o{};
-    for (u32 w = wg; w <= j.last; ++w) {
-      const size_t at = ((size_t)w * 2 + (w == wg)) * kTile + r;
-      const float bias = a.stats[at * 2], by = bias == INFINITY ? 0.f : __builtin_amdgcn_exp2f(low - bias);
-      const float4 y = *reinterpret_cast<const float4*>(a.parts + at * D + d);
-      sum = __builtin_fmaf(a.stats[at * 2 + 1], by, sum);
-      o[0] = __builtin_fmaf(y.x, by, o[0]);
-      o[1] = __builtin_fmaf(y.y, by, o[1]);
-      o[2] = __builtin_fmaf(y.z, by, o[2]);
-      o[3] = __builtin_fmaf(y.w, by, o[3]);
+    for (u32 w = wg; w <= j.last; w += 2) {
+      const bool two = w < j.last;
+      const size_t at0 = ((size_t)w * 2 + (w == wg)) * kTile + r, at1 = two ? (size_t)(w + 1) * 2 * kTile + r : at0;
+      const float2 s0 = *reinterpret_cast<const float2*>(a.stats + at0 * 2), s1 = *reinterpret_cast<const float2*>(a.stats + at1 * 2);
+      const float4 y0 = *reinterpret_cast<const float4*>(a.parts + at0 * D + d), y1 = *reinterpret_cast<const float4*>(a.parts + at1 * D + d);
+      const float bias1 = two ? s1.x : INFINITY, next = fminf(low, fminf(s0.x, bias1));
+      const float by = low == INFINITY ? 0.f : __builtin_amdgcn_exp2f(next - low);
+      const float by0 = s0.x == INFINITY ? 0.f : __builtin_amdgcn_exp2f(next - s0.x), by1 = bias1 == INFINITY ? 0.f : __builtin_amdgcn_exp2f(next - bias1);
+      low = next;
+      sum = __builtin_fmaf(s0.y, by0, sum * by);
+      o[0] = __builtin_fmaf(y0.x, by0, o[0] * by);
+      o[1] = __builtin_fmaf(y0.y, by0, o[1] * by);
+      o[2] = __builtin_fmaf(y0.z, by0, o[2] * by);
+      o[3] = __builtin_fmaf(y0.w, by0, o[3] * by);
+      if (two) {
+        sum = __builtin_fmaf(s1.y, by1, sum);
+        o[0] = __builtin_fmaf(y1.x, by1, o[0]);
+        o[1] = __builtin_fmaf(y1.y, by1, o[1]);
+        o[2] = __builtin_fmaf(y1.z, by1, o[2]);
+        o[3] = __builtin_fmaf(y1.w, by1, o[3]);
+      }
     }
     const float inv = 1.f / sum;
     const int tok = (j.row0 + r) / a.G, head = j.head * a.G + (j.row0 + r - tok * a.G);
