@@ -13,6 +13,17 @@
 // lane column, four consecutive tokens in each lane, which is the order the values are stored in, so the probabilities
 // go from the first product's result registers into the second's operand registers: O^T += V^T P^T.
 // The sum of the probabilities is a product as well, with ones: it adds up what the second product sees.
+//
+// Tiles.  32 tokens' keys and values go straight into a ring of four places in LDS.  While every row sees a whole tile, a wave
+// computes the next tile's scores beside this one's probabilities (v_mfma and v_exp from one wave side by side), reads fragments
+// ahead of their products, and does not touch masks; the tiles of the rows' own tokens go one by one.  A running maximum is
+// raised only when a score passes it by 2^kSlack.
+//
+// Bound by the matrix units and the vector instructions of the exponential together.  1000 rows behind 30001 tokens, 8 heads of 128
+// for 32, bf16: 495 us, 1.01 PFLOP/s (a library product of 8192^3: 1.46), matrix units busy 48 % and vector units 41 % of the
+// cycles; heads of 256 0.94 PFLOP/s; heads of 64 0.79, where the exponentials weigh twice as much.  Shorter items pay for their
+// starts, the rows' own tokens and the partials: a prompt of 4099 tokens, 32 heads of 128: 200 us, 0.69 PFLOP/s, 15 of them the join.
+// Heads of 256 have 16 rows a wave: 32 rows fill the registers with one wave a SIMD and take as long (step 148 | 144 us).
 #include <math.h>
 
 #include <type_traits>

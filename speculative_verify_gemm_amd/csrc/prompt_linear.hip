@@ -1,4 +1,21 @@
 // y = x . W^T of many int8 activation rows against the tiled int8 or 4-bit weights, gfx950.
+//
+//   W8: y[m][n] = sx[m] s[n] S[m][n],  W4: y[m][n] = sx[m] sum_g s[n][g] S_g[m][n],
+// S an int32 sum of products of codes (exact: at most 127^2 K, 127 * 15 * group), from v_mfma_i32_16x16x64_i8; the rest fp32.
+//
+// Three kernels, one rule between them (launch_best):
+//  big   256 x 256 outputs, one workgroup of 8 waves a compute unit (W8): a step of 64 values of K brings 32 KiB for 2 x 256 x
+//        256 x 64 operations, so that loads, LDS reads and products each take about the same time.  8192^3: 2468 TOP/s.
+//  mid   128 x 128 outputs, two workgroups a compute unit: for fewer tiles, and for 4-bit weights.
+//  few   16 columns and up to 128 rows, 8 waves that share K and add their sums up in LDS: bound by the weights' bytes.
+// big and mid go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
+// loads behind it, and neither the ring nor the products stop between tiles.  Stores are counted too, so they are not waited for.
+//
+// What bounds them.  W8 at 4099 x 24576 x 4096: 367 us in big and 15 in few for the last 3 rows, 2.25 POP/s, next to the 2.25 of a
+// library product of 4096 rows; the loads alone and the products alone each take about nine tenths of it.  W4 at 1001 x 4096 x
+// 12288: 107 us, 0.94 POP/s, bound by vector instructions: two for every four results of a product and group (the conversion and
+// the fused product-sum) and 45 a step to unpack a fragment; without the sums 97 us, without the unpacking 107, without loads 100.
+// Converting by adding 1.5 * 2^23 in the matrix unit instead takes as many instructions and the same time.
 #include <limits.h>
 
 #include <type_traits>
@@ -599,7 +616,11 @@ hipError_t launch_few(const Args& a, hipStream_t stream) {
 }
 
 // Which of them: the one that is expected to take the least time, in 1/100 us, from the rounds of workgroups that its tiles
-// take and what a round takes for a step of K.  Measured (W8, us): ...
+// take and what a round takes for a step of K.  Measured, us (kernel alone; rows x columns x K):
+//   W8   few | mid    128 x 24576 x 4096: 46 | 33    256 x 4096 x 4096: 16.5 | 20.2    512 x 4096 x 4096: 31 | 21
+//        mid | big    512 x 4096 x 4096: 21 | 44     512 x 24576 x 4096: 56 | 53       2048 x 12288 x 4096: 113 | 109
+//                     4096 x 24576 x 4096: 448 | 369
+//   W4   few | mid    256 x 4096 x 4096: 21 | 36     128 x 24576 x 4096: 55 | 37
 enum { kFew, kMid, kBig };
 constexpr long kMaxGridY = 65535;  // a launch has no more workgroups in y
 template <class F>
