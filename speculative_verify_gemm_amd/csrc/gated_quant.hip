@@ -6,7 +6,7 @@
 // those of svg_act.h.  One workgroup owns a row and holds it in registers.
 //
 // Bound by vector instructions, about 63 a value with a gate, of which the gate is half and the rotation and the codes are the
-// rest (4099 rows of 12288, bf16 halves of one product: 109 us, 2.3 TB/s, units busy 70 to 85 %; a table of 128 powers of two, which
+// rest (4099 rows of 12288, bf16 halves of one product: 109 to 115 us, 2.3 TB/s, vector units busy 91 %; a table of 128 powers of two, which
 // saves a third of the fp64 operations: 111 us); without a gate by memory (4099 rows of 4096, fp16: 18.6 us, 2.7 TB/s); few rows
 // by the chain of one load, a reduction and one store (40 rows of 4096: 4.1 us).
 #include "../../include/svgemm_prompt.h"

@@ -20,7 +20,7 @@
 // raised only when a score passes it by 2^kSlack.
 //
 // Bound by the matrix units and the vector instructions of the exponential together.  1000 rows behind 30001 tokens, 8 heads of 128
-// for 32, bf16: 495 us, 1.01 PFLOP/s (a library product of 8192^3: 1.46), matrix units busy 48 % and vector units 41 % of the
+// for 32, bf16: 495 us, 1.01 PFLOP/s (a library product of 8192^3: 1.46), matrix units and vector units each busy 47 % of the
 // cycles; heads of 256 0.94 PFLOP/s; heads of 64 0.79, where the exponentials weigh twice as much.  Shorter items pay for their
 // starts, the rows' own tokens and the partials: a prompt of 4099 tokens, 32 heads of 128: 200 us, 0.69 PFLOP/s, 15 of them the join.
 // Heads of 256 have 16 rows a wave: 32 rows fill the registers with one wave a SIMD and take as long (step 148 | 144 us).
@@ -691,7 +691,7 @@ __global__ __launch_bounds__(kTile / 16 / RT * 64, D == 64 ? 3 : 2) void k_promp
 
 // Joins the partials of the item that begins in workgroup blockIdx.x's share and goes on behind it: its first share's partial
 // lies at place 1 of that workgroup, the others' at place 0 of the next ones.
-// Bound by the partials' bytes: 512 items of 128 rows of 128 values, 84 MB, 15 us; 256 of 256 values, 12 us (one partial after the
+// Bound by the partials' bytes: 512 workgroups' of 128 rows of 128 values, 77 MB, 15 us; 256 of 256 values, 61 MB, 12 us (one partial after the
 // other, 16 rows a workgroup: 16 us each).
 constexpr int kJoinRows = 8, kJoinWaves = 4;
 template <int D, bool BF>

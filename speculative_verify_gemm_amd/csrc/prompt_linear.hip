@@ -11,11 +11,12 @@
 // big and mid go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
 // loads behind it, and neither the ring nor the products stop between tiles.  Stores are counted too, so they are not waited for.
 //
-// What bounds them.  W8 at 4099 x 24576 x 4096: 367 us in big and 15 in few for the last 3 rows, 2.25 POP/s, next to the 2.25 of a
-// library product of 4096 rows; the loads alone and the products alone each take about nine tenths of it.  W4 at 1001 x 4096 x
-// 12288: 107 us, 0.94 POP/s, bound by vector instructions: two for every four results of a product and group (the conversion and
-// the fused product-sum) and 45 a step to unpack a fragment; without the sums 97 us, without the unpacking 107, without loads 100.
-// Converting by adding 1.5 * 2^23 in the matrix unit instead takes as many instructions and the same time.
+// What bounds them.  W8 at 4099 x 24576 x 4096: 380 us a call, 17 of them in few for the last 3 rows (a library product of 4096 rows:
+// 367); the loads alone and the products alone each take about nine tenths of it, matrix units busy 52 %.  W4 at 1001 x 4096 x
+// 12288: 108 us, 0.94 POP/s, bound by vector instructions (busy 64 %, matrix units 17 %): two for each result of a product and
+// group (the conversion and the fused product-sum) and 45 a step to unpack a fragment; without the sums 97 us, without the
+// unpacking 107, without loads 100.  Converting by adding 1.5 * 2^23 in the matrix unit instead takes as many instructions and the
+// same time.
 #include <limits.h>
 
 #include <type_traits>
