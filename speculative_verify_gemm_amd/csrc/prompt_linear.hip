@@ -3,12 +3,13 @@
 //   W8: y[m][n] = sx[m] s[n] S[m][n],  W4: y[m][n] = sx[m] sum_g s[n][g] S_g[m][n],
 // S an int32 sum of products of codes (exact: at most 127^2 K, 127 * 15 * group), from v_mfma_i32_16x16x64_i8; the rest fp32.
 //
-// Three kernels, one rule between them (launch_best):
+// Four ways, one rule between them (launch_best):
 //  big   256 x 256 outputs, one workgroup of 8 waves a compute unit (W8): a step of 64 values of K brings 32 KiB for 2 x 256 x
 //        256 x 64 operations, so that loads, LDS reads and products each take about the same time.  8192^3: 2468 TOP/s.
 //  mid   128 x 128 outputs, two workgroups a compute unit: for fewer tiles, and for 4-bit weights.
+//  small 64 x 64 outputs, four workgroups a compute unit: for fewer tiles than compute units.
 //  few   16 columns and up to 128 rows, 8 waves that share K and add their sums up in LDS: bound by the weights' bytes.
-// big and mid go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
+// big, mid and small go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
 // loads behind it, and neither the ring nor the products stop between tiles.  Stores are counted too, so they are not waited for.
 //
 // What bounds them.  W8 at 4099 x 24576 x 4096: 380 us a call, 17 of them in few for the last 3 rows (a library product of 4096 rows:
@@ -621,31 +622,54 @@ hipError_t launch_few(const Args& a, hipStream_t stream) {
 //   W8   few | mid    128 x 24576 x 4096: 46 | 33    256 x 4096 x 4096: 16.5 | 20.2    512 x 4096 x 4096: 31 | 21
 //        mid | big    512 x 4096 x 4096: 21 | 44     512 x 24576 x 4096: 56 | 53       2048 x 12288 x 4096: 113 | 109
 //                     4096 x 24576 x 4096: 448 | 369
-//   W4   few | mid    256 x 4096 x 4096: 21 | 36     128 x 24576 x 4096: 55 | 37
-enum { kFew, kMid, kBig };
+//        small | mid  512 x 4096 x 4096: 18 | 21      768 x 4096 x 4096: 23.5 | 21        small | few  128 x 12288 x 4096: 18 | 21
+//   W4   few | mid    256 x 4096 x 4096: 21 | 36      128 x 24576 x 4096: 55 | 37          (groups of 64)
+//        small | mid  512 x 4096 x 4096: 26.5 | 39    1024 x 4096 x 4096: 41 | 40          4096 x 24576 x 4096: 932 | 729
+//                     512 x 4096 x 4096 in groups of 32: 38 | 60, of 128: 24 | 34
+enum { kFew, kSmall, kMid, kBig };
 constexpr long kMaxGridY = 65535;  // a launch has no more workgroups in y
+// A step's cost: few, in a round of one workgroup a compute unit, for a workgroup and each 16 of its rows (1 / 10000 us); small
+// and mid, for 1, 2, .. workgroups on a compute unit.
+struct Cost {
+  long few, few_rows;
+  long small[4];
+  int mids;
+  long mid[2];
+};
+constexpr Cost kCostW8{250, 120, {23, 27, 35, 44}, 2, {33, 58}};
+constexpr Cost kCostW4[3] = {{950, 570, {84, 108, 143, 179}, 1, {177, 0}},   // groups of 32
+                             {500, 300, {64, 72, 93, 118}, 2, {114, 190}},   // 64
+                             {425, 255, {59, 65, 82, 102}, 2, {97, 164}}};   // 128
+template <class F>
+constexpr const Cost& costs() {
+  if constexpr (F::k4) return kCostW4[F::kGroup / 64];
+  else return kCostW8;
+}
 template <class F>
 long cost_of(int way, int M, int N, int K) {
+  constexpr const Cost& c = costs<F>();
   const long cus = svg_cu_count(), steps = (K + F::kStep - 1) / F::kStep;
   const auto up = [](long x, long y) { return (x + y - 1) / y; };
+  const auto rounds = [&](long tiles, const long* each, long n) {
+    const long rest = up(tiles % (n * cus), cus);
+    return steps * (tiles / (n * cus) * each[n - 1] + (rest > 0 ? each[rest - 1] : 0));
+  };
   if (M == 0) return 0;
   if (way == kFew) {
     if (up(M, 128) > kMaxGridY) return LONG_MAX;
     const long tm = up(M < 128 ? M : 128, 16);
-    return up(up(N, 16) * up(M, 128), cus) * steps * (F::k4 ? 500 + 300 * tm : 250 + 120 * tm) / 100;
+    return up(up(N, 16) * up(M, 128), cus) * steps * (c.few + c.few_rows * tm) / 100;
   }
-  if (way == kMid) {
-    const long t = up(M, 128) * up(N, 128), rest = t % (2 * cus);
-    const long one = F::k4 ? 114 : 33, two = F::k4 ? 190 : 58;
-    return steps * (two * (t / (2 * cus)) + (rest > cus ? two : (rest > 0 ? one : 0)));
-  }
+  if (way == kSmall) return rounds(up(M, 64) * up(N, 64), c.small, 4);
+  if (way == kMid) return rounds(up(M, 128) * up(N, 128), c.mid, c.mids);
   return steps * 86 * up(up(M, 256) * up(N, 256), cus);
 }
 template <class F>
 hipError_t launch_way(int way, const Args& a, hipStream_t stream) {
   if (way == kFew) return launch_few<F>(a, stream);
+  if (way == kSmall) return launch<F, 1, 4, 4, 1, 4>(a, stream);
   if constexpr (F::k4) {
-    return launch<F, 1, 8, 8, 1, F::kGroup == 32 ? 1 : 2>(a, stream);
+    return launch<F, 1, 8, 8, 1, costs<F>().mids>(a, stream);
   } else {
     if (way == kMid) return launch<F, 2, 4, 4, 2, 2>(a, stream);
     return launch<F, 2, 4, 8, 4, 1>(a, stream);
@@ -659,13 +683,16 @@ hipError_t launch_best(const Args& a, hipStream_t stream) {
     const long c = cost_of<F>(w, M, a.N, a.K);
     if (c < least) least = c, way = w;
   };
+  look(kSmall, a.M);
   look(kMid, a.M);
   if constexpr (!F::k4) {
     look(kBig, a.M);
     // the rows of whole large tiles, and the rest another way, in a launch of its own (3 us)
     const int main = a.M & ~255, rest = a.M - main;
     if (main > 0 && rest > 0) {
-      const int then = cost_of<F>(kFew, rest, a.N, a.K) <= cost_of<F>(kMid, rest, a.N, a.K) ? kFew : kMid;
+      int then = kFew;
+      for (const int w : {kSmall, kMid})
+        if (cost_of<F>(w, rest, a.N, a.K) < cost_of<F>(then, rest, a.N, a.K)) then = w;
       if (cost_of<F>(kBig, main, a.N, a.K) + cost_of<F>(then, rest, a.N, a.K) + 300 < least) {
         Args first = a, second = a;
         first.M = main;

@@ -302,6 +302,52 @@ def test_attention(lens, n, H, G, dim, page, kind):
     check_attention(c, kind, q[:, :H * G * dim].reshape(-1, H * G, dim), qd, start, count, layer=1)
 
 
+def test_attention_of_many_short_items():
+    """Shares of many items, which go over heads, slots and slots without rows."""
+    rng = np.random.default_rng(17)
+    lens, n = rng.integers(0, 120, 200).tolist(), rng.integers(0, 13, 200).tolist()
+    n[3:9], n[-1] = [0] * 6, 0
+    c = K.make(3, lens, max(n), H=8, dim=64, page=32)
+    fill(c, rng, "fp16")
+    q, qd = queries(rng, sum(n), 8, 64, "fp16")
+    check_attention(c, "fp16", q[:, :8 * 64].reshape(-1, 8, 64), qd, *packed(n))
+
+
+@pytest.mark.parametrize("lens,n,H,G,dim,page,kind", [([2100, 3300], [5000, 1200], 8, 4, 64, 32, "fp16"), ([4000], [2500], 8, 2, 128, 32, "bf16"),
+                                                      ([2500, 0], [1500, 700], 8, 2, 256, 32, "bf16")])
+def test_attention_of_long_items_of_one_slot(lens, n, H, G, dim, page, kind):
+    """Shares that go on from item to item of a slot whose table row is longer than a wave looks up at once; the reference in
+    64 bits on the device, with the oracle's formulas."""
+    C.say(f"prompt_attention lens={lens} n={n} H={H} G={G} dim={dim} page={page} {kind}")
+    rng = np.random.default_rng(dim)
+    c = K.make(dim, lens, max(n), H=H, dim=dim, page=page)
+    fill(c, rng, kind)
+    R, A = sum(n), H * G
+    qd = torch.from_numpy(rng.standard_normal((R, A, dim)).astype(np.float32)).to(C.DEV).to(TYPES[kind])
+    start, count = packed(n)
+    cache = K.to_library(svg, c, kind)
+    out = torch.full_like(qd, 7.0)
+    svg.prompt_attention(cache, 0, svg.RowMap(i32(start), i32(count), n_rows=R), qd, out, svg.prompt_attention_workspace(cache, A, R))
+    f64 = lambda t: t.to(C.DEV, torch.float64)  # noqa: E731
+    for s in range(len(n)):
+        at = np.arange(lens[s] + n[s])
+        pg = c["table"][s][at // page].astype(np.int64)
+        t, d = (at % page)[:, None], np.arange(dim)[None, :]
+        sees = torch.arange(len(at), device=C.DEV)[None, :] <= lens[s] + torch.arange(n[s], device=C.DEV)[:, None]
+        for a in range(0, A, 3):
+            h = a // G
+            Kt, V = (f64(torch.from_numpy(wide(kind)(c[x][0, pg, h][np.arange(len(at))[:, None], f(t, d, dim)])))
+                     for x, f in (("k", CO.key_at), ("v", CO.value_at)))
+            x = f64(qd[start[s]:start[s] + n[s], a])
+            w = Kt.T.contiguous()
+            p = torch.softmax((dim ** -0.5 * (x @ w)).masked_fill(~sees, -np.inf), 1)
+            ref = p @ V
+            size = torch.stack(((dim ** -0.5 * (x.abs() @ w.abs())).masked_fill(~sees, 0).amax(1),
+                                V.abs().amax(1).cummax(0).values[lens[s]:], (p @ V.abs()).amax(1)), 1)
+            tol = attention_bound(c, kind, host64(ref), host64(size), len(at))
+            assert np.all(np.abs(host64(out[start[s]:start[s] + n[s], a]) - host64(ref)) <= tol), (s, a)
+
+
 def test_attention_of_rows_in_any_order():
     """Slots whose rows lie apart, in another order, dense with unused rows between, past the end."""
     rng = np.random.default_rng(4)
@@ -517,6 +563,20 @@ def test_w4_linear(M, N, Kd, group, fmt):
     Kd = -(-Kd // group) * group
     C.say(f"w4a8_prompt_linear M={M} N={N} K={Kd} {fmt} g{group}")
     check_linear(M, N, Kd, fmt, group, ("fp32", "bf16", "fp16")[(M + N) % 3])
+
+
+@pytest.mark.parametrize("M,N,Kd", [(300, 4100, 32), (300, 4101, 192), (449, 4099, 1056), (130, 12290, 96)])
+def test_w8_linear_of_medium_sizes(M, N, Kd):
+    for y in ("fp32", "bf16"):
+        check_linear(M, N, Kd, "w8", 0, y)
+
+
+@pytest.mark.parametrize("fmt", ["w4_z16", "w4_z4"])
+@pytest.mark.parametrize("M,N,Kd,group", [(515, 4100, 32, 32), (260, 4099, 96, 32), (515, 4101, 64, 64), (321, 4112, 704, 64), (515, 4100, 128, 128),
+                                          (400, 4097, 1152, 128), (200, 8211, 576, 64)])
+def test_w4_linear_of_medium_sizes(M, N, Kd, group, fmt):
+    for y in ("fp32", "fp16"):
+        check_linear(M, N, Kd, fmt, group, y)
 
 
 def test_the_linears_of_both_kinds_agree():
