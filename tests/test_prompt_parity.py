@@ -579,6 +579,31 @@ def test_w4_linear_of_medium_sizes(M, N, Kd, group, fmt):
         check_linear(M, N, Kd, fmt, group, y)
 
 
+@pytest.mark.parametrize("M,N,Kd,fmt,group", [(1408, 12288, 1024, "w8", 0), (2561, 8200, 1056, "w8", 0), (1100, 8208, 1024, "w4_z16", 64),
+                                              (1300, 4112, 4096, "w4_z4", 128)])
+def test_linears_of_many_tiles(M, N, Kd, fmt, group):
+    """More tiles than a round of workgroups has, rows past whole large tiles; the reference in 64 bits on the device."""
+    C.say(f"prompt linear M={M} N={N} K={Kd} {fmt} group={group}")
+    rng = np.random.default_rng(M)
+    wq, ws, wz, s, w = weights(rng, N, Kd, fmt, group)
+    x = codes(rng, M, Kd)
+    xs = (rng.random(M) * 1e-2 + 1e-4).astype(np.float32)
+    y = torch.full((M, N), 7.0, device=C.DEV)
+    xq, xsd = C.to_dev(NO.slab_codes(x).reshape(M, Kd)), C.to_dev(xs)
+    if fmt == "w8":
+        svg.w8a8_prompt_linear(xq, xsd, wq, ws, N, y)
+    else:
+        svg.w4a8_prompt_linear(xq, xsd, wq, ws, wz, fmt, group, N, y)
+    f64 = lambda t: torch.from_numpy(np.ascontiguousarray(t)).to(C.DEV).double()  # noqa: E731
+    ng, ref, size = s.shape[1], 0, 0
+    for g in range(ng):
+        k = slice(g * (Kd // ng), (g + 1) * (Kd // ng))
+        part = (f64(x[:, k]) @ f64(w[:, k].T)) * f64(s[:, g]) * f64(xs)[:, None]
+        ref, size = ref + part, size + part.abs()
+    tol = (3 if fmt == "w8" else ng + 2) * E * size * (1 + 1e-6)
+    assert bool(((y.double() - ref).abs() <= tol).all())
+
+
 def test_the_linears_of_both_kinds_agree():
     """The prompt linear on the rows of a verify batch: the verify linear's results."""
     rng = np.random.default_rng(3)
