@@ -75,6 +75,12 @@ SVG_DEV u32 odd_halves(u32 w) {
 // A probability is at most 2^kTop: the running maximum is raised when a score passes it by kSlack, and everything is lifted by
 // kTop - kSlack, so that small ones stay above the smallest number of fp16.
 constexpr float kTop = 15.f, kSlack = 7.f, kLift = kTop - kSlack;
+// A probability is 2^(f s + bias), bias = kLift - m: one operation, and one rounding, since m is a whole number of 1 / kGrid up to
+// kFar.  Beyond, the product inside that operation and the rounded one that m came from would differ by 2^-11 and more (from 2^24 on by
+// whole numbers, and kLift - m loses kLift), which fp16 has no room for: there it is 2^((f s - m) + kLift) with each step rounded, 2^kLift
+// where s is the maximum, whatever its size.  Such rows cost the others a branch in the step that raises maxima (a prompt of 4099
+// tokens 198 -> 201 us, 1000 rows behind 30001 495 -> 499; a clamp of every probability costs the second 4 %).
+constexpr float kFar = 16384.f, kGrid = 256.f;
 
 // What the second launch has to know of an item that begins in a workgroup's share and does not end there.
 struct Join {
@@ -87,7 +93,7 @@ struct Args {
   const uint16_t* q;
   uint16_t* out;
   const int32_t *start, *count;
-  float* stats;   // [groups][2][kTile] (bias, sum); the bias is infinite where no token was seen
+  float* stats;   // [groups][2][kTile] (minus the maximum, sum): infinite where no token was seen
   float* parts;   // [groups][2][kTile][dim]
   Join* joins;    // [groups + 1]: the last one's `last` is the number of workgroups that took part
   long ld_q;
@@ -260,7 +266,10 @@ struct Kernel {
   struct Row {
     f32x4 o[ND];
     f32x4 l;
-    float m, bias;   // the maximum that the row's exponents go by (-infinity: no token yet), and what is added to them
+    float limit;     // the score from which the maximum m is raised: m + kSlack; -infinity without a token, and beyond kFar
+    float bias;      // what is added to the exponents: kLift - m; kLift beyond kFar, where m is kept in LDS (`far`)
+    SVG_DEV bool beyond() const { return limit == -INFINITY && bias != 0.f; }
+    SVG_DEV float m(const float* far) const { return limit != -INFINITY ? limit - kSlack : (bias != 0.f ? *far : -INFINITY); }
   };
 
   // The pages of a slot's table row, 64 entries at a time: entry base + l in lane l (reading them one by one would wait for
@@ -316,7 +325,7 @@ struct Kernel {
     }
   }
 
-  SVG_DEV static void run(const Args& a, char* lds, Plan& plan) {
+  SVG_DEV static void run(const Args& a, char* lds, Plan& plan, float* far_all) {
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform_i(tid >> 6), col = lane & 15, quad = lane >> 4;
     make_plan<WAVES>(a, plan);
     const Deal deal = deal_of(a, plan);
@@ -332,6 +341,7 @@ struct Kernel {
     const unsigned long long end = deal.start(wg + 1);
     const u32 base = lds_at(lds);
     const float f = a.scale * 1.4426950408889634f;
+    float* const far = far_all + tid % 64 + wave * (64 * RT);
     const int shift = __builtin_ctz(a.c.page);
     const size_t page_bytes = (size_t)a.c.heads * a.c.page * D * 2;
     const int G = a.G;
@@ -382,7 +392,7 @@ struct Kernel {
 #pragma unroll
         for (int d = 0; d < ND; ++d) row[rt].o[d] = f32x4{};
         row[rt].l = f32x4{};
-        row[rt].m = -INFINITY;
+        row[rt].limit = -INFINITY;
         row[rt].bias = 0.f;
       }
       // pages: position p lies in entry p >> shift of the slot's table row
@@ -466,17 +476,28 @@ struct Kernel {
         return fmaxf(fmaxf(top, s[1][2]), s[1][3]);
       };
       // Raises a row's maximum to `top` (for the whole row: its four lanes agree).
-      auto raise = [&](Row& r, float top) {
+      auto raise = [&](Row& r, float top, float* far) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        if (top > r.m + kSlack) {
-          const float bias = kLift - top, by = r.m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(bias - r.bias);
-          r.m = top;
-          r.bias = bias;
+        const float before = r.m(far);
+        if (top - before > kSlack) {
+          const bool beyond = fabsf(top) > kFar;
+          const float m = beyond ? top : floorf(top * kGrid) * (1.f / kGrid);
+          const float by = before == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(before - m);
+          r.limit = beyond ? -INFINITY : m + kSlack;
+          r.bias = beyond ? kLift : kLift - m;
+          if (beyond) *far = m;
 #pragma unroll
           for (int d = 0; d < ND; ++d) r.o[d] *= by;
           r.l *= by;
         }
+      };
+      // Scores s of a row beyond kFar less its maximum, in the unit that they come in (s * unit are the exponents).
+      auto nearer = [&](const Row& r, f32x4 (&s)[2], float unit, float back, const float* far) {
+        if (!r.beyond()) return;
+        const float m = *far;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] = (s[e >> 2][e & 3] * unit - m) * back;
       };
       auto weights = [&](const f32x4 (&s)[2], float scale, float bias) {
         float w[8];
@@ -537,10 +558,13 @@ struct Kernel {
           if (!live) return;
           bool raised = false;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) raised = raised || top[rt] > row[rt].m + kSlack;
+          for (int rt = 0; rt < RT; ++rt) raised = raised || top[rt] > row[rt].limit;
           if (__any(raised)) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) raise(row[rt], top[rt]);
+            for (int rt = 0; rt < RT; ++rt) {
+              raise(row[rt], top[rt], far + 64 * rt);
+              if (__builtin_expect(__any(row[rt].beyond()), false)) nearer(row[rt], s[rt], f, 1.f / f, far + 64 * rt);
+            }
           }
           u32x4 p[RT];
           __builtin_amdgcn_s_setprio(1);
@@ -613,7 +637,10 @@ struct Kernel {
               }
           }
           const float top = highest(s[rt]);
-          if (__any(top > row[rt].m + kSlack)) raise(row[rt], top);
+          if (__any(top > row[rt].limit)) {
+            raise(row[rt], top, far + 64 * rt);
+            if (__builtin_expect(__any(row[rt].beyond()), false)) nearer(row[rt], s[rt], 1.f, 1.f, far + 64 * rt);
+          }
           p[rt] = weights(s[rt], 1.f, row[rt].bias);
         }
         bool odd = false;
@@ -673,7 +700,7 @@ struct Kernel {
           for (int d = 0; d < ND; ++d)
             *reinterpret_cast<float4*>(to + 16 * d) = make_float4(w.o[d][0], w.o[d][1], w.o[d][2], w.o[d][3]);
           if (quad == 0) {
-            a.stats[at_part * 2] = w.m == -INFINITY ? INFINITY : w.bias;
+            a.stats[at_part * 2] = -w.m(far + 64 * rt);
             a.stats[at_part * 2 + 1] = valid ? w.l[0] : __builtin_nanf("");
           }
         }
@@ -686,7 +713,8 @@ template <int D, bool BF, int STAGES, int RT>
 __global__ __launch_bounds__(kTile / 16 / RT * 64, D == 64 ? 3 : 2) void k_prompt_attention(Args a) {
   __shared__ __attribute__((aligned(1024))) char lds[STAGES * Kernel<D, BF, STAGES, RT>::STAGE];
   __shared__ Plan plan;
-  Kernel<D, BF, STAGES, RT>::run(a, lds, plan);
+  __shared__ float far[kTile / 16 * 64];
+  Kernel<D, BF, STAGES, RT>::run(a, lds, plan, far);
 }
 
 // Joins the partials of the item that begins in workgroup blockIdx.x's share and goes on behind it: its first share's partial
@@ -703,7 +731,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args 
   for (int u = threadIdx.x; u < kJoinRows * (D / 4); u += 64 * kJoinWaves) {
     const int r = blockIdx.y * kJoinRows + u / (D / 4), d = 4 * (u % (D / 4));
     if (r >= j.rows) continue;
-    // the weights go by the smallest bias so far; two partials on their way at once
+    // the weights go by the largest maximum so far, held as minus that; two partials on their way at once
     float low = INFINITY, sum = 0.f;
     f32x4 o{};
     for (u32 w = wg; w <= j.last; w += 2) {

@@ -1,0 +1,137 @@
+"""Edges of a prompt's operators: scores and values far from ordinary ones, buffers that are replaced, every kernel of the
+linears, sizes at the limits.  Tolerances by the number formats as in tests/test_prompt_parity.py (u, e and half_step)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import cache_oracle as CO
+from oracle import prompt_oracle as PO
+
+E = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    global C, K, P, svg
+    import cache_cases as K  # noqa: F401
+    import svg_cases as C  # noqa: F401
+    import test_prompt_parity as P  # noqa: F401
+    import speculative_verify_gemm_amd as svg
+    P.svg, P.C, P.K = svg, C, K
+
+
+# ---------------------------------------------------------------- attention
+def attend(c, kind, q, start, count, scale):
+    """(out fp64, the queries as the device has them)."""
+    R, A, _ = q.shape
+    qd = torch.from_numpy(q.astype(np.float32)).to(P.TYPES[kind]).to(C.DEV)
+    cache, rows = K.to_library(svg, c, kind), svg.RowMap(P.i32(start), P.i32(count), n_rows=R)
+    out = torch.full_like(qd, 7.0)
+    svg.prompt_attention(cache, 0, rows, qd, out, svg.prompt_attention_workspace(cache, A, R), scale=scale)
+    return P.host64(out), P.host64(qd)
+
+
+def tokens(c, kind, s, n, head=0):
+    """Keys and values of slot s's first n tokens, fp64."""
+    at = np.arange(n)
+    pg, t, d = c["table"][s][at // c["page"]].astype(np.int64), (at % c["page"])[:, None], np.arange(c["dim"])[None, :]
+    return tuple(P.wide(kind)(c[x][0, pg, head][at[:, None], f(t, d, c["dim"])]) for x, f in (("k", CO.key_at), ("v", CO.value_at)))
+
+
+def put(c, kind, name, s, values, head=0):
+    """Values [n, dim] as slot s's first n keys ("k") or values ("v")."""
+    w = K.bits(torch.from_numpy(np.asarray(values, np.float32)).to(P.TYPES[kind]))
+    d = np.arange(c["dim"])
+    for t in range(len(values)):
+        page, i = c["table"][s, t // c["page"]], t % c["page"]
+        c[name][0, page, head][(CO.key_at if name == "k" else CO.value_at)(i, d, c["dim"])] = w[t]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("power", [4, 10, 14, 17, 20, 22, 24, 26, 30])
+def test_scores_far_apart(gpu, power, dim, kind):
+    """Scales of 2^power and -2^power.  A score is off by (dim + 8) e B at most, B = |scale| sum |q k|: where the best token leads by
+    twice that and 40 more, the others together weigh less than 2^-49 and the row is that token's value: p v / p, two roundings of
+    fp32 and the output's.  Any other row lies between the smallest and the largest value."""
+    C.say(f"prompt_attention scale=2^{power} dim={dim} {kind}")
+    rng = np.random.default_rng(power)
+    lens, n = [300, 5, 900], [40, 5, 3]
+    c = K.make(3, lens, max(n), H=1, dim=dim, page=64)
+    P.fill(c, rng, kind)
+    start, count = P.packed(n)
+    q = rng.standard_normal((sum(n), 2, dim))
+    for scale in (2.0 ** power, -2.0 ** power):
+        got, q64 = attend(c, kind, q, start, count, scale)
+        assert np.isfinite(got).all()
+        clear = 0
+        for s in range(len(n)):
+            keys, v = tokens(c, kind, s, lens[s] + n[s])
+            for i in range(n[s]):
+                L = lens[s] + i + 1
+                for a in range(2):
+                    x, y = q64[start[s] + i, a], got[start[s] + i, a]
+                    sc = scale * (keys[:L] @ x)
+                    lead = 2 * (dim + 8) * E * abs(scale) * (np.abs(keys[:L]) @ np.abs(x)).max() + 40
+                    best = int(sc.argmax())
+                    if L == 1 or sc[best] - np.delete(sc, best).max() > lead:
+                        clear += 1
+                        big = np.abs(v[:L]).max()
+                        assert np.all(np.abs(y - v[best]) <= P.half_step(kind, v[best]) + 4 * E * np.abs(v[best]) + 2.0 ** -48 * big), (s, i, a)
+                    else:
+                        low, high = v[:L].min(0), v[:L].max(0)
+                        room = (L + 8) * E * np.abs(v[:L]).max()
+                        assert np.all(y >= low - room - P.half_step(kind, low)) and np.all(y <= high + room + P.half_step(kind, high)), (s, i, a)
+        assert power < 10 or clear >= 0.4 * 2 * sum(n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("power", [0, 12, 15, 18, 21, 24, 25, 26, 27, 30])
+def test_equal_scores_of_any_size(gpu, power, kind):
+    """Every key is the same: all probabilities are one number, and the row is the mean of its values.  L products and their sums in
+    fp32 are off by L e of the sum of the sizes, numerator and denominator each."""
+    rng = np.random.default_rng(power)
+    lens, n = [1000, 7], [40, 6]
+    c = K.make(3, lens, max(n), H=1, dim=64, page=32)
+    P.fill(c, rng, kind)
+    key = rng.standard_normal(64)
+    for s in range(2):
+        put(c, kind, "k", s, np.repeat(key[None], lens[s] + n[s], 0))
+    start, count = P.packed(n)
+    for sign in (1, -1):
+        got, _ = attend(c, kind, np.repeat(sign * key[None, None], sum(n), 0), start, count, 2.0 ** power)
+        for s in range(2):
+            v = tokens(c, kind, s, lens[s] + n[s])[1]
+            for i in range(n[s]):
+                L = lens[s] + i + 1
+                ref, size = v[:L].mean(0), np.abs(v[:L]).mean(0)
+                assert np.all(np.abs(got[start[s] + i, 0] - ref) <= (2 * L + 8) * E * size * 1.01 + P.half_step(kind, ref)), (sign, s, i)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("first", [2.0 ** 23, 2.0 ** 24, 2.0 ** 25, -2.0 ** 24, -2.0 ** 25])
+def test_scores_that_just_pass_the_largest_so_far(gpu, first, kind):
+    """Scores of 2^24 and 8 powers of two more behind them, where the steps of fp32 are 2 (and 4): the products of a score with scale and
+    log2(e) are off by 3 steps of half an ulp together, so that the ratio of two probabilities is 2^8 within 2^-6 and 2^6 at 2^24, within
+    2^12 at 2^25.  Values 0 for the first and 1 for the others; 128 of the one, 192 and more of the others."""
+    rng = np.random.default_rng(3)
+    ctx, n = 320, 20
+    c = K.make(3, [ctx], n, H=1, dim=64, page=32)
+    P.fill(c, rng, kind)
+    later = np.arange(ctx + n) >= 128
+    keys, q = np.zeros((ctx + n, 64)), np.zeros((n, 1, 64))
+    q[..., 0], q[..., 1] = np.sign(first) * 2.0 ** 12, 1
+    keys[:, 0], keys[:, 1] = abs(first) / 2.0 ** 12, 8 * later
+    put(c, kind, "k", 0, keys)
+    put(c, kind, "v", 0, np.repeat(later[:, None] * 1.0, 64, 1))
+    got, _ = attend(c, kind, q, [0], [n], float(np.log(2.0)))
+    ulp = max(1.0, abs(first) * 2.0 ** -23)
+    ratio = 2.0 ** (8 - 3 * ulp) * 193 / 128
+    assert np.isfinite(got).all()
+    assert np.all(got >= ratio / (1 + ratio) * (1 - 2 * P.U[kind])) and np.all(got <= 1)
