@@ -105,7 +105,8 @@ svg_status rope_append(const svg_kv_cache* cache, int layer, const svg_rope* rop
  *  Row i of slot s: o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale * q . k_t), over the positions 0 .. len[s] + i.
  *  Scores, sums and accumulators are fp32; p enters the second product rounded to the cache's type (as v is held in it), so an
  *  output is off by its own rounding and by about as much again.  Of an fp16 cache a p below 2^-33 of the
- *  row's largest so far may be lost.
+ *  row's largest so far may be lost.  Finite scores and values of any size give finite rows (of a bf16 cache an output is off by up to
+ *  2^-116 a token besides, which only its smallest values show).
  *  Keys and values of tokens that a row does not see never reach it, whatever they are.  Of those it sees: a key that gives a
  *  NaN or +infinite score makes the row NaN (-infinity leaves the token out, and a row all of whose tokens are left out is NaN);
  *  a value that is not finite makes its own element of the row NaN or infinite, and no other.

@@ -73,8 +73,14 @@ SVG_DEV u32 odd_halves(u32 w) {
 }
 
 // A probability is at most 2^kTop: the running maximum is raised when a score passes it by kSlack, and everything is lifted by
-// kTop - kSlack, so that small ones stay above the smallest number of fp16.
-constexpr float kTop = 15.f, kSlack = 7.f, kLift = kTop - kSlack;
+// kTop - kSlack.  fp16: up, so that small ones stay above the type's smallest number.  bf16, whose values reach fp32's largest number: down,
+// so that those of 2^25 tokens (a table row's most) add up to less than 1 and O stays below the largest value; a product of O is
+// rounded to fp32's smallest number, 2^-149, which is 2^-116 in an output.
+constexpr float kSlack = 7.f;
+template <bool BF>
+constexpr float kTop = BF ? -26.f : 15.f;
+template <bool BF>
+constexpr float kLift = kTop<BF> - kSlack;
 // A probability is 2^(f s + bias), bias = kLift - m: one operation, and one rounding, since m is a whole number of 1 / kGrid up to
 // kFar.  Beyond, the product inside that operation and the rounded one that m came from would differ by 2^-11 and more (from 2^24 on by
 // whole numbers, and kLift - m loses kLift), which fp16 has no room for: there it is 2^((f s - m) + kLift) with each step rounded, 2^kLift
@@ -485,7 +491,7 @@ struct Kernel {
           const float m = beyond ? top : floorf(top * kGrid) * (1.f / kGrid);
           const float by = before == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(before - m);
           r.limit = beyond ? -INFINITY : m + kSlack;
-          r.bias = beyond ? kLift : kLift - m;
+          r.bias = beyond ? kLift<BF> : kLift<BF> - m;
           if (beyond) *far = m;
 #pragma unroll
           for (int d = 0; d < ND; ++d) r.o[d] *= by;

@@ -135,3 +135,29 @@ def test_scores_that_just_pass_the_largest_so_far(gpu, first, kind):
     ratio = 2.0 ** (8 - 3 * ulp) * 193 / 128
     assert np.isfinite(got).all()
     assert np.all(got >= ratio / (1 + ratio) * (1 - 2 * P.U[kind])) and np.all(got <= 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("exponent", [127, 120, 113, 100, -60, -85, -100, -110, -126])
+def test_values_of_any_size_in_a_bf16_cache(gpu, exponent, dim):
+    """Values of up to 2^exponent (127: bf16's largest number): a row is a mean of values, so it is finite.  Accumulators end at 2^-149 and
+    the probabilities at 2^-33 or more for the largest: a rounding there is off by 2^-149 / 2^-33, and there is one for each of up to
+    L products and the joins."""
+    rng = np.random.default_rng(exponent + 130)
+    lens, n = [1500, 0, 70], [30, 40, 1]
+    c = K.make(3, lens, max(n), H=1, dim=dim, page=64)
+    P.fill(c, rng, "bf16")
+    largest = float(torch.finfo(torch.bfloat16).max)
+    for s in range(3):
+        size = rng.random((lens[s] + n[s], dim)) * 0.5 + 0.5
+        size[::7] = 1.0
+        sign = np.where(rng.random(size.shape) < 0.9, 1.0, -1.0) if s else 1.0
+        put(c, "bf16", "v", s, np.clip(np.ldexp(size, exponent + (exponent == 127)), 0, largest) * sign)
+    start, count = P.packed(n)
+    for spread in (1e-3, 1.0, 30.0):
+        got, q64 = attend(c, "bf16", rng.standard_normal((sum(n), 2, dim)), start, count, spread / dim ** 0.5)
+        assert np.isfinite(got).all()
+        ref, _, size = PO.attention(c, P.wide("bf16"), 0, q64, start, count, spread / dim ** 0.5)
+        tol = P.attention_bound(c, "bf16", ref, size, 1530) + 1600 * 2.0 ** (-149 + 33)
+        assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
