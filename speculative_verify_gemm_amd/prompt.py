@@ -63,7 +63,9 @@ class RowMap:
     """Where a step's rows belong (kv_row_map writes it, rope_append and
     prompt_attention read it): start and count int32 [n_slots], pos and place
     int32 [n_rows], and, if wanted, slot int32 [n_rows].  The object keeps the
-    tensors; without pos and place (n_rows given) only prompt_attention takes it."""
+    tensors; without pos and place (n_rows given) only prompt_attention takes it.
+    The tensors may be set to others of the same shape and device (calls that a
+    graph has captured go on with the ones they were made with)."""
 
     def __init__(self, start, count, pos=None, place=None, slot=None, n_rows=None):
         dev = _device(start, "start")
@@ -75,11 +77,19 @@ class RowMap:
             raise ValueError("pos, place and slot must be [n_rows]")
         if pos is not None and n_rows is not None and n_rows != pos.shape[0]:
             raise ValueError("n_rows must be the length of pos")
-        self.start, self.count, self.pos, self.place, self.slot = start, count, pos, place, slot
+        self._t = dict(start=start, count=count, slot=slot, pos=pos, place=place)
         self.device, self.n_slots = dev, start.shape[0]
         self.n_rows = pos.shape[0] if pos is not None else int(n_rows)
-        at = lambda t, name: None if t is None else _tensor(t, name, _I32, dev)  # noqa: E731
-        self._p = [at(t, n) for t, n in ((start, "start"), (count, "count"), (slot, "slot"), (pos, "pos"), (place, "place"))]
+        self._p = [None if t is None else _tensor(t, name, _I32, dev) for name, t in self._t.items()]
+
+    def _set(self, name, t):
+        now = self._t[name]
+        if now is None:
+            raise ValueError(f"rows has no {name}")
+        if t is None or t.shape != now.shape:
+            raise ValueError(f"{name} must have shape {list(now.shape)}")
+        self._p[list(self._t).index(name)] = _tensor(t, name, _I32, self.device)
+        self._t[name] = t
 
     @classmethod
     def empty(cls, cache, n_rows):
@@ -89,13 +99,17 @@ class RowMap:
         return cls(zero(), zero(), none(n_rows), none(n_rows), none(n_rows))
 
 
+for _name in ("start", "count", "slot", "pos", "place"):
+    setattr(RowMap, _name, property(lambda self, n=_name: self._t[n], lambda self, t, n=_name: self._set(n, t)))
+
+
 def kv_row_map(cache, n_new, rows, T=0, parent=None, stream=None):
     """Fill `rows` (a RowMap) for a step in which slot s has n_new[s] new rows
     (int32 [n_slots]): packed one slot after another (T = 0), or T a slot, chains
     or draft trees (parent int32 [n_slots, T]).  Behind kv_reserve; once for all layers."""
     if rows.device != cache.device or rows.n_slots != cache.n_slots:
         raise ValueError("rows must be a RowMap of the cache's device and number of slots")
-    if rows.pos is None:
+    if rows._p[3] is None:
         raise ValueError("rows has no pos and place")
     pp = None if parent is None else _slots(parent, "parent", cache, T)
     _call(_lib.kv_row_map, cache.device, stream, cache._ref, _slots(n_new, "n_new", cache), pp, T, rows.n_rows, *rows._p)
@@ -105,16 +119,46 @@ def kv_row_map(cache, n_new, rows, T=0, parent=None, stream=None):
 class Rope:
     """Rotary positions: the angle of pair i at position p is p * freq[i], freq
     float64 [rot / 2] on the device; pairs (2 i, 2 i + 1) if interleaved, else
-    (i, i + rot / 2); cosines and sines are multiplied by amplitude."""
+    (i, i + rot / 2); cosines and sines are multiplied by amplitude.  The object
+    keeps freq, which may be set to another tensor of its shape and device, as
+    interleaved and amplitude may be set anew (calls that a graph has captured go on
+    with what they were made with)."""
 
     def __init__(self, freq, interleaved=False, amplitude=1.0):
         dev = _device(freq, "freq")
         if freq.dim() != 1:
             raise ValueError("freq must be [rot / 2]")
-        self.freq, self.device, self.rot = freq, dev, 2 * freq.shape[0]
-        self.interleaved, self.amplitude = bool(interleaved), float(amplitude)
-        self._c = RopeC(_tensor(freq, "freq", torch.float64, dev), self.rot, int(self.interleaved), self.amplitude)
+        self.device, self.rot = dev, 2 * freq.shape[0]
+        self._c = RopeC(None, self.rot)
         self._ref = ctypes.byref(self._c)
+        self.freq, self.interleaved, self.amplitude = freq, interleaved, amplitude
+
+    @property
+    def freq(self):
+        return self._freq
+
+    @freq.setter
+    def freq(self, t):
+        if t.shape != (self.rot // 2,):
+            raise ValueError(f"freq must have shape {[self.rot // 2]}")
+        self._c.freq = _tensor(t, "freq", torch.float64, self.device)
+        self._freq = t
+
+    @property
+    def interleaved(self):
+        return bool(self._c.interleaved)
+
+    @interleaved.setter
+    def interleaved(self, v):
+        self._c.interleaved = int(bool(v))
+
+    @property
+    def amplitude(self):
+        return self._amplitude
+
+    @amplitude.setter
+    def amplitude(self, v):
+        self._c.amplitude = self._amplitude = float(v)
 
     @classmethod
     def make(cls, rot, base=10000.0, interleaved=False, scaling=None, factor=1.0, trained=None, bounds=(32.0, 1.0), amplitude=None,
@@ -162,7 +206,7 @@ def rope_append(cache, layer, rows, rope, q, k, v, q_out=None, stream=None):
     width = cache.heads * D
     pk, lk, n, kind = _float_rows(k, "k", dev, None, width)
     pv, lv, nv, _ = _float_rows(v, "v", dev, k.dtype, width)
-    if rows.pos is None:
+    if rows._p[3] is None:
         raise ValueError("rows has no pos and place")
     if n != rows.n_rows or nv != n:
         raise ValueError("k and v must have n_rows rows")

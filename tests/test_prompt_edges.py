@@ -161,3 +161,72 @@ def test_values_of_any_size_in_a_bf16_cache(gpu, exponent, dim):
         ref, _, size = PO.attention(c, P.wide("bf16"), 0, q64, start, count, spread / dim ** 0.5)
         tol = P.attention_bound(c, "bf16", ref, size, 1530) + 1600 * 2.0 ** (-149 + 33)
         assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
+
+
+# ------------------------------------------------------- tensors that are replaced
+@pytest.mark.gpu
+def test_a_row_maps_tensors_may_be_replaced(gpu):
+    """A call uses the tensors that the object has at that time, and the object keeps those."""
+    c = K.make(1, [5, 40], 40, H=1, dim=64, page=32)
+    cache = K.to_library(svg, c)
+    rows = svg.RowMap.empty(cache, 12)
+    svg.kv_row_map(cache, P.i32([3, 2]), rows)
+    first = {n: getattr(rows, n) for n in ("start", "count", "slot", "pos", "place")}
+    kept = {n: t.clone() for n, t in first.items()}
+    for n, t in first.items():
+        setattr(rows, n, torch.full_like(t, 77))
+        assert getattr(rows, n) is not t
+    svg.kv_row_map(cache, P.i32([7, 4]), rows)
+    for n, w in zip(("start", "count", "slot", "pos", "place"), PO.row_map(c, [7, 4], 0, 12)):
+        assert np.array_equal(C.host(getattr(rows, n)), w) and torch.equal(first[n], kept[n]), n
+    # what reads them: the rotation takes pos and place, the attention start and count
+    x = torch.randn((12, 3, 64), device=C.DEV)
+    rope, out = svg.Rope.make(64, device=C.DEV), torch.full((12, 1, 64), 7.0, device=C.DEV)
+    rows.pos, rows.place = torch.full_like(rows.pos, -1), torch.full_like(rows.place, -1)
+    svg.rope_append(cache, 0, rows, rope, x[:, :1], x[:, 1:2], x[:, 2:], out)
+    assert bool((out == 7).all())
+    rows.pos = torch.zeros_like(rows.pos)
+    svg.rope_append(cache, 0, rows, rope, x[:, :1], x[:, 1:2], x[:, 2:], out)
+    assert torch.equal(out, x[:, :1])
+    rows.count = torch.zeros_like(rows.count)
+    q = torch.ones((12, 1, 64), dtype=torch.float16, device=C.DEV)
+    o = torch.full_like(q, 7.0)
+    svg.prompt_attention(cache, 0, rows, q, o, svg.prompt_attention_workspace(cache, 1, 12))
+    assert bool((o == 7).all())
+    for name, bad, error in (("pos", rows.pos[:11], ValueError), ("pos", None, ValueError), ("start", rows.start.long(), TypeError),
+                             ("count", rows.count.cpu(), ValueError), ("place", torch.zeros(24, dtype=torch.int32, device=C.DEV)[::2], ValueError)):
+        now = getattr(rows, name)
+        with pytest.raises(error):
+            setattr(rows, name, bad)
+        assert getattr(rows, name) is now
+    with pytest.raises(ValueError):
+        svg.RowMap(rows.start, rows.count, n_rows=3).pos = rows.pos
+
+
+@pytest.mark.gpu
+def test_a_rotations_frequencies_may_be_replaced(gpu):
+    c = K.make(1, [5], 8, H=1, dim=64, page=32)
+    cache = K.to_library(svg, c)
+    rows = svg.RowMap.empty(cache, 6)
+    svg.kv_row_map(cache, P.i32([6]), rows)
+    rope = svg.Rope.make(32, device=C.DEV)
+    x = torch.randn((6, 3, 64), device=C.DEV)
+
+    def turned(r):
+        out = torch.zeros((6, 1, 64), device=C.DEV)
+        svg.rope_append(cache, 0, rows, r, x[:, :1], x[:, 1:2], x[:, 2:], out)
+        return out
+
+    before = turned(rope)
+    rope.freq = svg.Rope.make(32, 500.0, device=C.DEV).freq
+    rope.interleaved, rope.amplitude = True, 1.5
+    assert rope.interleaved is True and rope.amplitude == 1.5
+    fresh = svg.Rope(svg.Rope.make(32, 500.0, device=C.DEV).freq, interleaved=True, amplitude=1.5)
+    after = turned(rope)
+    assert torch.equal(after, turned(fresh)) and not torch.equal(after, before)
+    for bad, error in ((rope.freq[:15], ValueError), (rope.freq.float(), TypeError), (rope.freq.cpu(), ValueError)):
+        with pytest.raises(error):
+            rope.freq = bad
+    rope.amplitude = float("nan")
+    with pytest.raises(svg.SvgError):
+        turned(rope)
