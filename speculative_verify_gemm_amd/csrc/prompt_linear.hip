@@ -248,15 +248,18 @@ struct W4 {
 };
 
 // 4 bytes a lane from global memory straight into LDS (256 bytes from `to` on), as load_to_lds.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 SVG_DEV void load4_to_lds(const char* from, u32 lane4, u32 to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane4), "s"(from) : "memory");
+               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane4), "s"(from) : "memory", "m0");
 }
 // 2 bytes a lane, each to a dword of its own.
 SVG_DEV void load2_to_lds(const char* from, u32 lane2, u32 to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2"
-               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane2), "s"(from) : "memory");
+               ::"s"(__builtin_amdgcn_readfirstlane((int)to)), "v"(lane2), "s"(from) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // A pointer that is the same for the wave, in scalar registers.
 SVG_DEV const char* uniform(const char* p) {
   const unsigned long long v = reinterpret_cast<unsigned long long>(p);

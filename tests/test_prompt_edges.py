@@ -230,3 +230,19 @@ def test_a_rotations_frequencies_may_be_replaced(gpu):
     rope.amplitude = float("nan")
     with pytest.raises(svg.SvgError):
         turned(rope)
+
+
+# ------------------------------------------------------------------ the sources
+def test_assembly_declares_the_registers_that_it_writes():
+    """m0 holds where loads into LDS go: what writes it has to name it, or the compiler may keep a value of its own there."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_verify_gemm_amd", "csrc")
+    found = 0
+    for name in sorted(os.listdir(csrc)):
+        for block in re.findall(r"\basm\s+volatile\s*\((.*?)\);", open(os.path.join(csrc, name)).read(), re.S):
+            code, operands = block.split(":", 1) if ":" in block else (block, "")
+            if re.search(r"s_mov_b32 m0\b", code):
+                found += 1
+                assert '"m0"' in operands.split(":")[-1], (name, code)
+    assert found >= 3
