@@ -629,7 +629,7 @@ hipError_t launch_few(const Args& a, hipStream_t stream) {
 //   W4   few | mid    256 x 4096 x 4096: 21 | 36      128 x 24576 x 4096: 55 | 37          (groups of 64)
 //        small | mid  512 x 4096 x 4096: 26.5 | 39    1024 x 4096 x 4096: 41 | 40          4096 x 24576 x 4096: 932 | 729
 //                     512 x 4096 x 4096 in groups of 32: 38 | 60, of 128: 24 | 34
-enum { kFew, kSmall, kMid, kBig };
+enum { kNone = -1, kFew, kSmall, kMid, kBig };
 constexpr long kMaxGridY = 65535;  // a launch has no more workgroups in y
 // A step's cost: few, in a round of one workgroup a compute unit, for a workgroup and each 16 of its rows (1 / 10000 us); small
 // and mid, for 1, 2, .. workgroups on a compute unit.
@@ -649,9 +649,9 @@ constexpr const Cost& costs() {
   else return kCostW8;
 }
 template <class F>
-long cost_of(int way, int M, int N, int K) {
+long cost_of(int way, int M, int N, int K, long cus) {
   constexpr const Cost& c = costs<F>();
-  const long cus = svg_cu_count(), steps = (K + F::kStep - 1) / F::kStep;
+  const long steps = (K + F::kStep - 1) / F::kStep;
   const auto up = [](long x, long y) { return (x + y - 1) / y; };
   const auto rounds = [&](long tiles, const long* each, long n) {
     const long rest = up(tiles % (n * cus), cus);
@@ -678,37 +678,54 @@ hipError_t launch_way(int way, const Args& a, hipStream_t stream) {
     return launch<F, 2, 4, 8, 4, 1>(a, stream);
   }
 }
+// The ways of a product: the first rows one way, and the others (if any) another, in a launch of its own.
+struct Choice {
+  int way, rows, then;
+};
 template <class F>
-hipError_t launch_best(const Args& a, hipStream_t stream) {
-  int way = kFew;
-  long least = cost_of<F>(kFew, a.M, a.N, a.K);
-  const auto look = [&](int w, int M) {
-    const long c = cost_of<F>(w, M, a.N, a.K);
-    if (c < least) least = c, way = w;
+Choice choose(int M, int N, int K, int cus) {
+  Choice best{kFew, M, kNone};
+  long least = cost_of<F>(kFew, M, N, K, cus);
+  const auto look = [&](int way) {
+    const long c = cost_of<F>(way, M, N, K, cus);
+    if (c < least) least = c, best.way = way;
   };
-  look(kSmall, a.M);
-  look(kMid, a.M);
+  look(kSmall);
+  look(kMid);
   if constexpr (!F::k4) {
-    look(kBig, a.M);
-    // the rows of whole large tiles, and the rest another way, in a launch of its own (3 us)
-    const int main = a.M & ~255, rest = a.M - main;
+    look(kBig);
+    // the rows of whole large tiles, and the rest another way (3 us)
+    const int main = M & ~255, rest = M - main;
     if (main > 0 && rest > 0) {
       int then = kFew;
       for (const int w : {kSmall, kMid})
-        if (cost_of<F>(w, rest, a.N, a.K) < cost_of<F>(then, rest, a.N, a.K)) then = w;
-      if (cost_of<F>(kBig, main, a.N, a.K) + cost_of<F>(then, rest, a.N, a.K) + 300 < least) {
-        Args first = a, second = a;
-        first.M = main;
-        second.M = rest;
-        second.xq += (size_t)main * a.K;
-        second.x_scale += main;
-        second.y = static_cast<char*>(a.y) + (size_t)main * a.N * (a.y_type == SVG_F32 ? 4 : 2);
-        if (const hipError_t e = launch_way<F>(kBig, first, stream)) return e;
-        return launch_way<F>(then, second, stream);
-      }
+        if (cost_of<F>(w, rest, N, K, cus) < cost_of<F>(then, rest, N, K, cus)) then = w;
+      if (cost_of<F>(kBig, main, N, K, cus) + cost_of<F>(then, rest, N, K, cus) + 300 < least) best = {kBig, main, then};
     }
   }
-  return launch_way<F>(way, a, stream);
+  return best;
+}
+template <class F>
+hipError_t launch_best(const Args& a, hipStream_t stream) {
+  const Choice c = choose<F>(a.M, a.N, a.K, svg_cu_count());
+  Args first = a;
+  first.M = c.rows;
+  const hipError_t e = launch_way<F>(c.way, first, stream);
+  if (e != hipSuccess || c.then == kNone) return e;
+  Args second = a;
+  second.M = a.M - c.rows;
+  second.xq += (size_t)c.rows * a.K;
+  second.x_scale += c.rows;
+  second.y = static_cast<char*>(a.y) + (size_t)c.rows * a.N * (a.y_type == SVG_F32 ? 4 : 2);
+  return launch_way<F>(c.then, second, stream);
+}
+
+// The weights' format, as a type, for f.
+template <class Fn>
+auto of_format(bool w8, bool z4, int group, const Fn& f) {
+  if (w8) return f(W8{});
+  if (z4) return group == 32 ? f(W4<32, true>{}) : (group == 64 ? f(W4<64, true>{}) : f(W4<128, true>{}));
+  return group == 32 ? f(W4<32, false>{}) : (group == 64 ? f(W4<64, false>{}) : f(W4<128, false>{}));
 }
 
 }  // namespace
@@ -721,6 +738,12 @@ hipError_t svg_launch_prompt_w8(const int8_t* xq, const float* x_scale, int M, i
 hipError_t svg_launch_prompt_w4(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
                                 const void* w_zero, bool z4, int group, int N, void* y, int y_type, hipStream_t stream) {
   const Args a{xq, x_scale, reinterpret_cast<const char*>(wq), w_scale, static_cast<const char*>(w_zero), y, M, N, K, y_type, 0, 0, 0};
-  if (z4) return group == 32 ? launch_best<W4<32, true>>(a, stream) : (group == 64 ? launch_best<W4<64, true>>(a, stream) : launch_best<W4<128, true>>(a, stream));
-  return group == 32 ? launch_best<W4<32, false>>(a, stream) : (group == 64 ? launch_best<W4<64, false>>(a, stream) : launch_best<W4<128, false>>(a, stream));
+  return of_format(false, z4, group, [&](auto f) { return launch_best<decltype(f)>(a, stream); });
+}
+
+void svg_prompt_linear_choice(int fmt, int group, int M, int N, int K, int cus, int32_t* choice) {
+  const Choice c = of_format(fmt == SVG_W8_SYM, fmt == SVG_W4_ASYM_Z4, group, [&](auto f) { return choose<decltype(f)>(M, N, K, cus); });
+  choice[0] = c.way;
+  choice[1] = c.rows;
+  choice[2] = c.then;
 }

@@ -107,6 +107,9 @@ hipError_t svg_launch_prompt_w8(const int8_t* xq, const float* x_scale, int M, i
                                 void* y, int y_type, hipStream_t stream);
 hipError_t svg_launch_prompt_w4(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
                                 const void* w_zero, bool z4, int group, int N, void* y, int y_type, hipStream_t stream);
+// Which kernels a prompt linear takes on a device of `cus` compute units (host only; for the tests, which name the kernel that
+// they mean): the way of the first rows (0 few, 1 small, 2 mid, 3 big), their number, the way of the others (-1: none).
+extern "C" void svg_prompt_linear_choice(int fmt, int group, int M, int N, int K, int cus, int32_t* choice);
 hipError_t svg_launch_gated_quant(const void* x, int64_t ld_x, const void* gate, int64_t ld_gate, int x_type, int M, int K,
                                   const int8_t* signs, int block, int8_t* xq, float* x_scale, hipStream_t stream);
 

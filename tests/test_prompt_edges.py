@@ -6,6 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import cache_oracle as CO
+from oracle import norm_oracle as NO
 from oracle import prompt_oracle as PO
 
 E = 2.0 ** -24
@@ -161,6 +162,95 @@ def test_values_of_any_size_in_a_bf16_cache(gpu, exponent, dim):
         ref, _, size = PO.attention(c, P.wide("bf16"), 0, q64, start, count, spread / dim ** 0.5)
         tol = P.attention_bound(c, "bf16", ref, size, 1530) + 1600 * 2.0 ** (-149 + 33)
         assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
+
+
+# ------------------------------------------------------------------ linears
+FEW, SMALL, MID, BIG = range(4)
+ROWS, COLS = {FEW: 100, SMALL: 300, MID: 1001, BIG: 1150}, {FEW: 515, SMALL: 4091, MID: 4091, BIG: 8187}
+
+
+def linear_cases():
+    """(format, group, ways as svg_prompt_linear_choice has them, M, N, K, y): every kernel, of 1 to 3 steps of K, of one more than the
+    ring has places, with a rest of K; odd numbers of columns, and whole tiles (stored four values at a time); more than one
+    tile for a workgroup; every type of output."""
+    cases = []
+    types = ("fp32", "bf16", "fp16")
+
+    def add(fmt, group, way, M, N, K, then=None):
+        ways = (way, M if then is None else M & ~255, -1 if then is None else then)
+        for y in (types if way == BIG or (K > 500 and way != FEW) else (types[len(cases) % 3],)):
+            cases.append((fmt, group, ways, M, N, K, y))
+
+    for way in (FEW, SMALL, MID, BIG):
+        for K in (32, 64, 96, 192, 256, 320, 1056):
+            add("w8", 0, way, ROWS[way], COLS[way], K)
+    for way, M, N in ((SMALL, 320, 4096), (MID, 1024, 4096), (BIG, 1280, 12288)):
+        for K in (32, 160, 640):
+            add("w8", 0, way, M, N, K)
+    add("w8", 0, MID, 2049, 3010, 96)
+    add("w8", 0, BIG, 1283, 12277, 1056, FEW)
+    add("w8", 0, BIG, 2304, 12288, 320)
+    for fmt in ("w4_z16", "w4_z4"):
+        for group in (32, 64, 128):
+            for way in (FEW, SMALL, MID):
+                for K in (group, 128 + group, 256 + group, 384, 1024 + group):
+                    add(fmt, group, way, ROWS[way], COLS[way], K)
+            add(fmt, group, SMALL, 320, 4096, 512)
+            add(fmt, group, MID, 1024, 4096, 512 + group)
+            add(fmt, group, MID, 1921, 4091 if group == 32 else 8187, 256 + group)
+    return cases
+
+
+def choice(lib, fmt, group, M, N, K, cus):
+    import ctypes
+    got = (ctypes.c_int32 * 3)()
+    lib.svg_prompt_linear_choice({"w4_z4": 0, "w4_z16": 1, "w8": 2}[fmt], group, M, N, K, cus, got)
+    return tuple(got)
+
+
+def test_the_sizes_take_every_kernel_of_the_linears():
+    """The rule on 256 compute units, on the host: each case takes the kernel that it names, and all kernels of all formats are taken."""
+    import speculative_verify_gemm_amd as lib
+    taken = set()
+    for fmt, group, ways, M, N, K, y in linear_cases():
+        assert choice(lib.lib, fmt, group, M, N, K, 256) == ways, (fmt, group, M, N, K)
+        taken |= {(fmt, group, w, y) for w in ways[::2] if w >= 0}
+    for fmt, group in [("w8", 0)] + [(f, g) for f in ("w4_z16", "w4_z4") for g in (32, 64, 128)]:
+        for way in (FEW, SMALL, MID) + ((BIG,) if fmt == "w8" else ()):
+            types = {t[3] for t in taken if t[:3] == (fmt, group, way)}
+            assert types == {"fp32", "bf16", "fp16"} if way != FEW else types, (fmt, group, way, types)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,group,ways,M,N,K,y", linear_cases())
+def test_every_kernel_of_the_linears(gpu, fmt, group, ways, M, N, K, y):
+    """Against the formula in 64 bits on the device; bounds as in tests/test_prompt_parity.py."""
+    C.say(f"prompt linear {fmt} group={group} ways={ways} M={M} N={N} K={K} {y}")
+    cus = torch.cuda.get_device_properties(C.DEV).multi_processor_count
+    assert choice(svg.lib, fmt, group, M, N, K, cus) == ways
+    rng = np.random.default_rng(M * 7 + N + K)
+    wq, ws, wz, s, w = P.weights(rng, N, K, fmt, group)
+    x = P.codes(rng, M, K)
+    xs = (rng.random(M) * 1e-2 + 1e-4).astype(np.float32)
+    guard = 64
+    buf = torch.full((M * N + 2 * guard,), 7.0, dtype=P.TYPES[y], device=C.DEV)
+    out = buf[guard:-guard].view(M, N)
+    xq, xsd = C.to_dev(NO.slab_codes(x).reshape(M, K)), C.to_dev(xs)
+    if fmt == "w8":
+        svg.w8a8_prompt_linear(xq, xsd, wq, ws, N, out)
+    else:
+        svg.w4a8_prompt_linear(xq, xsd, wq, ws, wz, fmt, group, N, out)
+    f64 = lambda t: torch.from_numpy(np.ascontiguousarray(t)).to(C.DEV).double()  # noqa: E731
+    xd, wd, sd, rows = f64(x), f64(w), f64(s), f64(xs)[:, None]
+    ng, ref, size = s.shape[1], 0, 0
+    for g in range(ng):
+        k = slice(g * (K // ng), (g + 1) * (K // ng))
+        part = (xd[:, k].contiguous() @ wd[:, k].T.contiguous()) * sd[:, g] * rows
+        ref, size = ref + part, size + part.abs()
+    half = (ref.abs() * P.U[y]).clamp(min=2.0 ** -25 if y == "fp16" else 0.0)
+    tol = (3 if fmt == "w8" else ng + 2) * E * size * (1 + P.U[y]) + half
+    assert bool(((out.double() - ref).abs() <= tol * (1 + 1e-6)).all()), float(((out.double() - ref).abs() / tol).max())
+    assert bool((buf[:guard] == 7).all()) and bool((buf[-guard:] == 7).all())
 
 
 # ------------------------------------------------------- tensors that are replaced
