@@ -130,7 +130,8 @@ svg_status prompt_attention(const svg_kv_cache* cache, int layer, const void* q,
  *  xq, x_scale   M rows in 32-row slab buffers, as add_rmsnorm_quant_i8 and gated_quant_i8 write them: rows 32 b .. 32 b + 31 (the
  *                last ones fewer) at xq + 32 b K, code (row m, k) of a buffer of R rows at byte ((k / 32) * R + m % 32) * 32 + k % 32.
  *                xq 16-byte aligned.
- *  M, K, N       M >= 0 (M <= 2^24), K % 32 == 0 (W4: K % group == 0), K <= 131072, M * K < 2^40; M == 0 or N == 0: nothing enqueued.
+ *  M, K, N       M >= 0 (M <= 2^24), K % 32 == 0 (W4: K % group == 0), K <= 131072, M * K < 2^40, 0 <= N <= 2^30; M == 0 or N == 0: nothing
+ *                enqueued.
  *  wq, w_scale, w_zero, fmt, group   the tiled storage as for w4a8_linear / w8a8_linear (svg_weight_sizes), wq 16-byte aligned.  w_scale
  *                and w_zero 4-byte.  fp16 zeros are whole numbers 0 .. 15, as rht_rotate_weights writes them.
  *  y             [M][N] of y_type (SVG_F32, SVG_F16, SVG_BF16), row-major, 4-byte aligned.
@@ -138,8 +139,8 @@ svg_status prompt_attention(const svg_kv_cache* cache, int layer, const void* q,
  *  W8: y[m][n] = x_scale[m] * s[n] * S[m][n];  W4: x_scale[m] * sum_g s[n][g] * S_g[m][n]; the integer sums are exact, the rest fp32,
  *  then one rounding to y_type.  A row's W8 results do not depend on M and on the other rows; W4's sum over the groups
  *  may be taken in another order for another M.
- *  Errors: SVG_EINVAL for a null required pointer, M, N < 0 or K <= 0; SVG_EUNSUPPORTED for an unknown y_type, fmt or group, K, M, M * K
- *  of 2^40 or M * N of 2^39 or more, weights that svg_weight_sizes refuses; SVG_EALIGN.
+ *  Errors: SVG_EINVAL for a null required pointer, M, N < 0 or K <= 0; SVG_EUNSUPPORTED for an unknown y_type, fmt or group, K, M, N, M * K
+ *  of 2^40 or M * N of 2^39 or more; SVG_EALIGN.
  */
 svg_status w4a8_prompt_linear(const int8_t* xq, const float* x_scale, int M, int K, const uint8_t* wq, const uint16_t* w_scale,
                               const void* w_zero, int fmt, int group, int N, void* y, int y_type, void* stream);

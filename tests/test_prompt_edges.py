@@ -253,6 +253,52 @@ def test_every_kernel_of_the_linears(gpu, fmt, group, ways, M, N, K, y):
     assert bool((buf[:guard] == 7).all()) and bool((buf[-guard:] == 7).all())
 
 
+
+@pytest.mark.parametrize("N", [2 ** 30 + 1, 2 ** 31 - 16, 2 ** 31 - 1])
+def test_more_columns_than_a_linear_takes(N):
+    """Columns are counted in 32 bits, a tile past the last one included."""
+    import speculative_verify_gemm_amd as lib
+    A = 0x10000      # aligned, never dereferenced: the call is refused
+    for M in (0, 1, 40):
+        assert lib.lib.w8a8_prompt_linear(A, A, M, 32, A, A, N, A, 0, None) == 2 and "N > 2^30" in lib.last_error()
+        assert lib.lib.w4a8_prompt_linear(A, A, M, 64, A, A, A, 1, 64, N, A, 0, None) == 2 and "N > 2^30" in lib.last_error()
+    assert lib.lib.w8a8_prompt_linear(A, A, 0, 32, A, A, 2 ** 30, A, 0, None) == 0
+
+
+def test_the_widest_products_are_not_for_the_kernel_of_few_rows():
+    """It has 512 threads for 16 columns, and a launch fewer than 2^32 in a dimension; 65535 workgroups in the other."""
+    import speculative_verify_gemm_amd as lib
+    for fmt, group in [("w8", 0)] + [(f, g) for f in ("w4_z16", "w4_z4") for g in (32, 64, 128)]:
+        for N in (2 ** 27 - 511, 2 ** 27, 2 ** 27 + 16, 2 ** 28 + 5, 2 ** 30):
+            for M in (1, 16, 17, 33, 100, 128, 129, 257, 300):
+                if (M + 15) // 16 * (N // 16) < 2 ** 31:
+                    for cus in (8, 64, 256, 304):
+                        assert FEW not in choice(lib.lib, fmt, group, M, N, 128, cus)[::2], (fmt, group, M, N, cus)
+        for M in (65535 * 128 + 1, 2 ** 24):
+            assert choice(lib.lib, fmt, group, M, 5, 128, 256)[0] != FEW
+
+
+@pytest.mark.gpu
+def test_weights_past_32_bits(gpu):
+    """Codes of 2^33 bytes and more: offsets of a column's codes that 32 bits do not hold."""
+    M, N, Kd = 3, 2 ** 27 + 21, 64
+    C.say(f"w8a8_prompt_linear M={M} N={N} K={Kd}")
+    Np = -(-N // 16) * 16
+    g = torch.Generator(device=C.DEV).manual_seed(3)
+    wq = torch.randint(-127, 128, (Np * Kd,), dtype=torch.int8, device=C.DEV, generator=g)
+    ws = (torch.rand(N, device=C.DEV, generator=g) * 2e-3 + 1e-3).half()
+    x = P.codes(np.random.default_rng(1), M, Kd)
+    xs = torch.rand(M, device=C.DEV, generator=g) * 1e-2 + 1e-4
+    y = torch.full((M, N), 7.0, device=C.DEV)
+    svg.w8a8_prompt_linear(C.to_dev(NO.slab_codes(x).reshape(M, Kd)), xs, wq, ws, N, y)
+    xd, tiles = C.to_dev(x).double(), wq.view(Np // 16, 4, 16, 16)       # [tile][16 values of K][row][value]
+    for at in range(0, N, 1 << 22):
+        n = min(N - at, 1 << 22)
+        w = tiles[at // 16:(at + n + 15) // 16].permute(0, 2, 1, 3).reshape(-1, Kd)[:n].double()
+        ref = (xd @ w.T.contiguous()) * ws[at:at + n].double() * xs.double()[:, None]
+        assert bool(((y[:, at:at + n].double() - ref).abs() <= 3 * E * ref.abs() * (1 + 1e-6)).all()), at
+
+
 # ------------------------------------------------------- tensors that are replaced
 @pytest.mark.gpu
 def test_a_row_maps_tensors_may_be_replaced(gpu):
@@ -320,6 +366,7 @@ def test_a_rotations_frequencies_may_be_replaced(gpu):
     rope.amplitude = float("nan")
     with pytest.raises(svg.SvgError):
         turned(rope)
+
 
 
 # ------------------------------------------------------------------ the sources
