@@ -369,6 +369,84 @@ def test_a_rotations_frequencies_may_be_replaced(gpu):
 
 
 
+# ------------------------------------------------------- more rows than one turn of a launch
+def long_table(pages, page, S, heads=1, dim=64):
+    """A cache whose S slots have `pages` pages each, in an order of their own."""
+    cache = svg.KVCache.empty(1, S * pages, heads, dim, page, S, pages, device=C.DEV)
+    g = torch.Generator(device=C.DEV).manual_seed(7)
+    cache.k.zero_(), cache.v.zero_()
+    cache.table = torch.randperm(S * pages, device=C.DEV, generator=g).int().view(S, pages)
+    cache.pages.fill_(pages), cache.refs.fill_(1)
+    return cache
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [0, 2 ** 19 + 3])
+def test_a_row_map_of_more_rows_than_threads(gpu, T):
+    """A launch has 2^20 threads at most: rows go on behind them."""
+    S, page, n = 3, 128, [2 ** 19 + 1, 7, 2 ** 19 - 5]
+    C.say(f"kv_row_map T={T} n={n}")
+    cache = long_table(-(-(max(n) + 50) // page), page, S)
+    cache.len.copy_(P.i32([0, 40, 9]))
+    R = S * T if T else sum(n) + 300
+    rows = svg.RowMap.empty(cache, R)
+    svg.kv_row_map(cache, P.i32(n), rows, T=T)
+    assert R > 2 ** 20
+    first = [s * T for s in range(S)] if T else list(np.cumsum([0] + n[:-1]))
+    table, lens = C.host(cache.table).astype(np.int64), C.host(cache.len)
+    slot, pos, place = (np.full(R, -1, np.int64) for _ in range(3))
+    for s in range(S):
+        at = slice(first[s], first[s] + n[s])
+        p = lens[s] + np.arange(n[s])
+        slot[at], pos[at], place[at] = s, p, table[s, p // page] * page + p % page
+    for name, want in (("start", first), ("count", n), ("slot", slot), ("pos", pos), ("place", place)):
+        assert np.array_equal(C.host(getattr(rows, name)), want), name
+
+
+@pytest.mark.gpu
+def test_a_rotation_of_more_rows_than_one_turn(gpu):
+    """Workgroups take 2^21 rows at a time: as many again, and the rest, are the same as in calls of their own."""
+    R, half, page = 2 ** 21 + 40, 2 ** 20 + 32, 32
+    C.say(f"rope_append n_rows={R}")
+    cache, other = (long_table(-(-R // page), page, 1) for _ in range(2))
+    g = torch.Generator(device=C.DEV).manual_seed(5)
+    k, v = (torch.randn((R, 64), device=C.DEV, generator=g).half() for _ in range(2))
+    rope = svg.Rope.make(64, device=C.DEV)
+    rows = svg.RowMap.empty(cache, R)
+    svg.kv_row_map(cache, P.i32([R]), rows)
+    assert bool((rows.place >= 0).all())
+    svg.rope_append(cache, 0, rows, rope, None, k, v)
+    for at in (slice(0, half), slice(half, R)):
+        part = svg.RowMap(rows.start, rows.count, rows.pos[at], rows.place[at])
+        svg.rope_append(other, 0, part, rope, None, k[at], v[at])
+    assert torch.equal(cache.k, other.k) and torch.equal(cache.v, other.v)
+    last = int(rows.place[-1])
+    d = torch.arange(64)
+    assert torch.equal(cache.v[0, last // page, 0].cpu()[CO.value_at(last % page, d, 64)], v[-1].cpu())
+
+
+@pytest.mark.gpu
+def test_codes_of_more_rows_than_a_launch_has_in_x(gpu):
+    """Rows go on in the second dimension behind 2^20; the rows of whole slabs are those of a call of their own."""
+    M, Kd, half = 2 ** 20 + 37, 32, 2 ** 19
+    C.say(f"gated_quant_i8 M={M} K={Kd}")
+    g = torch.Generator(device=C.DEV).manual_seed(5)
+    x, gate = (torch.randn((M, Kd), device=C.DEV, generator=g).bfloat16() for _ in range(2))
+    signs = (torch.randint(0, 2, (Kd,), device=C.DEV, generator=g) * 2 - 1).to(torch.int8)
+
+    def call(x, gate):
+        q, s = torch.full(x.shape, 99, dtype=torch.int8, device=C.DEV), torch.full(x.shape[:1], 7.0, device=C.DEV)
+        svg.gated_quant_i8(x, gate, signs, q, s)
+        return q.view(-1), s
+
+    q, s = call(x, gate)
+    parts = [call(x[at], gate[at]) for at in (slice(0, half), slice(half, M))]
+    assert torch.equal(q, torch.cat([p[0] for p in parts])) and torch.equal(s, torch.cat([p[1] for p in parts]))
+    at = slice(2 ** 20 - 64, M)                      # from the last slabs of the first dimension on
+    codes, scales = PO.gated_quant(x[at].float().cpu().numpy(), gate[at].float().cpu().numpy(), C.host(signs), 32)
+    assert np.array_equal(C.host(s[at]), scales) and np.array_equal(C.host(q[(2 ** 20 - 64) * Kd:]), NO.slab_codes(codes))
+
+
 # ------------------------------------------------------------------ the sources
 def test_assembly_declares_the_registers_that_it_writes():
     """m0 holds where loads into LDS go: what writes it has to name it, or the compiler may keep a value of its own there."""
