@@ -166,9 +166,11 @@ class Rope:
         """freq[i] = base^(-2 i / rot), for contexts `factor` times the trained
         ones bent by `scaling`: "linear" (positions divided by factor), "base"
         (base times factor^(rot / (rot - 2)): the slowest pair as with "linear",
-        the fastest as it was) or "bands" (pairs that turn more than bounds[0]
-        times over the `trained` positions as they were, those that turn less than bounds[1] times divided
-        by factor, a ramp in the pair's index between them; amplitude 0.1 ln(factor) + 1 unless given)."""
+        the fastest as it was) or "bands" (YaRN's interpolation by parts: pairs that
+        turn more than bounds[0] times over the `trained` positions as they were,
+        those that turn less than bounds[1] times divided by factor, a ramp in the
+        pair's index between them; amplitude 0.1 ln(factor) + 1 unless given).  The ramp's ends are
+        whole numbers, rounded outward and kept to 0 and rot - 1, as models trained with it have them."""
         if rot < 2 or rot % 2:
             raise ValueError("rot must be even")
         if not factor > 0 or not base > 1:
@@ -187,7 +189,7 @@ class Rope:
             # the pair (a real number) that turns n times over the trained positions
             low, high = (rot * math.log(trained / (2 * math.pi * n)) / (2 * math.log(base)) for n in bounds)
             low, high = max(math.floor(low), 0), min(math.ceil(high), rot - 1)
-            ramp = ((torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 0.001)).clamp(0, 1)
+            ramp = ((torch.arange(rot // 2, dtype=torch.float64) - low) / max(high - low, 1)).clamp(0, 1)  # (one whole number: a step)
             freq = freq * (1 - ramp) + freq / factor * ramp
             if amplitude is None:
                 amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0

@@ -447,6 +447,31 @@ def test_codes_of_more_rows_than_a_launch_has_in_x(gpu):
     assert np.array_equal(C.host(s[at]), scales) and np.array_equal(C.host(q[(2 ** 20 - 64) * Kd:]), NO.slab_codes(codes))
 
 
+
+# ------------------------------------------------------------------ frequencies
+@pytest.mark.parametrize("rot,base,trained,bounds", [(64, 1e4, 4096, (32.0, 1.0)), (128, 5e5, 8192, (32.0, 1.0)), (128, 1e6, 32768, (8.0, 2.0)),
+                                                     (64, 1e4, 4096, (2.001, 2.0)), (16, 1e4, 100, (32.0, 1.0)), (64, 100.0, 10 ** 9, (32.0, 1.0))])
+def test_bands_of_frequencies(rot, base, trained, bounds):
+    """Pair by pair: x turns trained base^(-2 x / rot) / (2 pi) times, so n turns are at x = rot ln(trained / (2 pi n)) / (2 ln base); the
+    weight of the divided frequency goes from 0 to 1 between the whole numbers around the two; a step where they are one."""
+    import math
+
+    import speculative_verify_gemm_amd as lib
+
+    class Host:
+        def __init__(self, freq, interleaved=False, amplitude=1.0):
+            self.freq = freq
+
+    got = lib.Rope.make.__func__(Host, rot, base, scaling="bands", factor=4.0, trained=trained, bounds=bounds, device="cpu").freq
+    low, high = (rot * math.log(trained / (2 * math.pi * n)) / (2 * math.log(base)) for n in bounds)
+    low, high = max(math.floor(low), 0), min(math.ceil(high), rot - 1)
+    for i in range(rot // 2):
+        part = 0.0 if i <= low else 1.0 if i >= high else (i - low) / (high - low)
+        plain = base ** (-2 * i / rot)
+        want = plain * (1 - part) + plain / 4 * part
+        assert math.isclose(got[i], want, rel_tol=1e-13), i
+
+
 # ------------------------------------------------------------------ the sources
 def test_assembly_declares_the_registers_that_it_writes():
     """m0 holds where loads into LDS go: what writes it has to name it, or the compiler may keep a value of its own there."""
