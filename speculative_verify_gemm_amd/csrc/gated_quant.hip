@@ -5,10 +5,10 @@
 // fp64 here (its error there, below 2^-50, moves that rounding once in 2^25 values); the rotation and the codes are
 // those of svg_act.h.  One workgroup owns a row and holds it in registers.
 //
-// Bound by vector instructions, about 63 a value with a gate, of which the gate is half and the rotation and the codes are the
+// Bound by vector instructions: about 63 a value with a gate, of which the gate is half and the rotation and the codes are the
 // rest (4099 rows of 12288, bf16 halves of one product: 109 to 115 us, 2.3 TB/s, vector units busy 91 %; a table of 128 powers of two, which
-// saves a third of the fp64 operations: 111 us); without a gate by memory (4099 rows of 4096, fp16: 18.6 us, 2.7 TB/s); few rows
-// by the chain of one load, a reduction and one store (40 rows of 4096: 4.1 us).
+// saves a third of the fp64 operations: 111 us), about 31 without one (4099 rows of 4096, fp16: 18.6 us, 2.7 TB/s, where a copy reaches
+// 4.7; the instructions alone are about 13 of them); few rows by the chain of one load, a reduction and one store (40 rows of 4096: 4.1 us).
 #include "../../include/svgemm_prompt.h"
 #include "svg_act.h"
 #include "svg_internal.h"

@@ -19,10 +19,16 @@
 // ahead of their products, and does not touch masks; the tiles of the rows' own tokens go one by one.  A running maximum is
 // raised only when a score passes it by 2^kSlack.
 //
+// Precision.  Scores, maxima, sums and accumulators are fp32.  The probabilities enter the second product rounded to the cache's type,
+// as the values are held in it, and their sum is that of the rounded ones: a second part of them would be half as many
+// products again.  Distance from the 64-bit result over the result's size (rms), here | all in fp32 but the output: bf16 2.0e-3 | 1.7e-3,
+// fp16 2.5e-4 | 2.1e-4.
+//
 // Bound by the matrix units and the vector instructions of the exponential together.  1000 rows behind 30001 tokens, 8 heads of 128
-// for 32, bf16: 495 us, 1.01 PFLOP/s (a library product of 8192^3: 1.46), matrix units and vector units each busy 47 % of the
-// cycles; heads of 256 0.94 PFLOP/s; heads of 64 0.79, where the exponentials weigh twice as much.  Shorter items pay for their
-// starts, the rows' own tokens and the partials: a prompt of 4099 tokens, 32 heads of 128: 200 us, 0.69 PFLOP/s, 15 of them the join.
+// for 32, bf16: 500 us, 1.0 PFLOP/s (a library product of 8192^3: 1.46), matrix units and vector units each busy 47 % of the
+// cycles (in how many neither is has not been counted); heads of 256 1.05 PFLOP/s; heads of 64 0.80, where the exponentials weigh
+// twice as much.  Shorter items pay for their starts, the rows' own tokens and the partials: a prompt of 4099 tokens, 32 heads of 128:
+// 200 us, 0.69 PFLOP/s, 15 of them the join.
 // Heads of 256 have 16 rows a wave: 32 rows fill the registers with one wave a SIMD and take as long (step 148 | 144 us).
 #include <math.h>
 

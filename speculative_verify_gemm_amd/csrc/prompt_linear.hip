@@ -5,19 +5,28 @@
 //
 // Four ways, one rule between them (launch_best):
 //  big   256 x 256 outputs, one workgroup of 8 waves a compute unit (W8): a step of 64 values of K brings 32 KiB for 2 x 256 x
-//        256 x 64 operations, so that loads, LDS reads and products each take about the same time.  8192^3: 2468 TOP/s.
+//        256 x 64 operations, so that loads, LDS reads and products each take about the same time.  8192^3: 425 us, 2580 TOP/s.
 //  mid   128 x 128 outputs, two workgroups a compute unit: for fewer tiles, and for 4-bit weights.
 //  small 64 x 64 outputs, four workgroups a compute unit: for fewer tiles than compute units.
 //  few   16 columns and up to 128 rows, 8 waves that share K and add their sums up in LDS: bound by the weights' bytes.
 // big, mid and small go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
-// loads behind it, and neither the ring nor the products stop between tiles.  Stores are counted too, so they are not waited for.
+// loads behind it, and neither the ring nor the products stop between tiles.  W8's stores, four values each, are counted too, so
+// that whole tiles' are not waited for; W4's lane has one value of a row, so that it stores four times as often as is counted and the next
+// tile's first step waits for most of them, as it does for all of a tile's that are stored value by value.
 //
-// What bounds them.  W8 at 4099 x 24576 x 4096: 380 us a call, 17 of them in few for the last 3 rows (a library product of 4096 rows:
-// 367); the loads alone and the products alone each take about nine tenths of it, matrix units busy 52 %.  W4 at 1001 x 4096 x
-// 12288: 108 us, 0.94 POP/s, bound by vector instructions (busy 64 %, matrix units 17 %): two for each result of a product and
-// group (the conversion and the fused product-sum) and 45 a step to unpack a fragment; without the sums 97 us, without the
-// unpacking 107, without loads 100.  Converting by adding 1.5 * 2^23 in the matrix unit instead takes as many instructions and the
-// same time.
+// What bounds them.  W8 at 4099 x 24576 x 4096: 380 us a call, 17 of them in few for the last 3 rows (4096 rows: 369, a library product
+// 367); the loads alone and the products alone each take about nine tenths of it, matrix units busy 52 %.  W8 at 512 x 4096 x 4096: 18 us
+// of 6.9 that its operations take at the library's rate: 64 steps of 64 values, each 0.27 us of wait, barrier and the chain through LDS
+// whatever the work.  W4 at 1001 x 4096 x 12288: 108 us, 0.94 POP/s: the chain within a wave (read, unpack, product, conversion, sum,
+// barrier), since 256 tiles leave a compute unit one workgroup and a SIMD two waves.  No part of it alone is the bound: vector units are busy
+// 64 %, matrix units 17 %; without the sums, three quarters of the vector instructions, it takes 97 us, without the unpacking (45
+// instructions a step) 107, without loads 100.  Converting by adding 1.5 * 2^23 in the matrix unit instead takes as many instructions
+// and the same time.
+//
+// Registers.  few with eight row tiles (97 rows and more) spills where weights have 4 bits: vector registers | bytes of scratch a lane
+// 40 | 148 for groups of 32 with fp16 zeros, 20 | 84 with 4-bit ones, 9 | 40 for 64 with fp16 zeros, 3 to 4 | 16 to 20 for 128; small 3 | 12 for
+// groups of 32 with fp16 zeros; big has 20 bytes of scratch for scalar registers.  The waits by counts allow for it: what a spill adds
+// behind a load only makes them stricter.
 #include <limits.h>
 
 #include <type_traits>
@@ -285,8 +294,8 @@ __global__ __launch_bounds__(64 * WM * WN, WGS * WM * WN / 4) void k_prompt_line
   constexpr int XI = MF / 4, WI = F::k4 ? 0 : NF / 4;                 // 64 row scales, 64 column scales a load
   static_assert(FRAGS % WAVES == 0 && PARAMS <= WAVES && MF % 4 == 0 && NF % 4 == 0 && XI + WI <= WAVES, "loads of a wave");
   static_assert(TM % F::kRing == 0, "the places of the activations' fragments are the same in every step");
-  constexpr int LOADS = FRAGS / WAVES, STORES = TM * TN;
-  static_assert(STORES + LOADS < 64, "what the counter of loads holds");
+  constexpr int LOADS = FRAGS / WAVES, STORES = TM * TN;              // (STORES: at least so many for each wave's part of a whole tile)
+  static_assert(STORES + LOADS < 64, "the largest count that is waited for");
   __shared__ __attribute__((aligned(1024))) char lds[STAGES * STAGE + (XI + WI) * 256];
   char* const scales = lds + STAGES * STAGE;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
@@ -630,7 +639,9 @@ hipError_t launch_few(const Args& a, hipStream_t stream) {
 //        small | mid  512 x 4096 x 4096: 26.5 | 39    1024 x 4096 x 4096: 41 | 40          4096 x 24576 x 4096: 932 | 729
 //                     512 x 4096 x 4096 in groups of 32: 38 | 60, of 128: 24 | 34
 enum { kNone = -1, kFew, kSmall, kMid, kBig };
-constexpr long kMaxGridY = 65535;  // a launch has no more workgroups in y
+// A launch has no more workgroups in y.  (In x it has fewer than 2^32 threads, 2^27 columns of few: so wide a product always costs less
+// in small, where a workgroup takes tile after tile.)
+constexpr long kMaxGridY = 65535;
 // A step's cost: few, in a round of one workgroup a compute unit, for a workgroup and each 16 of its rows (1 / 10000 us); small
 // and mid, for 1, 2, .. workgroups on a compute unit.
 struct Cost {
