@@ -212,6 +212,8 @@ svg_status kv_copy_pages(const svg_kv_cache* cache, const int32_t* src, const in
  *  +infinity, and may where it is -infinity, which by the definition only leaves the token out (the parts of q decide);
  *  a value that is not finite makes its own element of the row NaN or infinite (unless the token's p is small enough to
  *  be lost, see above), and no other.
+ *  Of a bf16 cache the accumulators hold up to 2^15 times a value, added up over the tokens: an element is not finite either where
+ *  that passes fp32's largest number, which takes values of 2^113 and more (2^103 for 1024 tokens of like weight).
  *  NaN rows: a node whose root path breaks the rule above, or meets a node in a page that other slots hold too (which
  *  kv_append has passed over); a row that reads a page number outside the cache; all of a slot whose pages do not cover
  *  len + n_nodes.
