@@ -164,6 +164,125 @@ def test_values_of_any_size_in_a_bf16_cache(gpu, exponent, dim):
         assert np.all(np.abs(got - ref) <= tol), float((np.abs(got - ref) / tol).max())
 
 
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite(gpu, value, kind):
+    """A row whose query is not finite is NaN; every other row is, bit for bit, what it is without that."""
+    rng = np.random.default_rng(3)
+    lens, n = [200, 7], [30, 20]
+    c = K.make(3, lens, max(n), H=2, dim=64, page=32)
+    P.fill(c, rng, kind)
+    start, count = P.packed(n)
+    q = rng.standard_normal((sum(n), 6, 64))
+    clean, _ = attend(c, kind, q, start, count, 0.125)
+    at = [(0, 0), (7, 3), (29, 5), (33, 1)]
+    for r, a in at:
+        q[r, a, 11] = value
+    got, _ = attend(c, kind, q, start, count, 0.125)
+    for r, a in at:
+        assert np.isnan(got[r, a]).all() or np.isinf(value)      # (an infinite one may leave tokens out: their scores are -infinity)
+        got[r, a] = clean[r, a]
+    assert np.array_equal(got, clean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_tokens_that_are_left_out(gpu, kind):
+    """Keys that give scores of -infinity: the first 150 of 400 for every row, then all that some rows see (NaN)."""
+    rng = np.random.default_rng(5)
+    lens, n = [400, 0], [40, 37]
+    c = K.make(3, lens, max(n), H=1, dim=64, page=32)
+    P.fill(c, rng, kind)
+    keys, _v = tokens(c, kind, 0, 440)
+    keys[:150, 9] = -np.inf
+    put(c, kind, "k", 0, keys)
+    keys, _v = tokens(c, kind, 1, 37)
+    keys[:20, 9] = -np.inf
+    put(c, kind, "k", 1, keys)
+    q = rng.standard_normal((77, 2, 64))
+    q[..., 9] = 1.0
+    start, count = P.packed(n)
+    got, q64 = attend(c, kind, q, start, count, 0.125)
+    for s, first in ((0, 150), (1, 20)):
+        keys, v = tokens(c, kind, s, lens[s] + n[s])
+        for i in range(n[s]):
+            L = lens[s] + i + 1
+            for a in range(2):
+                y = got[start[s] + i, a]
+                if L <= first:
+                    assert np.isnan(y).all(), (s, i, a)
+                    continue
+                x = q64[start[s] + i, a]
+                w = np.exp(0.125 * (keys[first:L] @ x))
+                w /= w.sum()
+                size = np.array([0.125 * (np.abs(keys[first:L]) @ np.abs(x)).max(), np.abs(v[:L]).max(), (w @ np.abs(v[first:L])).max()])
+                ref = w @ v[first:L]
+                assert np.all(np.abs(y - ref) <= P.attention_bound(c, kind, ref, size, L)), (s, i, a)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_pages_past_32_bits(gpu, kind):
+    """A pool of 8 GiB of keys and as many of values: what its last pages give is what the same pages of a small pool give."""
+    H, dim, page, ctx, n, many = 8, 128, 128, 500, 300, 2 ** 15 + 3
+    C.say(f"rope_append, prompt_attention: {many} pages of {H * page * dim * 2} bytes {kind}")
+    held = -(-(ctx + n) // page)
+    rng = np.random.default_rng(3)
+    ids = [many - 1, 5, 2 ** 14 + 1, many - 2, 2 ** 14, many - 9, 2 ** 13 + 1][:held]
+    x = torch.from_numpy(rng.standard_normal((n, 3 * H, dim)).astype(np.float32)).to(P.TYPES[kind]).to(C.DEV)
+    old = torch.from_numpy(rng.standard_normal((2, held, H, page * dim)).astype(np.float32)).to(P.TYPES[kind]).to(C.DEV)
+    rope, got = svg.Rope.make(dim, device=C.DEV), []
+    for pages, at in ((held, list(range(held))), (many, ids)):
+        cache = svg.KVCache.empty(1, pages, H, dim, page, 1, held, dtype=P.TYPES[kind], device=C.DEV)
+        where = torch.tensor(at, device=C.DEV)
+        cache.k[0, where], cache.v[0, where] = old[0], old[1]
+        cache.table.copy_(where[None]), cache.pages.fill_(held), cache.len.fill_(ctx)
+        cache.refs[where] = 1
+        rows = svg.RowMap.empty(cache, n)
+        svg.kv_row_map(cache, P.i32([n]), rows)
+        q, out = (torch.zeros((n, H, dim), dtype=P.TYPES[kind], device=C.DEV) for _ in range(2))
+        svg.rope_append(cache, 0, rows, rope, x[:, :H], x[:, H:2 * H], x[:, 2 * H:], q)
+        svg.prompt_attention(cache, 0, rows, q, out, svg.prompt_attention_workspace(cache, H, n))
+        got.append((cache.k[0, where], cache.v[0, where], q, out))
+        del cache
+    torch.cuda.empty_cache()
+    assert bool(torch.isfinite(got[0][3].float()).all())
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_rows_that_lie_gigabytes_apart(gpu):
+    """Row strides of 2^30 bytes: a call's rows are those of a compact copy."""
+    M, ld, H, dim = 5, 2 ** 29 + 64, 1, 64
+    C.say(f"strides of {2 * ld} bytes")
+    wide = torch.empty(M * ld, dtype=torch.float16, device=C.DEV).view(M, ld)
+    part = wide[:, 8:8 + 6 * dim]
+    part.copy_(torch.randn((M, 6 * dim), device=C.DEV))
+    assert part.stride(0) == ld
+    signs = (torch.randint(0, 2, (2 * dim,), device=C.DEV) * 2 - 1).to(torch.int8)
+    c = K.make(3, [40], M, H=H, dim=dim, page=32)
+    P.fill(c, np.random.default_rng(1), "fp16")
+    rope, got = svg.Rope.make(dim, device=C.DEV), []
+    for x in (part, part.contiguous()):
+        cache = K.to_library(svg, c)
+        rows = svg.RowMap.empty(cache, M)
+        svg.kv_row_map(cache, P.i32([M]), rows)
+        q, k, v = x[:, :4 * dim].unflatten(1, (4, dim)), x[:, 4 * dim:5 * dim], x[:, 5 * dim:]
+        turned, out = (torch.zeros((M, 4, dim), dtype=torch.float16, device=C.DEV) for _ in range(2))
+        svg.rope_append(cache, 0, rows, rope, q, k, v, turned)
+        svg.prompt_attention(cache, 0, rows, q, out, svg.prompt_attention_workspace(cache, 4, M))
+        codes, scale = torch.zeros((M, 2 * dim), dtype=torch.int8, device=C.DEV), torch.zeros(M, device=C.DEV)
+        svg.gated_quant_i8(x[:, :2 * dim], x[:, 2 * dim:4 * dim], signs, codes, scale)
+        got.append((turned, out, codes, scale, cache.k, cache.v))
+    del wide, part
+    torch.cuda.empty_cache()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ linears
 FEW, SMALL, MID, BIG = range(4)
 ROWS, COLS = {FEW: 100, SMALL: 300, MID: 1001, BIG: 1150}, {FEW: 515, SMALL: 4091, MID: 4091, BIG: 8187}
@@ -252,6 +371,39 @@ def test_every_kernel_of_the_linears(gpu, fmt, group, ways, M, N, K, y):
     assert bool(((out.double() - ref).abs() <= tol * (1 + 1e-6)).all()), float(((out.double() - ref).abs() / tol).max())
     assert bool((buf[:guard] == 7).all()) and bool((buf[-guard:] == 7).all())
 
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,group,M,N,K", [("w8", 0, 100, 512, 96), ("w8", 0, 320, 4096, 320), ("w8", 0, 1024, 4096, 320), ("w8", 0, 1280, 12288, 96),
+                                             ("w4_z16", 32, 100, 512, 160), ("w4_z16", 64, 320, 4096, 192), ("w4_z4", 64, 1024, 4096, 192),
+                                             ("w4_z4", 128, 1024, 4096, 128), ("w4_z16", 32, 1024, 4096, 416), ("w4_z4", 32, 100, 512, 96)])
+def test_the_least_alignment(gpu, fmt, group, M, N, K):
+    """y, scales and zeros at 4 bytes, not 8 or 16: the results of aligned ones, bit for bit."""
+    C.say(f"prompt linear {fmt} group={group} M={M} N={N} K={K}, 4-byte alignment")
+    rng = np.random.default_rng(M + K)
+    wq, ws, wz, _s, _w = P.weights(rng, N, K, fmt, group)
+    xq = C.to_dev(NO.slab_codes(P.codes(rng, M, K)).reshape(M, K))
+    xs = torch.rand(M, device=C.DEV) * 1e-2 + 1e-4
+
+    def moved(t):
+        if t is None:
+            return None
+        step = 4 // t.element_size()
+        b = torch.zeros(t.numel() + 2 * step, dtype=t.dtype, device=C.DEV)[step:step + t.numel()].view(t.shape)
+        b.copy_(t)
+        assert b.data_ptr() % 8 == 4
+        return b
+
+    for y in ("fp32", "bf16"):
+        got = []
+        for at in (lambda t: t, moved):
+            out = at(torch.full((M, N), 7.0, dtype=P.TYPES[y], device=C.DEV))
+            if fmt == "w8":
+                svg.w8a8_prompt_linear(xq, at(xs), wq, at(ws), N, out)
+            else:
+                svg.w4a8_prompt_linear(xq, at(xs), wq, at(ws), at(wz), fmt, group, N, out)
+            got.append(out)
+        assert torch.equal(*got) and not bool((got[0] == 7).all())
 
 
 @pytest.mark.parametrize("N", [2 ** 30 + 1, 2 ** 31 - 16, 2 ** 31 - 1])
