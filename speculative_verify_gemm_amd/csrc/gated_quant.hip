@@ -7,7 +7,7 @@
 //
 // Bound by vector instructions: about 63 a value with a gate, of which the gate is half and the rotation and the codes are the
 // rest (4099 rows of 12288, bf16 halves of one product: 109 to 115 us, 2.3 TB/s, vector units busy 91 %; a table of 128 powers of two, which
-// saves a third of the fp64 operations: 111 us), about 31 without one (4099 rows of 4096, fp16: 18.6 us, 2.7 TB/s, where a copy reaches
+// saves a third of the fp64 operations: 111 us), about 31 without one (4099 rows of 4096, fp16: 19 us, 2.6 TB/s, where a copy reaches
 // 4.7; the instructions alone are about 13 of them); few rows by the chain of one load, a reduction and one store (40 rows of 4096: 4.1 us).
 #include "../../include/svgemm_prompt.h"
 #include "svg_act.h"

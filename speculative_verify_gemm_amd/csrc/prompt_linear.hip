@@ -3,7 +3,7 @@
 //   W8: y[m][n] = sx[m] s[n] S[m][n],  W4: y[m][n] = sx[m] sum_g s[n][g] S_g[m][n],
 // S an int32 sum of products of codes (exact: at most 127^2 K, 127 * 15 * group), from v_mfma_i32_16x16x64_i8; the rest fp32.
 //
-// Four ways, one rule between them (launch_best):
+// Four ways, one rule between them (choose):
 //  big   256 x 256 outputs, one workgroup of 8 waves a compute unit (W8): a step of 64 values of K brings 32 KiB for 2 x 256 x
 //        256 x 64 operations, so that loads, LDS reads and products each take about the same time.  8192^3: 425 us, 2580 TOP/s.
 //  mid   128 x 128 outputs, two workgroups a compute unit: for fewer tiles, and for 4-bit weights.
@@ -12,7 +12,7 @@
 // big, mid and small go from tile to tile (k_prompt_linear): loads go straight into a ring in LDS, a stage is waited for by the count of
 // loads behind it, and neither the ring nor the products stop between tiles.  W8's stores, four values each, are counted too, so
 // that whole tiles' are not waited for; W4's lane has one value of a row, so that it stores four times as often as is counted and the next
-// tile's first step waits for most of them, as it does for all of a tile's that are stored value by value.
+// tile's first step waits for most of them.  A tile that is not whole, or whose rows of y cannot take four values at once, waits for all.
 //
 // What bounds them.  W8 at 4099 x 24576 x 4096: 380 us a call, 17 of them in few for the last 3 rows (4096 rows: 369, a library product
 // 367); the loads alone and the products alone each take about nine tenths of it, matrix units busy 52 %.  W8 at 512 x 4096 x 4096: 18 us
