@@ -25,7 +25,7 @@
 // fp16 2.5e-4 | 2.1e-4.
 //
 // Bound by the matrix units and the vector instructions of the exponential together.  1000 rows behind 30001 tokens, 8 heads of 128
-// for 32, bf16: 500 us, 1.0 PFLOP/s (a library product of 8192^3: 1.46), matrix units and vector units each busy 47 % of the
+// for 32, bf16: 500 us, 1.0 PFLOP/s (a library product of 8192^3: 1.46), matrix units and vector units each busy 46 to 47 % of the
 // cycles (in how many neither is has not been counted); heads of 256 1.05 PFLOP/s; heads of 64 0.80, where the exponentials weigh
 // twice as much.  Shorter items pay for their starts, the rows' own tokens and the partials: a prompt of 4099 tokens, 32 heads of 128:
 // 200 us, 0.69 PFLOP/s, 15 of them the join.
@@ -87,12 +87,13 @@ template <bool BF>
 constexpr float kTop = BF ? -26.f : 15.f;
 template <bool BF>
 constexpr float kLift = kTop<BF> - kSlack;
-// A probability is 2^(f s + bias), bias = kLift - m: one operation, and one rounding, since m is a whole number of 1 / kGrid up to
-// kFar.  Beyond, the product inside that operation and the rounded one that m came from would differ by 2^-11 and more (from 2^24 on by
-// whole numbers, and kLift - m loses kLift), which fp16 has no room for: there it is 2^((f s - m) + kLift) with each step rounded, 2^kLift
-// where s is the maximum, whatever its size.  Such rows cost the others a branch in the step that raises maxima (a prompt of 4099
-// tokens 198 -> 201 us, 1000 rows behind 30001 495 -> 499; a clamp of every probability costs the second 4 %).
-constexpr float kFar = 16384.f, kGrid = 256.f;
+// A probability is 2^(f s + bias), bias = kLift - m: one operation.  What rounds kLift - m is the same for all of a row's
+// probabilities since then, and goes out with their sum; the largest is a power of two and loses nothing to 16 bits.  Beyond kFar the product
+// inside that operation and the rounded one that m came from would differ by 2^-11 and more (from 2^24 on by whole numbers, and kLift - m
+// loses kLift), which fp16 has no room for: there it is 2^((f s - m) + kLift) with each step rounded, 2^kLift where s is the maximum,
+// whatever its size.  Such rows cost the others a branch in the step that raises maxima (a prompt of 4099 tokens 201 -> 204 us, 1000
+// rows behind 30001 504 either way; a clamp of every probability costs those 4 %).
+constexpr float kFar = 16384.f;
 
 // What the second launch has to know of an item that begins in a workgroup's share and does not end there.
 struct Join {
@@ -105,7 +106,7 @@ struct Args {
   const uint16_t* q;
   uint16_t* out;
   const int32_t *start, *count;
-  float* stats;   // [groups][2][kTile] (minus the maximum, sum): infinite where no token was seen
+  float* stats;   // [groups][2][kTile] (kLift less the maximum, sum): infinite where no token was seen
   float* parts;   // [groups][2][kTile][dim]
   Join* joins;    // [groups + 1]: the last one's `last` is the number of workgroups that took part
   long ld_q;
@@ -282,6 +283,8 @@ struct Kernel {
     float bias;      // what is added to the exponents: kLift - m; kLift beyond kFar, where m is kept in LDS (`far`)
     SVG_DEV bool beyond() const { return limit == -INFINITY && bias != 0.f; }
     SVG_DEV float m(const float* far) const { return limit != -INFINITY ? limit - kSlack : (bias != 0.f ? *far : -INFINITY); }
+    // kLift less the maximum that o and l are relative to
+    SVG_DEV float offset(const float* far) const { return limit != -INFINITY ? bias : (bias != 0.f ? kLift<BF> - *far : INFINITY); }
   };
 
   // The pages of a slot's table row, 64 entries at a time: entry base + l in lane l (reading them one by one would wait for
@@ -491,14 +494,20 @@ struct Kernel {
       auto raise = [&](Row& r, float top, float* far) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float before = r.m(far);
+        float before = r.limit - kSlack;
+        if (__builtin_expect(__any(r.beyond()), false)) before = r.m(far);
         if (top - before > kSlack) {
           const bool beyond = fabsf(top) > kFar;
-          const float m = beyond ? top : floorf(top * kGrid) * (1.f / kGrid);
-          const float by = before == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(before - m);
-          r.limit = beyond ? -INFINITY : m + kSlack;
-          r.bias = beyond ? kLift<BF> : kLift<BF> - m;
-          if (beyond) *far = m;
+          float bias = kLift<BF> - top, by = __builtin_amdgcn_exp2f(bias - r.bias), limit = top + kSlack;
+          if (__builtin_expect(__any(beyond || r.beyond()), false)) {
+            by = beyond || r.beyond() ? __builtin_amdgcn_exp2f(before - top) : by;
+            limit = beyond ? -INFINITY : limit;
+            bias = beyond ? kLift<BF> : bias;
+            if (beyond) *far = top;
+          }
+          by = before == -INFINITY ? 0.f : by;
+          r.limit = limit;
+          r.bias = bias;
 #pragma unroll
           for (int d = 0; d < ND; ++d) r.o[d] *= by;
           r.l *= by;
@@ -712,7 +721,7 @@ struct Kernel {
           for (int d = 0; d < ND; ++d)
             *reinterpret_cast<float4*>(to + 16 * d) = make_float4(w.o[d][0], w.o[d][1], w.o[d][2], w.o[d][3]);
           if (quad == 0) {
-            a.stats[at_part * 2] = -w.m(far + 64 * rt);
+            a.stats[at_part * 2] = w.offset(far + 64 * rt);
             a.stats[at_part * 2 + 1] = valid ? w.l[0] : __builtin_nanf("");
           }
         }
@@ -743,7 +752,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_prompt_attention_join(Args 
   for (int u = threadIdx.x; u < kJoinRows * (D / 4); u += 64 * kJoinWaves) {
     const int r = blockIdx.y * kJoinRows + u / (D / 4), d = 4 * (u % (D / 4));
     if (r >= j.rows) continue;
-    // the weights go by the largest maximum so far, held as minus that; two partials on their way at once
+    // the weights go by the smallest offset (the largest maximum) so far; two partials on their way at once
     float low = INFINITY, sum = 0.f;
     f32x4 o{};
     for (u32 w = wg; w <= j.last; w += 2) {
